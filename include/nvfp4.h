@@ -62,7 +62,8 @@ typedef enum {
     NVFP4_OP_CALIB_F32 = 3,  /* m, n, k ignored */
     NVFP4_OP_LINEAR_DYNAMIC = 4, /* m = M, n = N, k = K of nvfp4_linear_dynamic */
     NVFP4_OP_QUANTIZE_E4M3 = 5,  /* nvfp4_quantize_e4m3 (m, n, k ignored) */
-    NVFP4_OP_LINEAR_LOWRANK = 6  /* nvfp4_linear_lowrank: m = M, n = rank (k ignored) */
+    NVFP4_OP_LINEAR_LOWRANK = 6, /* nvfp4_linear_lowrank: m = M, n = rank (k ignored) */
+    NVFP4_OP_LINEAR_DYNAMIC_MXFP4 = 7 /* nvfp4_linear_dynamic_mxfp4: m = M, n = N, k = K */
 } nvfp4_op;
 
 /* Human-readable name of a status. Never NULL. */
@@ -348,6 +349,77 @@ nvfp4_status nvfp4_quantize_e4m3(const void *x, nvfp4_dtype dt, int64_t rows, in
 nvfp4_status nvfp4_linear_e4m3(const uint8_t *a, const float *a_scale, const uint8_t *w,
                                const float *w_scale, int64_t M, int64_t N, int64_t K,
                                nvfp4_dtype out_dt, void *y, cudaStream_t stream);
+
+/*
+ * MXFP4 (the OCP Microscaling Formats specification's FP4 format): E2M1 codes packed as above and
+ * one power-of-two scale per block of 32 values along a row, stored as an E8M0 byte b:
+ *   value = E2M1(code) x 2^(b - 127);  b = 255 is NaN (the whole block is NaN).
+ * No tensor-wide scale. cols must be a multiple of 32.
+ *   codes      : rows x cols/2 bytes, row-major;
+ *   scales_lin : rows x cols/32 bytes, row-major;
+ *   scales_swz : nvfp4_mxfp4_scales_bytes(rows, cols, 1) bytes, the tensor-core operand layout:
+ *                the atoms of nvfp4.h's NVFP4 layout (128 rows x 4 blocks, 512 bytes) over the
+ *                [rows x cols/32] scale matrix. Padding rows / blocks are zero.
+ */
+
+/* Bytes of the scales of a rows x cols MXFP4 matrix: linear (swizzled = 0) or swizzled (1). */
+size_t nvfp4_mxfp4_scales_bytes(int64_t rows, int64_t cols, int swizzled);
+
+/* Block scale of nvfp4_quantize_mxfp4, from the block's largest magnitude m. */
+typedef enum {
+    NVFP4_MX_SCALE_FLOOR = 0, /* 2^(floor(log2 m) - 2): the specification's; values whose
+                                 quotient is above 6 saturate */
+    NVFP4_MX_SCALE_CEIL = 1   /* the smallest 2^s with m <= 6 * 2^s: nothing saturates */
+} nvfp4_mx_scale_rule;
+
+/*
+ * Quantize x [rows x cols] (fp32 or bf16, row-major) to MXFP4 along its rows, its columns, or both
+ * in one read of x. The scale is that of scale_rule, at least 2^-127 (b = 0: also a block of
+ * zeros); code = E2M1(x / scale), the exact quotient rounded to nearest even, saturating at 6,
+ * sign kept. A block that holds a NaN or an infinity gets b = 255 and zero codes.
+ * Along the rows: codes, scales_swz and / or scales_lin. Along the columns: codes_t, ... hold
+ * x^T as a matrix of cols rows and ceil(rows/32)*32 columns (x's rows, padded with zeros to whole
+ * blocks), so that both operands of a product summed over x's rows have the same length. codes or
+ * codes_t may be NULL (not both), with their scales; a set that is written needs one scale array.
+ * All arrays 16-byte aligned. No workspace.
+ */
+nvfp4_status nvfp4_quantize_mxfp4(const void *x, nvfp4_dtype dt, int64_t rows, int64_t cols,
+                                  int scale_rule, uint8_t *codes, uint8_t *scales_swz,
+                                  uint8_t *scales_lin, uint8_t *codes_t, uint8_t *scales_swz_t,
+                                  uint8_t *scales_lin_t, cudaStream_t stream);
+
+/*
+ * MXFP4 -> fp32 or bf16: out = E2M1(code) * 2^(b - 127) as one fp32 product (exact unless it
+ * overflows), bf16 rounded to nearest even. Reads linear scales. No workspace.
+ */
+nvfp4_status nvfp4_dequantize_mxfp4(const uint8_t *codes, const uint8_t *scales_lin, int64_t rows,
+                                    int64_t cols, nvfp4_dtype out_dt, void *out,
+                                    cudaStream_t stream);
+
+/*
+ * Block-scaled linear layer on MXFP4 operands, Y = dequant(A) . dequant(W)^T, A: M x K,
+ * W: N x K, accumulated in fp32 by the FP4 tensor cores and stored as out_dt (bf16 rounded to
+ * nearest even). With the column form of nvfp4_quantize_mxfp4 the same call gives a layer's
+ * gradients: of y = x . w^T, dx = linear(q(dy), q(w^T)) and dw = linear(q(dy^T), q(x^T)).
+ * flags: nvfp4_linear_flags, as in nvfp4_linear_ex. ws: nvfp4_workspace_bytes(NVFP4_OP_LINEAR, M,
+ * N, K) bytes. Products of scales beyond the fp32 range overflow to infinity or vanish.
+ */
+nvfp4_status nvfp4_linear_mxfp4(const uint8_t *a_codes, const uint8_t *a_scales_swz,
+                                const uint8_t *w_codes, const uint8_t *w_scales_swz, int64_t M,
+                                int64_t N, int64_t K, nvfp4_dtype out_dt, void *y, void *ws,
+                                size_t ws_bytes, uint32_t flags, cudaStream_t stream);
+
+/*
+ * nvfp4_linear_mxfp4 on unquantized activations x (M x K, fp32 or bf16): A is exactly what
+ * nvfp4_quantize_mxfp4(x, NVFP4_MX_SCALE_FLOOR) gives. For M <= 16 one kernel does both where the
+ * shape fits it (each CTA encodes its range of K); other shapes run the two calls with the
+ * quantized activations in ws: nvfp4_workspace_bytes(NVFP4_OP_LINEAR_DYNAMIC_MXFP4, M, N, K)
+ * bytes (0 for the fused case).
+ */
+nvfp4_status nvfp4_linear_dynamic_mxfp4(const void *x, nvfp4_dtype x_dt, const uint8_t *w_codes,
+                                        const uint8_t *w_scales_swz, int64_t M, int64_t N,
+                                        int64_t K, nvfp4_dtype out_dt, void *y, void *ws,
+                                        size_t ws_bytes, uint32_t flags, cudaStream_t stream);
 
 /*
  * Test of the failure-detection path. No counterpart in the paper. Launches one small kernel

@@ -12,6 +12,8 @@ device memory and the current stream, nothing else.
     e_w = quantize_e4m3(w_bf16)               # FP8 E4M3 tensorwise (embed / lm_head layers)
     y8 = linear_e4m3(quantize_e4m3(x_bf16), e_w)
     y_lr = linear_lowrank(q_x, q_w, x_bf16, down, up)  # FP4 + BF16 rank-r branch
+    m_x, m_xt = quantize_mxfp4(x_bf16, orient="both")  # MXFP4 along the rows and the columns
+    y_mx = linear_mxfp4(m_x, m_w)             # microscaled product, no global scale
 
 The C entry points are also available under their own names (``nvfp4_quantize`` ...).
 """
@@ -26,6 +28,8 @@ from ._lib import (NVFP4_BF16, NVFP4_F32, NVFP4_LINEAR_DEFAULT, NVFP4_LINEAR_RES
 
 __all__ = ["NVFP4Tensor", "quantize", "quantize_fp8", "quantize_batch", "dequantize", "linear",
            "linear_dynamic", "linear_nvfp4_out", "linear_lowrank", "E4M3Tensor", "quantize_e4m3", "linear_e4m3",
+           "MXFP4Tensor", "quantize_mxfp4", "dequantize_mxfp4", "linear_mxfp4",
+           "linear_dynamic_mxfp4",
            "calib_percentile_amax", "sync_status", "free_workspaces", "load", "NVFP4Error"]
 
 
@@ -360,6 +364,183 @@ def linear_e4m3(a: E4M3Tensor, w: E4M3Tensor, out_dtype=torch.bfloat16,
     st = load().nvfp4_linear_e4m3(_ptr(a.codes), _ptr(a.scale), _ptr(w.codes), _ptr(w.scale),
                                   M, N, K, dt, _ptr(out), _stream(dev))
     check(st, "nvfp4_linear_e4m3")
+    return out
+
+
+@dataclass
+class MXFP4Tensor:
+    """An MXFP4 [rows x cols] matrix: codes [rows, cols/2] u8, E8M0 scales (one per 32 values) in
+    the tensor-core layout (flat u8) and / or linear [rows, cols/32] u8."""
+    codes: torch.Tensor
+    scales_swz: torch.Tensor
+    scales_lin: torch.Tensor
+    rows: int
+    cols: int
+
+
+_MX_RULES = {"floor": _lib.NVFP4_MX_SCALE_FLOOR, "ceil": _lib.NVFP4_MX_SCALE_CEIL}
+_OUT_TYPES = {torch.float32: NVFP4_F32, torch.bfloat16: NVFP4_BF16}
+
+
+def _scratch(device, nbytes):
+    """A call's own workspace on the current stream (None if it needs none). It is not kept: a
+    captured graph holds its own in its memory pool, so two graphs never share one, and the
+    allocator hands an eager call's back to this stream only."""
+    return torch.empty(nbytes, dtype=torch.uint8, device=device) if nbytes else None
+
+
+def _on_device(dev):
+    """The library launches on the current device: make the tensors' device current."""
+    return torch.cuda.device(dev)
+
+
+def _check_arrays(what, device, **arrays):
+    """name=(tensor, dtype, shape): every tensor given lies contiguous on `device`, with that type
+    and shape (None: not checked); None tensors are skipped."""
+    for name, (t, dtype, shape) in arrays.items():
+        if t is None:
+            continue
+        if not isinstance(t, torch.Tensor) or not t.is_cuda or t.device != device:
+            raise ValueError(f"{what}: {name} must be a tensor on {device}")
+        if dtype is not None and t.dtype != dtype:
+            raise TypeError(f"{what}: {name} must be {dtype}")
+        if shape is not None and tuple(t.shape) != tuple(shape):
+            raise ValueError(f"{what}: {name} must have shape {tuple(shape)}")
+        if not t.is_contiguous():
+            raise ValueError(f"{what}: {name} must be contiguous")
+
+
+def _check_mx(what, q, device, swizzled=False, linear=False):
+    """An MXFP4Tensor's arrays on `device`, large enough for its size, with the scales the call
+    reads."""
+    if not isinstance(q, MXFP4Tensor):
+        raise TypeError(f"{what} expects MXFP4Tensor operands")
+    if q.cols % 32 or q.rows < 0 or q.cols < 0:
+        raise ValueError(f"{what}: cols must be a multiple of 32")
+    if (swizzled and q.scales_swz is None) or (linear and q.scales_lin is None):
+        raise ValueError(f"{what} needs the {'swizzled' if swizzled else 'linear'} scales")
+    _check_arrays(what, device, codes=(q.codes, torch.uint8, (q.rows, q.cols // 2)),
+                  scales_swz=(q.scales_swz, torch.uint8,
+                              (load().nvfp4_mxfp4_scales_bytes(q.rows, q.cols, 1),)),
+                  scales_lin=(q.scales_lin, torch.uint8, (q.rows, q.cols // 32)))
+
+
+def _mx_out(what, out, rows, cols, dtype, device):
+    if dtype not in _OUT_TYPES:
+        raise TypeError(f"{what}: out_dtype must be float32 or bfloat16")
+    if out is None:
+        return torch.empty((rows, cols), dtype=dtype, device=device)
+    _check_arrays(what, device, out=(out, dtype, (rows, cols)))
+    return out
+
+
+def _mx_alloc(rows, cols, device, swizzled, linear):
+    codes = torch.empty((rows, cols // 2), dtype=torch.uint8, device=device)
+    swz = (torch.empty(load().nvfp4_mxfp4_scales_bytes(rows, cols, 1), dtype=torch.uint8,
+                       device=device) if swizzled else None)
+    lin = torch.empty((rows, cols // 32), dtype=torch.uint8, device=device) if linear else None
+    return MXFP4Tensor(codes, swz, lin, rows, cols)
+
+
+def quantize_mxfp4(x: torch.Tensor, scale_rule: str = "floor", orient: str = "rows",
+                   swizzled=True, linear=False):
+    """MXFP4-quantize a 2-D fp32 / bf16 CUDA tensor (cols % 32 == 0): E2M1 codes with one
+    power-of-two scale per 32 values. scale_rule: "floor" (2^(floor(log2 max) - 2), large values
+    may saturate) or "ceil" (the smallest scale at which nothing saturates). orient: "rows" (blocks
+    along the rows, an MXFP4Tensor [rows, cols]), "cols" (the same of x^T, [cols, rows padded to a
+    multiple of 32 with zeros]) or "both" (the pair of them, x read once)."""
+    if not isinstance(x, torch.Tensor) or x.dtype not in _OUT_TYPES or x.dim() != 2 or \
+            not x.is_cuda:
+        raise TypeError("quantize_mxfp4 expects a 2-D CUDA fp32 or bf16 tensor")
+    if scale_rule not in _MX_RULES:
+        raise ValueError(f"scale_rule must be one of {sorted(_MX_RULES)}")
+    if orient not in ("rows", "cols", "both"):
+        raise ValueError("orient must be 'rows', 'cols' or 'both'")
+    if not swizzled and not linear:
+        raise ValueError("quantize_mxfp4 needs swizzled or linear scales")
+    x = x.contiguous()
+    rows, cols = x.shape
+    if cols % 32:
+        raise ValueError("quantize_mxfp4: cols must be a multiple of 32")
+    qr = _mx_alloc(rows, cols, x.device, swizzled, linear) if orient != "cols" else None
+    qc = _mx_alloc(cols, -(-rows // 32) * 32, x.device, swizzled, linear) \
+        if orient != "rows" else None
+    with _on_device(x.device):
+        ptrs = [_ptr(t) for q in (qr, qc)
+                for t in ((q.codes, q.scales_swz, q.scales_lin) if q else (None,) * 3)]
+        st = load().nvfp4_quantize_mxfp4(_ptr(x), _OUT_TYPES[x.dtype], rows, cols,
+                                         _MX_RULES[scale_rule], *ptrs, _stream(x.device))
+    check(st, "nvfp4_quantize_mxfp4")
+    return (qr, qc) if orient == "both" else qr or qc
+
+
+def dequantize_mxfp4(q: MXFP4Tensor, out_dtype=torch.float32,
+                     out: torch.Tensor = None) -> torch.Tensor:
+    """fp32 / bf16 values of q [rows, cols] (needs its linear scales)."""
+    if not isinstance(q, MXFP4Tensor):
+        raise TypeError("dequantize_mxfp4 expects an MXFP4Tensor")
+    dev = q.codes.device
+    _check_mx("dequantize_mxfp4", q, dev, linear=True)
+    out = _mx_out("dequantize_mxfp4", out, q.rows, q.cols, out_dtype, dev)
+    with _on_device(dev):
+        st = load().nvfp4_dequantize_mxfp4(_ptr(q.codes), _ptr(q.scales_lin), q.rows, q.cols,
+                                           _OUT_TYPES[out_dtype], _ptr(out), _stream(dev))
+    check(st, "nvfp4_dequantize_mxfp4")
+    return out
+
+
+def linear_mxfp4(a: MXFP4Tensor, w: MXFP4Tensor, out_dtype=torch.bfloat16,
+                 out: torch.Tensor = None, resident_weights: bool = False) -> torch.Tensor:
+    """Y = dequant(a) . dequant(w)^T, [a.rows x w.rows], from MXFP4 operands with fp32
+    accumulation. With x quantized "rows" and "cols", w and dy likewise, the gradients of
+    y = x . w^T are linear_mxfp4(dy_rows, w_cols) and linear_mxfp4(dy_cols, x_cols).
+    resident_weights: as in linear()."""
+    if not isinstance(a, MXFP4Tensor):
+        raise TypeError("linear_mxfp4 expects MXFP4Tensor operands")
+    dev = a.codes.device
+    _check_mx("linear_mxfp4", a, dev, swizzled=True)
+    _check_mx("linear_mxfp4", w, dev, swizzled=True)
+    if a.cols != w.cols:
+        raise ValueError("K mismatch")
+    M, N, K = a.rows, w.rows, a.cols
+    out = _mx_out("linear_mxfp4", out, M, N, out_dtype, dev)
+    flags = NVFP4_LINEAR_RESIDENT_WEIGHTS if resident_weights else NVFP4_LINEAR_DEFAULT
+    L = load()
+    with _on_device(dev):
+        ws_bytes = L.nvfp4_workspace_bytes(NVFP4_OP_LINEAR, M, N, K)
+        ws = _scratch(dev, ws_bytes)
+        st = L.nvfp4_linear_mxfp4(_ptr(a.codes), _ptr(a.scales_swz), _ptr(w.codes),
+                                  _ptr(w.scales_swz), M, N, K, _OUT_TYPES[out_dtype], _ptr(out),
+                                  _ptr(ws), ws_bytes, flags, _stream(dev))
+    check(st, "nvfp4_linear_mxfp4")
+    return out
+
+
+def linear_dynamic_mxfp4(x: torch.Tensor, w: MXFP4Tensor, out_dtype=torch.bfloat16,
+                         out: torch.Tensor = None,
+                         resident_weights: bool = False) -> torch.Tensor:
+    """Y = dequant(quantize_mxfp4(x)) . dequant(w)^T from fp32 / bf16 activations x [M x K]; one
+    fused kernel for M <= 16."""
+    if not isinstance(x, torch.Tensor) or x.dtype not in _OUT_TYPES or x.dim() != 2 or \
+            not x.is_cuda:
+        raise TypeError("linear_dynamic_mxfp4 expects a 2-D CUDA fp32 or bf16 tensor")
+    dev = x.device
+    _check_mx("linear_dynamic_mxfp4", w, dev, swizzled=True)
+    x = x.contiguous()
+    M, K = x.shape
+    if K != w.cols:
+        raise ValueError("K mismatch")
+    N = w.rows
+    out = _mx_out("linear_dynamic_mxfp4", out, M, N, out_dtype, dev)
+    flags = NVFP4_LINEAR_RESIDENT_WEIGHTS if resident_weights else NVFP4_LINEAR_DEFAULT
+    L = load()
+    with _on_device(dev):
+        ws_bytes = L.nvfp4_workspace_bytes(_lib.NVFP4_OP_LINEAR_DYNAMIC_MXFP4, M, N, K)
+        ws = _scratch(dev, ws_bytes)
+        st = L.nvfp4_linear_dynamic_mxfp4(_ptr(x), _OUT_TYPES[x.dtype], _ptr(w.codes),
+                                          _ptr(w.scales_swz), M, N, K, _OUT_TYPES[out_dtype],
+                                          _ptr(out), _ptr(ws), ws_bytes, flags, _stream(dev))
+    check(st, "nvfp4_linear_dynamic_mxfp4")
     return out
 
 

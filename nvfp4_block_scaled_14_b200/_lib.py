@@ -33,6 +33,9 @@ NVFP4_OP_CALIB_F32 = 3
 NVFP4_OP_LINEAR_DYNAMIC = 4
 NVFP4_OP_QUANTIZE_E4M3 = 5
 NVFP4_OP_LINEAR_LOWRANK = 6
+NVFP4_OP_LINEAR_DYNAMIC_MXFP4 = 7
+NVFP4_MX_SCALE_FLOOR = 0
+NVFP4_MX_SCALE_CEIL = 1
 NVFP4_ACT_IDENTITY = 0
 NVFP4_ACT_GELU_TANH = 1
 
@@ -85,6 +88,14 @@ _SIGNATURES = {
     "nvfp4_linear_lowrank": ([_vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _i64, _i64, _i64, _i64,
                               _vp, _vp, _sz, _vp], _int),
     "nvfp4_linear_e4m3": ([_vp, _vp, _vp, _vp, _i64, _i64, _i64, _int, _vp, _vp], _int),
+    "nvfp4_mxfp4_scales_bytes": ([_i64, _i64, _int], _sz),
+    "nvfp4_quantize_mxfp4": ([_vp, _int, _i64, _i64, _int, _vp, _vp, _vp, _vp, _vp, _vp, _vp],
+                             _int),
+    "nvfp4_dequantize_mxfp4": ([_vp, _vp, _i64, _i64, _int, _vp, _vp], _int),
+    "nvfp4_linear_mxfp4": ([_vp, _vp, _vp, _vp, _i64, _i64, _i64, _int, _vp, _vp, _sz, _u32, _vp],
+                           _int),
+    "nvfp4_linear_dynamic_mxfp4": ([_vp, _int, _vp, _vp, _i64, _i64, _i64, _int, _vp, _vp, _sz,
+                                    _u32, _vp], _int),
     "nvfp4_selftest_wait_timeout": ([_vp], _int),
     "nvfp4_selftest_grid_exchange": ([_int, _vp, _int, _int, ctypes.c_uint32, ctypes.c_uint32,
                                       _vp, _vp, ctypes.c_size_t, _vp], _int),

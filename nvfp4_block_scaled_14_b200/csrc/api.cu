@@ -213,6 +213,50 @@ DynWs linear_dynamic_ws(int64_t M, int64_t N, int64_t K)
     return d;
 }
 
+// Workspace of nvfp4_linear_dynamic_mxfp4 when it runs as quantize + linear (total = 0 when the
+// fused kernel takes the shape).
+struct DynMxWs {
+    size_t codes, scales, lws, total;
+};
+DynMxWs linear_dynamic_mx_ws(int64_t M, int64_t N, int64_t K)
+{
+    DynMxWs d{};
+    LinearPlan pl;
+    if (plan_linear_xq(M, N, K, &pl))
+        return d;
+    d.codes = 0;
+    d.scales = d.codes + align256(nvfp4_codes_bytes(M, K));
+    d.lws = d.scales + align256(nvfp4_mxfp4_scales_bytes(M, K, 1));
+    d.total = d.lws + align256(plan_linear(M, N, K).ws_bytes);
+    return d;
+}
+
+// Host-side checks shared by the MXFP4 linear calls (sizes, enums, empty results). Returns
+// NVFP4_OK with *done set when there is nothing left to launch.
+nvfp4_status check_linear_mx(int64_t M, int64_t N, int64_t K, nvfp4_dtype out_dt, uint32_t flags,
+                             void *y, cudaStream_t stream, bool *done)
+{
+    *done = true;
+    if (flags & ~(uint32_t)NVFP4_LINEAR_RESIDENT_WEIGHTS)
+        return NVFP4_ERR_INVALID_ARG;
+    if (M < 0 || N < 0 || K < 0 || M >= kMaxDim || N >= kMaxDim || K >= kMaxDim || K % 32 != 0)
+        return NVFP4_ERR_SHAPE;
+    if (out_dt != NVFP4_F32 && out_dt != NVFP4_BF16)
+        return NVFP4_ERR_INVALID_ARG;
+    if (M == 0 || N == 0)
+        return NVFP4_OK;
+    if (!y)
+        return NVFP4_ERR_INVALID_ARG;
+    const nvfp4_status st = check_device();
+    if (st != NVFP4_OK)
+        return st;
+    if (K == 0)
+        return map_cuda(
+            cudaMemsetAsync(y, 0, (size_t)M * N * (out_dt == NVFP4_BF16 ? 2 : 4), stream));
+    *done = false;
+    return NVFP4_OK;
+}
+
 } // namespace
 
 extern "C" {
@@ -294,6 +338,10 @@ size_t nvfp4_workspace_bytes(int op, int64_t m, int64_t n, int64_t k)
         if (m <= 0 || n <= 0 || m >= kMaxDim || n > 256)
             return 0;
         return (size_t)m * (size_t)n * 2;
+    case NVFP4_OP_LINEAR_DYNAMIC_MXFP4:
+        if (m <= 0 || n <= 0 || k <= 0)
+            return 0;
+        return linear_dynamic_mx_ws(m, n, k).total;
     case NVFP4_OP_CALIB_BF16: return calib_workspace_bytes(1);
     case NVFP4_OP_CALIB_F32: return calib_workspace_bytes(0);
     }
@@ -443,6 +491,123 @@ nvfp4_status nvfp4_linear_ex(const uint8_t *a_codes, const uint8_t *a_scales_swz
     if (st != NVFP4_OK)
         return st;
     return map_cuda(e);
+}
+
+size_t nvfp4_mxfp4_scales_bytes(int64_t rows, int64_t cols, int swizzled)
+{
+    if (rows < 0 || cols < 0)
+        return 0;
+    const int64_t nb = cols / 32;
+    if (!swizzled)
+        return (size_t)(rows * nb);
+    return (size_t)(((rows + 127) / 128) * 128 * ((nb + 3) / 4) * 4);
+}
+
+nvfp4_status nvfp4_quantize_mxfp4(const void *x, nvfp4_dtype dt, int64_t rows, int64_t cols,
+                                  int scale_rule, uint8_t *codes, uint8_t *scales_swz,
+                                  uint8_t *scales_lin, uint8_t *codes_t, uint8_t *scales_swz_t,
+                                  uint8_t *scales_lin_t, cudaStream_t stream)
+{
+    if ((dt != NVFP4_F32 && dt != NVFP4_BF16) ||
+        (scale_rule != NVFP4_MX_SCALE_FLOOR && scale_rule != NVFP4_MX_SCALE_CEIL))
+        return NVFP4_ERR_INVALID_ARG;
+    nvfp4_status st = check_matrix(rows, cols);
+    if (st != NVFP4_OK)
+        return st;
+    if (rows == 0 || cols == 0)
+        return NVFP4_OK;
+    if (!x || (!codes && !codes_t) || (codes && !scales_swz && !scales_lin) ||
+        (codes_t && !scales_swz_t && !scales_lin_t) || (!codes && (scales_swz || scales_lin)) ||
+        (!codes_t && (scales_swz_t || scales_lin_t)))
+        return NVFP4_ERR_INVALID_ARG;
+    const void *ptrs[] = {x, codes, scales_swz, scales_lin, codes_t, scales_swz_t, scales_lin_t};
+    for (const void *q : ptrs)
+        if (!aligned16(q))
+            return NVFP4_ERR_ALIGNMENT;
+    if ((st = check_device()) != NVFP4_OK)
+        return st;
+    return map_cuda(launch_quantize_mx(x, dt == NVFP4_BF16, rows, cols,
+                                       scale_rule == NVFP4_MX_SCALE_CEIL, codes, scales_swz,
+                                       scales_lin, codes_t, scales_swz_t, scales_lin_t, stream));
+}
+
+nvfp4_status nvfp4_dequantize_mxfp4(const uint8_t *codes, const uint8_t *scales_lin, int64_t rows,
+                                    int64_t cols, nvfp4_dtype out_dt, void *out,
+                                    cudaStream_t stream)
+{
+    nvfp4_status st = check_matrix(rows, cols);
+    if (st != NVFP4_OK)
+        return st;
+    if (out_dt != NVFP4_F32 && out_dt != NVFP4_BF16)
+        return NVFP4_ERR_INVALID_ARG;
+    if (rows == 0 || cols == 0)
+        return NVFP4_OK;
+    if (!codes || !scales_lin || !out)
+        return NVFP4_ERR_INVALID_ARG;
+    if (!aligned16(codes) || !aligned16(out))
+        return NVFP4_ERR_ALIGNMENT;
+    if ((st = check_device()) != NVFP4_OK)
+        return st;
+    return map_cuda(launch_dequantize_mx(codes, scales_lin, rows, cols, out_dt == NVFP4_BF16, out,
+                                         stream));
+}
+
+nvfp4_status nvfp4_linear_mxfp4(const uint8_t *a_codes, const uint8_t *a_scales_swz,
+                                const uint8_t *w_codes, const uint8_t *w_scales_swz, int64_t M,
+                                int64_t N, int64_t K, nvfp4_dtype out_dt, void *y, void *ws,
+                                size_t ws_bytes, uint32_t flags, cudaStream_t stream)
+{
+    bool done;
+    nvfp4_status st = check_linear_mx(M, N, K, out_dt, flags, y, stream, &done);
+    if (done)
+        return st;
+    if (!a_codes || !a_scales_swz || !w_codes || !w_scales_swz)
+        return NVFP4_ERR_INVALID_ARG;
+    if (!aligned16(a_codes) || !aligned16(a_scales_swz) || !aligned16(w_codes) ||
+        !aligned16(w_scales_swz) || !aligned16(y) || !aligned16(ws))
+        return NVFP4_ERR_ALIGNMENT;
+    const LinearPlan pl = plan_linear(M, N, K, flags);
+    if (pl.ws_bytes > 0 && (!ws || ws_bytes < pl.ws_bytes))
+        return NVFP4_ERR_WORKSPACE;
+    st = NVFP4_OK;
+    const cudaError_t e = launch_linear_mx(pl, a_codes, a_scales_swz, w_codes, w_scales_swz, M, N,
+                                           K, out_dt == NVFP4_BF16, y, ws, flags, stream, &st);
+    return st != NVFP4_OK ? st : map_cuda(e);
+}
+
+nvfp4_status nvfp4_linear_dynamic_mxfp4(const void *x, nvfp4_dtype x_dt, const uint8_t *w_codes,
+                                        const uint8_t *w_scales_swz, int64_t M, int64_t N,
+                                        int64_t K, nvfp4_dtype out_dt, void *y, void *ws,
+                                        size_t ws_bytes, uint32_t flags, cudaStream_t stream)
+{
+    if (x_dt != NVFP4_F32 && x_dt != NVFP4_BF16)
+        return NVFP4_ERR_INVALID_ARG;
+    bool done;
+    nvfp4_status st = check_linear_mx(M, N, K, out_dt, flags, y, stream, &done);
+    if (done)
+        return st;
+    if (!x || !w_codes || !w_scales_swz)
+        return NVFP4_ERR_INVALID_ARG;
+    if (!aligned16(x) || !aligned16(w_codes) || !aligned16(w_scales_swz) || !aligned16(y) ||
+        !aligned16(ws))
+        return NVFP4_ERR_ALIGNMENT;
+    LinearPlan pl;
+    if (plan_linear_xq(M, N, K, &pl)) {
+        const cudaError_t e =
+            launch_linear_xq_mx(pl, x, x_dt == NVFP4_BF16, w_codes, w_scales_swz, M, N, K,
+                                out_dt == NVFP4_BF16, y, flags, stream, &st);
+        return st != NVFP4_OK ? st : map_cuda(e);
+    }
+    const DynMxWs d = linear_dynamic_mx_ws(M, N, K);
+    if (!ws || ws_bytes < d.total)
+        return NVFP4_ERR_WORKSPACE;
+    uint8_t *w = reinterpret_cast<uint8_t *>(ws);
+    st = nvfp4_quantize_mxfp4(x, x_dt, M, K, NVFP4_MX_SCALE_FLOOR, w + d.codes, w + d.scales,
+                              nullptr, nullptr, nullptr, nullptr, stream);
+    if (st != NVFP4_OK)
+        return st;
+    return nvfp4_linear_mxfp4(w + d.codes, w + d.scales, w_codes, w_scales_swz, M, N, K, out_dt, y,
+                              w + d.lws, ws_bytes - d.lws, flags, stream);
 }
 
 nvfp4_status nvfp4_calib_percentile_amax(const void *const *batches, int num_batches,

@@ -45,6 +45,7 @@
 #include <mutex>
 #include <type_traits>
 
+#include "mxfp4_encode.cuh"
 #include "nvfp4_encode.cuh"
 #include "nvfp4_internal.cuh"
 #include "sm100_ptx.cuh"
@@ -63,14 +64,100 @@ constexpr uint32_t kWaitLimit = 1u << 20;
 #endif
 constexpr bool kUsePairKernel = NVFP4_PAIR_KERNEL != 0;
 
+// Operand formats. Both hold E2M1 codes in 256-wide k-tiles of 128 bytes a row; they differ in
+// the scales only. NVFP4: one E4M3 byte per 16 values, so a k-tile has four scale atoms (128
+// rows x 4 blocks) and each K64 MMA takes the four bytes of one atom (scale_vec::4X). MXFP4: one
+// E8M0 byte per 32 values, two atoms per k-tile, and each K64 MMA takes half of an atom's four
+// bytes (scale_vec::2X; the scale-factor ids in the instruction descriptor, 0 or 2, say which).
+// MXFP4 has no global scale: alpha = 1.
+struct FmtNvfp4 {
+    static constexpr bool kMx = false;
+    static constexpr int kAtoms = 4;  // scale atoms per k-tile and 128-row band
+    static constexpr int kBlock = 16; // values per scale
+    static constexpr uint32_t kIdesc = 0u;
+};
+struct FmtMxfp4 {
+    static constexpr bool kMx = true;
+    static constexpr int kAtoms = 2;
+    static constexpr int kBlock = 32;
+    static constexpr uint32_t kIdesc = 1u << 23; // UE8M0 scales
+};
+
+// Scale atom, and instruction-descriptor bits, of the kb-th K64 MMA of a k-tile.
+template <class F> __device__ __forceinline__ constexpr int sf_atom(int kb)
+{
+    return F::kMx ? kb >> 1 : kb;
+}
+template <class F> __device__ __forceinline__ constexpr uint32_t sf_id_bits(int kb)
+{
+    return F::kMx ? ((uint32_t)(kb & 1) * 2u) * ((1u << 29) | (1u << 4)) : 0u;
+}
+
+// alpha of the epilogue: sgA * sgW, 1 for MXFP4.
+template <class F>
+__device__ __forceinline__ float product_scale(const float *a_gs, const float *w_gs)
+{
+    if constexpr (F::kMx)
+        return 1.0f;
+    else
+        return __fmul_rn(*a_gs, *w_gs);
+}
+
+// The scale atoms (F::kAtoms x 512 bytes) at shared address `ssf` -> TMEM columns tcol.. of this
+// warp's lane quarter: 4 columns per atom, lane r holding the atom's 16-byte row r.
+template <class F> __device__ __forceinline__ void feed_atoms(uint32_t ssf, uint32_t tcol, int lane)
+{
+    uint32_t r[4 * F::kAtoms];
+#pragma unroll
+    for (int kb = 0; kb < F::kAtoms; ++kb) {
+        const uint4 w = lds128(ssf + kb * 512 + lane * 16);
+        r[4 * kb] = w.x;
+        r[4 * kb + 1] = w.y;
+        r[4 * kb + 2] = w.z;
+        r[4 * kb + 3] = w.w;
+    }
+    if constexpr (F::kMx)
+        tmem_st_32x32b_x8(tcol, r);
+    else
+        tmem_st_32x32b_x16(tcol, r);
+}
+
+template <class F>
+__device__ __forceinline__ void tc_mma_fp4(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc,
+                                           uint32_t idesc, uint32_t sfa_tmem, uint32_t sfb_tmem,
+                                           uint32_t accumulate)
+{
+    if constexpr (F::kMx)
+        tc_mma_mxf4(d_tmem, adesc, bdesc, idesc, sfa_tmem, sfb_tmem, accumulate);
+    else
+        tc_mma_nvf4(d_tmem, adesc, bdesc, idesc, sfa_tmem, sfb_tmem, accumulate);
+}
+
+template <class F>
+__device__ __forceinline__ void tc_mma_fp4_pair(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc,
+                                                uint32_t idesc, uint32_t sfa_tmem,
+                                                uint32_t sfb_tmem, uint32_t accumulate)
+{
+    if constexpr (F::kMx)
+        tc_mma_mxf4_pair(d_tmem, adesc, bdesc, idesc, sfa_tmem, sfb_tmem, accumulate);
+    else
+        tc_mma_nvf4_pair(d_tmem, adesc, bdesc, idesc, sfa_tmem, sfb_tmem, accumulate);
+}
+
+// Stages of the 1-SM kernels' operand ring for a B tile of BN rows.
+constexpr int default_stages(int bn)
+{
+    return bn == 256 ? NVFP4_STAGES_256 : (bn == 128 ? 6 : 7);
+}
+
 // Shared-memory / TMEM layout of the 1-SM kernels for a B tile of BN rows and STAGES stages.
-template <int BN, int STAGES = (BN == 256 ? NVFP4_STAGES_256 : (BN == 128 ? 6 : 7))> struct Cfg {
+template <int BN, class F, int STAGES = default_stages(BN)> struct Cfg {
     static constexpr int kStages = STAGES;
     static constexpr int kSfbBands = BN > 128 ? 2 : 1;
     static constexpr int kABytes = BM * 128;
     static constexpr int kBBytes = BN * 128;
-    static constexpr int kSfaBytes = 4 * 512;
-    static constexpr int kSfbBytes = kSfbBands * 4 * 512;
+    static constexpr int kSfaBytes = F::kAtoms * 512;
+    static constexpr int kSfbBytes = kSfbBands * F::kAtoms * 512;
     static constexpr int kStageBytes = kABytes + kBBytes + kSfaBytes + kSfbBytes;
     static constexpr int kOffB = kStages * kABytes;
     static constexpr int kOffSfa = kOffB + kStages * kBBytes;
@@ -95,9 +182,9 @@ template <int BN, int STAGES = (BN == 256 ? NVFP4_STAGES_256 : (BN == 128 ? 6 : 
                                      : kUsedCols <= 256 ? 256
                                                         : 512;
     static constexpr uint32_t kTx = kStageBytes;
-    // instruction descriptor: E2M1 x E2M1, K-major both, UE4M3 scales, M = 128, N = BN
-    static constexpr uint32_t kIdesc =
-        (1u << 7) | (1u << 10) | ((uint32_t)(BN >> 3) << 17) | ((uint32_t)(BM >> 4) << 24);
+    // instruction descriptor: E2M1 x E2M1, K-major both, M = 128, N = BN (scale type from F)
+    static constexpr uint32_t kIdesc = F::kIdesc | (1u << 7) | (1u << 10) |
+                                       ((uint32_t)(BN >> 3) << 17) | ((uint32_t)(BM >> 4) << 24);
     static constexpr bool kResidentB = false;
     static_assert(kSmemBytes <= 232448, "shared memory budget");
     static_assert(kUsedCols <= 512, "TMEM budget");
@@ -318,7 +405,7 @@ __device__ __forceinline__ void store_row_bf16_swap(const GemmParams &p, int64_t
     }
 }
 
-template <int BN>
+template <int BN, class F>
 __global__ void __launch_bounds__(kThreads, 1)
     nvfp4_gemm_kernel(const __grid_constant__ CUtensorMap tmA,
                       const __grid_constant__ CUtensorMap tmB,
@@ -326,7 +413,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                       const __grid_constant__ CUtensorMap tmSFB,
                       const __grid_constant__ CUtensorMap tmY, const GemmParams p)
 {
-    using C = Cfg<BN>;
+    using C = Cfg<BN, F>;
     extern __shared__ __align__(1024) uint8_t smem[];
     if ((smem_u32(smem) & 1023u) != 0) { // the swizzled operand tiles need 1024-B alignment
         if (threadIdx.x == 0)
@@ -400,8 +487,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                     mbar_arrive_expect_tx(&full_bar[stage], C::kTx);
                     tma_load_2d(sa, &tmA, &full_bar[stage], kt * 128, (int)(ta * BM));
                     tma_load_2d(sb, &tmB, &full_bar[stage], kt * 128, (int)(tb * BN));
-                    tma_load_3d(ssfa, &tmSFA, &full_bar[stage], 0, kt * 4, (int)ta);
-                    tma_load_3d(ssfb, &tmSFB, &full_bar[stage], 0, kt * 4,
+                    tma_load_3d(ssfa, &tmSFA, &full_bar[stage], 0, kt * F::kAtoms, (int)ta);
+                    tma_load_3d(ssfb, &tmSFB, &full_bar[stage], 0, kt * F::kAtoms,
                                 (int)((tb * BN) >> 7));
                     ++issued;
                     if (++stage == C::kStages) {
@@ -447,44 +534,25 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const uint32_t tslot =
                     tmem + ((uint32_t)(q * 32) << 16) + C::kSfCol + slot * C::kSlotCols;
                 // SFA: atom kb -> columns 4*kb .. 4*kb+3 (row r of the atom in lane r)
-                uint32_t ra[16];
-#pragma unroll
-                for (int kb = 0; kb < 4; ++kb) {
-                    const uint4 w = lds128(ssfa + kb * 512 + lane * 16);
-                    ra[4 * kb] = w.x;
-                    ra[4 * kb + 1] = w.y;
-                    ra[4 * kb + 2] = w.z;
-                    ra[4 * kb + 3] = w.w;
-                }
-                tmem_st_32x32b_x16(tslot, ra);
+                feed_atoms<F>(ssfa, tslot, lane);
                 // SFB: atom (band h, kb) -> columns 16 + kb*kSfbColsPerKb + 4*h
+                if constexpr (C::kSfbBands == 1) {
+                    feed_atoms<F>(ssfb, tslot + 16, lane);
+                } else {
 #pragma unroll
-                for (int h = 0; h < C::kSfbBands; ++h) {
-                    uint32_t rb[16];
+                    for (int h = 0; h < C::kSfbBands; ++h) {
+                        uint4 w[F::kAtoms];
 #pragma unroll
-                    for (int kb = 0; kb < 4; ++kb) {
-                        const uint4 w = lds128(ssfb + (h * 4 + kb) * 512 + lane * 16);
-                        rb[4 * kb] = w.x;
-                        rb[4 * kb + 1] = w.y;
-                        rb[4 * kb + 2] = w.z;
-                        rb[4 * kb + 3] = w.w;
-                    }
-                    if constexpr (C::kSfbBands == 1) {
-                        tmem_st_32x32b_x16(tslot + 16, rb);
-                    } else {
+                        for (int kb = 0; kb < F::kAtoms; ++kb)
+                            w[kb] = lds128(ssfb + (h * F::kAtoms + kb) * 512 + lane * 16);
                         // interleave bands: kb-major, band-minor
 #pragma unroll
-                        for (int kb = 0; kb < 4; ++kb) {
-                            uint32_t t4[16];
-#pragma unroll
-                            for (int i = 0; i < 4; ++i)
-                                t4[i] = rb[4 * kb + i];
+                        for (int kb = 0; kb < F::kAtoms; ++kb)
                             asm volatile("tcgen05.st.sync.aligned.32x32b.x4.b32 [%0], "
                                          "{%1, %2, %3, %4};" ::"r"(tslot + 16 +
                                                                      kb * C::kSfbColsPerKb + 4 * h),
-                                         "r"(t4[0]), "r"(t4[1]), "r"(t4[2]), "r"(t4[3])
+                                         "r"(w[kb].x), "r"(w[kb].y), "r"(w[kb].z), "r"(w[kb].w)
                                          : "memory");
-                        }
                     }
                 }
                 tmem_st_wait();
@@ -537,9 +605,10 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                     for (int kb = 0; kb < 4; ++kb) {
                         // advance 32 bytes (64 FP4 values) along K inside the swizzle atom
-                        tc_mma_nvf4(tmem, adesc + (uint64_t)(2 * kb), bdesc + (uint64_t)(2 * kb),
-                                    C::kIdesc, tsfa + kb * 4, tsfb + kb * C::kSfbColsPerKb,
-                                    (kt > k0 || kb > 0) ? 1u : 0u);
+                        tc_mma_fp4<F>(tmem, adesc + (uint64_t)(2 * kb), bdesc + (uint64_t)(2 * kb),
+                                      C::kIdesc | sf_id_bits<F>(kb), tsfa + sf_atom<F>(kb) * 4,
+                                      tsfb + sf_atom<F>(kb) * C::kSfbColsPerKb,
+                                      (kt > k0 || kb > 0) ? 1u : 0u);
                     }
                     tc_commit(&empty_bar[stage]);
                     tc_commit(&sf_empty[slot]);
@@ -571,7 +640,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     } else {
         // ------------------------------- epilogue (warps 2..5) ----------------------
         const int q = warp & 3; // TMEM lane quarter this warp may access
-        const float alpha = __fmul_rn(*p.a_gs, *p.w_gs);
+        const float alpha = product_scale<F>(p.a_gs, p.w_gs);
         uint32_t acc_phase = 0;
         for (int64_t u = blockIdx.x; u < p.units; u += gridDim.x) {
             const int split = (int)(u / tiles_ab);
@@ -854,12 +923,12 @@ __device__ __forceinline__ void stage_store_tile_halves(const GemmParams &p, con
 // bf16 staging tile (the output leaves in two halves), four scale slots; quantizing epilogue:
 // four stages and 64 KB of staging (fp32 columns 128-255 of each row), two scale slots and 128
 // TMEM columns for columns 0-127 (both kept while the tile is quantized after the hand-back).
-template <bool QOUT> struct Pair {
+template <bool QOUT, class F> struct Pair {
     static constexpr int kStages = QOUT ? 4 : 5;
     static constexpr int kABytes = 128 * 128;     // this CTA's 128 rows of A
     static constexpr int kBBytes = 128 * 128;     // this CTA's 128 rows of B
-    static constexpr int kSfaBytes = 4 * 512;     // SFA atoms of this CTA's rows
-    static constexpr int kSfbBytes = 2 * 4 * 512; // SFB atoms of all 256 columns
+    static constexpr int kSfaBytes = F::kAtoms * 512;     // SFA atoms of this CTA's rows
+    static constexpr int kSfbBytes = 2 * F::kAtoms * 512; // SFB atoms of all 256 columns
     static constexpr int kOffB = kStages * kABytes;
     static constexpr int kOffSfa = kOffB + kStages * kBBytes;
     static constexpr int kOffSfb = kOffSfa + kStages * kSfaBytes;
@@ -877,8 +946,9 @@ template <bool QOUT> struct Pair {
     static constexpr int kSfCol = 256;
     static constexpr int kParkCol = kSfCol + kSfSlots * kSlotCols; // QOUT: columns 0-127 kept
     static constexpr int kTmemCols = 512;
-    static constexpr uint32_t kIdesc =
-        (1u << 7) | (1u << 10) | ((uint32_t)(256 >> 3) << 17) | ((uint32_t)(256 >> 4) << 24);
+    static constexpr uint32_t kIdesc = F::kIdesc | (1u << 7) | (1u << 10) |
+                                       ((uint32_t)(256 >> 3) << 17) |
+                                       ((uint32_t)(256 >> 4) << 24);
     // low-rank k-tiles: kind::f16 with D fp32 (bits 4-5 = 1), A and B bf16 (bits 7-9 and
     // 10-12 = 1), K-major, M256 x N256; a 64-wide bf16 k-tile fills the same 128-byte smem
     // rows as a 256-wide FP4 k-tile, so it reuses the stage buffers and their byte counts
@@ -902,7 +972,7 @@ __device__ __forceinline__ void tc_mma_bf16_pair(uint32_t d_tmem, uint64_t adesc
                  : "memory");
 }
 
-template <bool QOUT, bool LR>
+template <bool QOUT, bool LR, class F>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     nvfp4_gemm_pair_kernel(const __grid_constant__ CUtensorMap tmA,
                            const __grid_constant__ CUtensorMap tmB,
@@ -912,7 +982,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                            const __grid_constant__ CUtensorMap tmT,
                            const __grid_constant__ CUtensorMap tmU, const GemmParams p)
 {
-    using C = Pair<QOUT>;
+    using C = Pair<QOUT, F>;
+    static_assert(!F::kMx || (!QOUT && !LR), "MXFP4: plain bf16 output only");
     extern __shared__ __align__(1024) uint8_t smem[];
     if ((smem_u32(smem) & 1023u) != 0) {
         if (threadIdx.x == 0)
@@ -1009,9 +1080,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                     tma_load_2d_pair(smem + C::kOffB + stage * C::kBBytes, &tmB, leader_full,
                                      kt * 128, brow);
                     tma_load_3d(smem + C::kOffSfa + stage * C::kSfaBytes, &tmSFA, &sfdata[stage], 0,
-                                kt * 4, arow >> 7);
+                                kt * F::kAtoms, arow >> 7);
                     tma_load_3d(smem + C::kOffSfb + stage * C::kSfbBytes, &tmSFB, &sfdata[stage], 0,
-                                kt * 4, (int)(tb * 2));
+                                kt * F::kAtoms, (int)(tb * 2));
                     if (++stage == C::kStages) {
                         stage = 0;
                         phase ^= 1;
@@ -1054,33 +1125,20 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 const uint32_t ssfb = smem_u32(smem + C::kOffSfb + stage * C::kSfbBytes);
                 const uint32_t tslot =
                     tmem + ((uint32_t)(q * 32) << 16) + C::kSfCol + slot * C::kSlotCols;
-                uint32_t ra[16];
-#pragma unroll
-                for (int kb = 0; kb < 4; ++kb) {
-                    const uint4 w = lds128(ssfa + kb * 512 + lane * 16);
-                    ra[4 * kb] = w.x;
-                    ra[4 * kb + 1] = w.y;
-                    ra[4 * kb + 2] = w.z;
-                    ra[4 * kb + 3] = w.w;
-                }
-                tmem_st_32x32b_x16(tslot, ra);
+                feed_atoms<F>(ssfa, tslot, lane);
                 // SFB: atom (band h, kb) -> columns 16 + 8*kb + 4*h
 #pragma unroll
-                for (int kb = 0; kb < 4; ++kb) {
-                    uint32_t rb[16];
+                for (int kb = 0; kb < F::kAtoms; ++kb) {
+                    uint32_t rb[8];
 #pragma unroll
                     for (int h = 0; h < 2; ++h) {
-                        const uint4 w = lds128(ssfb + (h * 4 + kb) * 512 + lane * 16);
+                        const uint4 w = lds128(ssfb + (h * F::kAtoms + kb) * 512 + lane * 16);
                         rb[4 * h] = w.x;
                         rb[4 * h + 1] = w.y;
                         rb[4 * h + 2] = w.z;
                         rb[4 * h + 3] = w.w;
                     }
-                    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], "
-                                 "{%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(tslot + 16 + 8 * kb),
-                                 "r"(rb[0]), "r"(rb[1]), "r"(rb[2]), "r"(rb[3]), "r"(rb[4]),
-                                 "r"(rb[5]), "r"(rb[6]), "r"(rb[7])
-                                 : "memory");
+                    tmem_st_32x32b_x8(tslot + 16 + 8 * kb, rb);
                 }
                 tmem_st_wait();
                 tc_fence_before();
@@ -1157,9 +1215,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                                       kLayoutSwizzle128B);
 #pragma unroll
                         for (int kb = 0; kb < 4; ++kb)
-                            tc_mma_nvf4_pair(tmem, adesc + (uint64_t)(2 * kb),
-                                             bdesc + (uint64_t)(2 * kb), C::kIdesc, tsfa + kb * 4,
-                                             tsfb + kb * 8, (kt > 0 || kb > 0) ? 1u : 0u);
+                            tc_mma_fp4_pair<F>(tmem, adesc + (uint64_t)(2 * kb),
+                                               bdesc + (uint64_t)(2 * kb),
+                                               C::kIdesc | sf_id_bits<F>(kb),
+                                               tsfa + sf_atom<F>(kb) * 4,
+                                               tsfb + sf_atom<F>(kb) * 8,
+                                               (kt > 0 || kb > 0) ? 1u : 0u);
                         tc_commit_pair_mc(&empty_bar[stage], 0x3);
                         tc_commit_pair_mc(&sf_empty[slot], 0x3);
                     }
@@ -1191,7 +1252,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         // ------------------------------- epilogue (both CTAs, warps 2..5) -------------
         const int q = warp & 3;
         pdl_wait(); // global scales (and Y's previous readers) belong to earlier kernels
-        float alpha = __fmul_rn(*p.a_gs, *p.w_gs);
+        float alpha = product_scale<F>(p.a_gs, p.w_gs);
         if (LR && alpha == 0.0f)
             alpha = 1.0f; // the FP4 product is zero; T' was not divided either
         const uint32_t leader_acc_empty = mapa_shared(smem_u32(acc_empty), 0);
@@ -1268,7 +1329,7 @@ __global__ void splitk_reduce_kernel(const float *__restrict__ partial, int spli
                                      const float *__restrict__ w_gs, void *__restrict__ y,
                                      int64_t ldy, int out_bf16, int swap)
 {
-    const float alpha = __fmul_rn(*a_gs, *w_gs);
+    const float alpha = a_gs ? __fmul_rn(*a_gs, *w_gs) : 1.0f; // MXFP4: no global scales
     const int64_t total = rows_a * rows_b;
     for (int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; i < total;
          i += (int64_t)gridDim.x * blockDim.x) {
@@ -1309,13 +1370,13 @@ __global__ void splitk_reduce_kernel(const float *__restrict__ partial, int spli
 // atoms (2 KB per k-tile) of this CTA's k-range (at most kXqMaxKt k-tiles) stay resident,
 // written by the CTA itself from the bf16 / fp32 activations.
 constexpr int kXqMaxKt = 8;
-template <int BN> struct XqLayout {
+template <int BN, class F> struct XqLayout {
     static constexpr int kStages = BN <= 16 ? 4 : 3;
     static constexpr int kSfbBands = 1;
     static constexpr int kABytes = BM * 128;
     static constexpr int kBBytes = BN * 128; // per resident k-tile
-    static constexpr int kSfaBytes = 4 * 512;
-    static constexpr int kSfbBytes = 4 * 512; // per resident k-tile
+    static constexpr int kSfaBytes = F::kAtoms * 512;
+    static constexpr int kSfbBytes = F::kAtoms * 512; // per resident k-tile
     static constexpr int kOffSfa = kStages * kABytes;
     static constexpr int kOffB = kOffSfa + kStages * kSfaBytes; // resident B
     static constexpr int kOffSfb = kOffB + kXqMaxKt * kBBytes;   // resident SFB atoms
@@ -1329,16 +1390,16 @@ template <int BN> struct XqLayout {
     static constexpr int kSfCol = kAccCols;
     static constexpr int kUsedCols = kSfCol + kSfSlots * kSlotCols;
     static constexpr int kTmemCols = kUsedCols <= 128 ? 128 : 256;
-    static constexpr uint32_t kIdesc =
-        (1u << 7) | (1u << 10) | ((uint32_t)(BN >> 3) << 17) | ((uint32_t)(BM >> 4) << 24);
+    static constexpr uint32_t kIdesc = F::kIdesc | (1u << 7) | (1u << 10) |
+                                       ((uint32_t)(BN >> 3) << 17) | ((uint32_t)(BM >> 4) << 24);
     static constexpr bool kResidentB = true;
     static_assert(kOffB % 1024 == 0, "swizzled operand alignment");
 };
 
-template <int BN, bool XQ = false> struct SmallCfg {
+template <int BN, bool XQ, class F> struct SmallCfg {
     // stages that keep one CTA at <= 113 KB of shared memory (two per SM)
     static constexpr int kStages = BN <= 16 ? 5 : BN <= 64 ? 4 : 3;
-    using L = typename std::conditional<XQ, XqLayout<BN>, Cfg<BN, kStages>>::type;
+    using L = typename std::conditional<XQ, XqLayout<BN, F>, Cfg<BN, F, kStages>>::type;
     static_assert(L::kSmemBytes <= 115712, "two CTAs per SM");
     static_assert(L::kTmemCols <= 256, "two CTAs per SM");
     // partial accumulators of a non-leader CTA, [BN][128] fp32, over the drained stages
@@ -1618,7 +1679,50 @@ __device__ __forceinline__ float xq_prologue(const SmallParams &p, uint8_t *smem
     return sg;
 }
 
-template <int BN, bool XQ>
+// MXFP4 form of the fused activation quantize: block scales need no tensor-wide maximum, so each
+// CTA encodes its k-range of x at once (one 32-value block per thread step), with the MXFP4
+// quantizer's arithmetic ("floor" scales; the codes equal nvfp4_quantize_mxfp4's).
+template <int BN, typename L>
+__device__ __forceinline__ void xq_prologue_mx(const SmallParams &p, uint8_t *smem, int k0, int k1)
+{
+    const int tid = threadIdx.x;
+    const int nk = k1 - k0;
+    uint4 *zb = reinterpret_cast<uint4 *>(smem + L::kOffB);
+    for (int i = tid; i < nk * L::kBBytes / 16; i += kThreads)
+        zb[i] = make_uint4(0u, 0u, 0u, 0u);
+    uint4 *zs = reinterpret_cast<uint4 *>(smem + L::kOffSfb);
+    for (int i = tid; i < nk * L::kSfbBytes / 16; i += kThreads)
+        zs[i] = make_uint4(0u, 0u, 0u, 0u);
+    __syncthreads();
+    const int nbk = (int)(p.K >> 5); // blocks per row
+    const int total = (int)p.rows_b * nk * 8;
+    for (int i = tid; i < total; i += kThreads) {
+        const int bb = i & 7;       // block inside the k-tile
+        const int j = (i >> 3) % nk; // resident k-tile
+        const int r = (i >> 3) / nk; // row
+        const int kb = (k0 + j) * 8 + bb;
+        if (kb >= nbk)
+            continue;
+        uint32_t w[4], sb;
+        if (p.x_bf16)
+            mx_encode_bf16(reinterpret_cast<const uint4 *>(
+                               reinterpret_cast<const uint8_t *>(p.x) + ((int64_t)r * p.K + kb * 32) * 2),
+                           w, sb);
+        else
+            mx_encode_f32(reinterpret_cast<const uint4 *>(
+                              reinterpret_cast<const uint8_t *>(p.x) + ((int64_t)r * p.K + kb * 32) * 4),
+                          w, sb);
+        // B tile j: row r at r * 128 bytes, 16-byte chunk (block) c stored at c ^ (r % 8)
+        *reinterpret_cast<uint4 *>(smem + L::kOffB + j * L::kBBytes + r * 128 +
+                                   ((bb ^ (r & 7)) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
+        smem[L::kOffSfb + j * L::kSfbBytes + (bb >> 2) * 512 + 16 * (r & 31) +
+             4 * ((r & 127) >> 5) + (bb & 3)] = (uint8_t)sb;
+    }
+    fence_proxy_async_smem(); // the tensor cores read the B tiles through the async proxy
+    __syncthreads();
+}
+
+template <int BN, bool XQ, class F>
 __global__ void __launch_bounds__(kThreads, 2)
     nvfp4_gemm_smallm_kernel(const __grid_constant__ CUtensorMap tmA,
                              const __grid_constant__ CUtensorMap tmB,
@@ -1626,7 +1730,7 @@ __global__ void __launch_bounds__(kThreads, 2)
                              const __grid_constant__ CUtensorMap tmSFB,
                              const __grid_constant__ CUtensorMap tmY, const SmallParams p)
 {
-    using C = typename SmallCfg<BN, XQ>::L;
+    using C = typename SmallCfg<BN, XQ, F>::L;
     extern __shared__ __align__(1024) uint8_t smem[];
     if ((smem_u32(smem) & 1023u) != 0) { // same for every CTA: the whole grid returns here
         if (threadIdx.x == 0)
@@ -1694,13 +1798,16 @@ __global__ void __launch_bounds__(kThreads, 2)
             tma_load_2d(smem + i * C::kABytes, &tmA, &full_bar[i], (k0 + i) * 128,
                         (int)(ta * BM));
             tma_load_3d(smem + C::kOffSfa + i * C::kSfaBytes, &tmSFA, &full_bar[i], 0,
-                        (k0 + i) * 4, (int)ta);
+                        (k0 + i) * F::kAtoms, (int)ta);
         }
     }
     float sg_x = 0.0f; // XQ: the activations' global scale
     if constexpr (XQ) {
         pdl_wait(); // the activations may come from the previous kernel
-        sg_x = xq_prologue<BN, C>(p, smem, rank, cs, k0, k1);
+        if constexpr (F::kMx)
+            xq_prologue_mx<BN, C>(p, smem, k0, k1);
+        else
+            sg_x = xq_prologue<BN, C>(p, smem, rank, cs, k0, k1);
     }
 
     if (warp == 0) {
@@ -1722,11 +1829,11 @@ __global__ void __launch_bounds__(kThreads, 2)
                     }
                     mbar_arrive_expect_tx(&full_bar[stage], C::kTx);
                     tma_load_2d(sa, &tmA, &full_bar[stage], kt * 128, (int)(ta * BM));
-                    tma_load_3d(ssfa, &tmSFA, &full_bar[stage], 0, kt * 4, (int)ta);
+                    tma_load_3d(ssfa, &tmSFA, &full_bar[stage], 0, kt * F::kAtoms, (int)ta);
                 }
                 if constexpr (!XQ) { // XQ: the activations are resident already
                     tma_load_2d(sb, &tmB, &full_bar[stage], kt * 128, 0);
-                    tma_load_3d(ssfb, &tmSFB, &full_bar[stage], 0, kt * 4, 0);
+                    tma_load_3d(ssfb, &tmSFB, &full_bar[stage], 0, kt * F::kAtoms, 0);
                 }
                 ++issued;
                 if (++stage == C::kStages) {
@@ -1765,22 +1872,8 @@ __global__ void __launch_bounds__(kThreads, 2)
                 smem_u32(smem + C::kOffSfb + (XQ ? kt - k0 : stage) * C::kSfbBytes);
             const uint32_t tslot =
                 tmem + ((uint32_t)(q * 32) << 16) + C::kSfCol + slot * C::kSlotCols;
-            uint32_t ra[16], rb[16];
-#pragma unroll
-            for (int kb = 0; kb < 4; ++kb) {
-                const uint4 wa = lds128(ssfa + kb * 512 + lane * 16);
-                const uint4 wb = lds128(ssfb + kb * 512 + lane * 16);
-                ra[4 * kb] = wa.x;
-                ra[4 * kb + 1] = wa.y;
-                ra[4 * kb + 2] = wa.z;
-                ra[4 * kb + 3] = wa.w;
-                rb[4 * kb] = wb.x;
-                rb[4 * kb + 1] = wb.y;
-                rb[4 * kb + 2] = wb.z;
-                rb[4 * kb + 3] = wb.w;
-            }
-            tmem_st_32x32b_x16(tslot, ra);
-            tmem_st_32x32b_x16(tslot + 16, rb);
+            feed_atoms<F>(ssfa, tslot, lane);
+            feed_atoms<F>(ssfb, tslot + 16, lane);
             tmem_st_wait();
             tc_fence_before();
             __syncwarp();
@@ -1818,9 +1911,10 @@ __global__ void __launch_bounds__(kThreads, 2)
                               1024, kLayoutSwizzle128B);
 #pragma unroll
                 for (int kb = 0; kb < 4; ++kb)
-                    tc_mma_nvf4(tmem, adesc + (uint64_t)(2 * kb), bdesc + (uint64_t)(2 * kb),
-                                C::kIdesc, tsfa + kb * 4, tsfa + 16 + kb * 4,
-                                (kt > k0 || kb > 0) ? 1u : 0u);
+                    tc_mma_fp4<F>(tmem, adesc + (uint64_t)(2 * kb), bdesc + (uint64_t)(2 * kb),
+                                  C::kIdesc | sf_id_bits<F>(kb), tsfa + sf_atom<F>(kb) * 4,
+                                  tsfa + 16 + sf_atom<F>(kb) * 4,
+                                  (kt > k0 || kb > 0) ? 1u : 0u);
                 tc_commit(&empty_bar[stage]);
                 tc_commit(&sf_empty[slot]);
             }
@@ -1852,7 +1946,10 @@ __global__ void __launch_bounds__(kThreads, 2)
         const uint32_t trow = tmem + ((uint32_t)(q * 32) << 16);
         constexpr int NC = BN < 32 ? BN : 32;
         pdl_wait(); // global scales and y belong to the stream's earlier work
-        alpha = __fmul_rn(XQ ? sg_x : *p.a_gs, *p.w_gs);
+        if constexpr (F::kMx)
+            alpha = 1.0f;
+        else
+            alpha = __fmul_rn(XQ ? sg_x : *p.a_gs, *p.w_gs);
         const bool ok = mbar_wait(acc_full, 0, kWaitLimit);
         if (!ok && lane == 0)
             set_timeout(p.status);
@@ -1943,14 +2040,15 @@ bool make_codes_map(CUtensorMap *m, const void *base, int64_t rows, int64_t K, i
                        CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// Swizzled scales viewed as [bands][atoms][128 x u32]; box = 4 atoms x box_bands bands.
+// Swizzled scales viewed as [bands][atoms][128 x u32]; box = one k-tile's atoms x box_bands bands.
+template <class F>
 bool make_sf_map(CUtensorMap *m, const void *base, int64_t rows, int64_t K, int box_bands)
 {
-    const int64_t apb = (K / 16 + 3) / 4;
+    const int64_t apb = (K / F::kBlock + 3) / 4;
     const int64_t bands = (rows + 127) / 128;
     cuuint64_t dims[3] = {128u, (cuuint64_t)apb, (cuuint64_t)bands};
     cuuint64_t strides[2] = {512u, (cuuint64_t)(apb * 512)};
-    cuuint32_t box[3] = {128u, 4u, (cuuint32_t)box_bands};
+    cuuint32_t box[3] = {128u, (cuuint32_t)F::kAtoms, (cuuint32_t)box_bands};
     cuuint32_t estr[3] = {1u, 1u, 1u};
     return encode_fn()(m, CU_TENSOR_MAP_DATA_TYPE_UINT32, 3, const_cast<void *>(base), dims,
                        strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
@@ -1987,12 +2085,12 @@ bool make_out_map_swap(CUtensorMap *m, void *base, int64_t rows, int64_t cols, i
                        CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int BN>
+template <int BN, class F>
 cudaError_t launch_bn(const LinearPlan &pl, const uint8_t *a_codes, const uint8_t *a_sf,
                       const uint8_t *b_codes, const uint8_t *b_sf, int64_t K, GemmParams gp,
                       cudaStream_t s, nvfp4_status *st)
 {
-    using C = Cfg<BN>;
+    using C = Cfg<BN, F>;
     CUtensorMap tmA, tmB, tmSFA, tmSFB, tmY;
     memset(&tmY, 0, sizeof(tmY));
     gp.tma_store = 0;
@@ -2002,8 +2100,8 @@ cudaError_t launch_bn(const LinearPlan &pl, const uint8_t *a_codes, const uint8_
         gp.tma_store = 1;
     if (!encode_fn() || !make_codes_map(&tmA, a_codes, pl.rows_a, K, BM) ||
         !make_codes_map(&tmB, b_codes, pl.rows_b, K, BN) ||
-        !make_sf_map(&tmSFA, a_sf, pl.rows_a, K, 1) ||
-        !make_sf_map(&tmSFB, b_sf, pl.rows_b, K, C::kSfbBands)) {
+        !make_sf_map<F>(&tmSFA, a_sf, pl.rows_a, K, 1) ||
+        !make_sf_map<F>(&tmSFB, b_sf, pl.rows_b, K, C::kSfbBands)) {
         *st = NVFP4_ERR_CUDA;
         return cudaErrorInvalidValue;
     }
@@ -2012,7 +2110,7 @@ cudaError_t launch_bn(const LinearPlan &pl, const uint8_t *a_codes, const uint8_
     cudaGetDevice(&dev);
     cudaError_t attr_err = cudaSuccess;
     std::call_once(flags[dev & 63], [&]() {
-        attr_err = cudaFuncSetAttribute(nvfp4_gemm_kernel<BN>,
+        attr_err = cudaFuncSetAttribute(nvfp4_gemm_kernel<BN, F>,
                                         cudaFuncAttributeMaxDynamicSharedMemorySize,
                                         C::kSmemBytes);
     });
@@ -2021,13 +2119,13 @@ cudaError_t launch_bn(const LinearPlan &pl, const uint8_t *a_codes, const uint8_
     int64_t grid = gp.units < num_sms() ? gp.units : num_sms();
     if (grid < 1)
         grid = 1;
-    nvfp4_gemm_kernel<BN><<<(unsigned)grid, kThreads, C::kSmemBytes, s>>>(tmA, tmB, tmSFA,
-                                                                          tmSFB, tmY, gp);
+    nvfp4_gemm_kernel<BN, F><<<(unsigned)grid, kThreads, C::kSmemBytes, s>>>(tmA, tmB, tmSFA,
+                                                                             tmSFB, tmY, gp);
     return cudaGetLastError();
 }
 
 // LR: lr_t (T' [M x lr_rank] bf16) and lr_u (U [N x lr_rank] bf16) feed the low-rank k-tiles.
-template <bool QOUT, bool LR = false>
+template <bool QOUT, bool LR = false, class F = FmtNvfp4>
 cudaError_t launch_pair(const uint8_t *a_codes, const uint8_t *a_sf, const uint8_t *w_codes,
                         const uint8_t *w_sf, int64_t M, int64_t N, int64_t K, GemmParams gp,
                         cudaStream_t s, nvfp4_status *st, const void *lr_t = nullptr,
@@ -2038,8 +2136,8 @@ cudaError_t launch_pair(const uint8_t *a_codes, const uint8_t *a_sf, const uint8
     std::memset(&tmT, 0, sizeof(tmT));
     std::memset(&tmU, 0, sizeof(tmU));
     if (!encode_fn() || !make_codes_map(&tmA, a_codes, M, K, 128) ||
-        !make_codes_map(&tmB, w_codes, N, K, 128) || !make_sf_map(&tmSFA, a_sf, M, K, 1) ||
-        !make_sf_map(&tmSFB, w_sf, N, K, 2) || (!QOUT && !make_out_map(&tmY, gp.y, M, N)) ||
+        !make_codes_map(&tmB, w_codes, N, K, 128) || !make_sf_map<F>(&tmSFA, a_sf, M, K, 1) ||
+        !make_sf_map<F>(&tmSFB, w_sf, N, K, 2) || (!QOUT && !make_out_map(&tmY, gp.y, M, N)) ||
         (LR && (!make_bf16_kmajor_map(&tmT, lr_t, M, lr_rank, 128) ||
                 !make_bf16_kmajor_map(&tmU, lr_u, N, lr_rank, 128)))) {
         *st = NVFP4_ERR_CUDA;
@@ -2051,9 +2149,9 @@ cudaError_t launch_pair(const uint8_t *a_codes, const uint8_t *a_sf, const uint8
     cudaGetDevice(&dev);
     cudaError_t attr_err = cudaSuccess;
     std::call_once(flags[dev & 63], [&]() {
-        attr_err = cudaFuncSetAttribute(nvfp4_gemm_pair_kernel<QOUT, LR>,
+        attr_err = cudaFuncSetAttribute(nvfp4_gemm_pair_kernel<QOUT, LR, F>,
                                         cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                        Pair<QOUT>::kSmemBytes);
+                                        Pair<QOUT, F>::kSmemBytes);
     });
     if (attr_err != cudaSuccess)
         return attr_err;
@@ -2071,31 +2169,31 @@ cudaError_t launch_pair(const uint8_t *a_codes, const uint8_t *a_sf, const uint8
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3((unsigned)(2 * clusters), 1, 1);
     cfg.blockDim = dim3(kThreads, 1, 1);
-    cfg.dynamicSmemBytes = Pair<QOUT>::kSmemBytes;
+    cfg.dynamicSmemBytes = Pair<QOUT, F>::kSmemBytes;
     cfg.stream = s;
     cudaLaunchAttribute at[1];
     at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     at[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = at;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, nvfp4_gemm_pair_kernel<QOUT, LR>, tmA, tmB, tmSFA, tmSFB, tmY,
-                              tmT, tmU, gp);
+    return cudaLaunchKernelEx(&cfg, nvfp4_gemm_pair_kernel<QOUT, LR, F>, tmA, tmB, tmSFA, tmSFB,
+                              tmY, tmT, tmU, gp);
 }
 
-template <int BN, bool XQ = false> cudaError_t smallm_set_smem_attr()
+template <int BN, bool XQ, class F> cudaError_t smallm_set_smem_attr()
 {
     static std::once_flag flags[64];
     int dev = 0;
     cudaGetDevice(&dev);
     cudaError_t e = cudaSuccess;
     std::call_once(flags[dev & 63], [&]() {
-        e = cudaFuncSetAttribute(nvfp4_gemm_smallm_kernel<BN, XQ>,
+        e = cudaFuncSetAttribute(nvfp4_gemm_smallm_kernel<BN, XQ, F>,
                                  cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                 SmallCfg<BN, XQ>::L::kSmemBytes);
-        if (e == cudaSuccess && !XQ)
+                                 SmallCfg<BN, XQ, F>::L::kSmemBytes);
+        if (e == cudaSuccess && !XQ && !F::kMx)
             e = cudaFuncSetAttribute(smallm_occupancy_proxy<BN>,
                                      cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                     SmallCfg<BN>::L::kSmemBytes);
+                                     SmallCfg<BN, false, FmtNvfp4>::L::kSmemBytes);
     });
     return e;
 }
@@ -2103,12 +2201,12 @@ template <int BN, bool XQ = false> cudaError_t smallm_set_smem_attr()
 // Clusters of cs CTAs of the small-M kernel that can be resident at once on this device.
 template <int BN> int smallm_max_clusters(int cs)
 {
-    if (smallm_set_smem_attr<BN>() != cudaSuccess)
+    if (smallm_set_smem_attr<BN, false, FmtNvfp4>() != cudaSuccess)
         return 0;
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3((unsigned)(cs * 1024), 1, 1);
     cfg.blockDim = dim3(kThreads, 1, 1);
-    cfg.dynamicSmemBytes = SmallCfg<BN>::L::kSmemBytes;
+    cfg.dynamicSmemBytes = SmallCfg<BN, false, FmtNvfp4>::L::kSmemBytes;
     cudaLaunchAttribute at[1];
     at[0].id = cudaLaunchAttributeClusterDimension;
     at[0].val.clusterDim.x = (unsigned)cs;
@@ -2152,12 +2250,12 @@ const SmallOccupancy &small_occupancy()
 
 int bn_index(int bn) { return bn <= 8 ? 0 : bn <= 16 ? 1 : bn <= 32 ? 2 : bn <= 64 ? 3 : 4; }
 
-template <int BN, bool XQ = false>
+template <int BN, bool XQ = false, class F = FmtNvfp4>
 cudaError_t launch_smallm(const LinearPlan &pl, const uint8_t *w_codes, const uint8_t *w_sf,
                           const uint8_t *a_codes, const uint8_t *a_sf, int64_t K,
                           const SmallParams &sp, cudaStream_t s, nvfp4_status *st)
 {
-    using C = typename SmallCfg<BN, XQ>::L;
+    using C = typename SmallCfg<BN, XQ, F>::L;
     CUtensorMap tmA, tmB, tmSFA, tmSFB, tmY;
     memset(&tmY, 0, sizeof(tmY));
     memset(&tmB, 0, sizeof(tmB));
@@ -2169,13 +2267,13 @@ cudaError_t launch_smallm(const LinearPlan &pl, const uint8_t *w_codes, const ui
         encode_fn() && make_out_map_swap(&tmY, sp.y, pl.rows_b, sp.ldy, sp.out_bf16, BN / pl.csplit))
         spl.tma_store = 1;
     if (!encode_fn() || !make_codes_map(&tmA, w_codes, pl.rows_a, K, BM) ||
-        !make_sf_map(&tmSFA, w_sf, pl.rows_a, K, 1) ||
+        !make_sf_map<F>(&tmSFA, w_sf, pl.rows_a, K, 1) ||
         (!XQ && (!make_codes_map(&tmB, a_codes, pl.rows_b, K, BN) ||
-                 !make_sf_map(&tmSFB, a_sf, pl.rows_b, K, 1)))) {
+                 !make_sf_map<F>(&tmSFB, a_sf, pl.rows_b, K, 1)))) {
         *st = NVFP4_ERR_CUDA;
         return cudaErrorInvalidValue;
     }
-    cudaError_t e = smallm_set_smem_attr<BN, XQ>();
+    cudaError_t e = smallm_set_smem_attr<BN, XQ, F>();
     if (e != cudaSuccess)
         return e;
     cudaLaunchConfig_t cfg{};
@@ -2197,7 +2295,7 @@ cudaError_t launch_smallm(const LinearPlan &pl, const uint8_t *w_codes, const ui
     }
     cfg.attrs = at;
     cfg.numAttrs = na;
-    return cudaLaunchKernelEx(&cfg, nvfp4_gemm_smallm_kernel<BN, XQ>, tmA, tmB, tmSFA, tmSFB,
+    return cudaLaunchKernelEx(&cfg, nvfp4_gemm_smallm_kernel<BN, XQ, F>, tmA, tmB, tmSFA, tmSFB,
                               tmY, spl);
 }
 
@@ -2287,7 +2385,10 @@ cudaError_t launch_linear_nvfp4_out(const uint8_t *a_codes, const uint8_t *a_sf,
     return launch_pair<true>(a_codes, a_sf, w_codes, w_sf, M, N, K, gp, s, st);
 }
 
-cudaError_t launch_linear(const LinearPlan &pl, const uint8_t *a_codes, const uint8_t *a_sf,
+namespace {
+
+template <class F>
+cudaError_t launch_linear_fmt(const LinearPlan &pl, const uint8_t *a_codes, const uint8_t *a_sf,
                           const float *a_gs, const uint8_t *w_codes, const uint8_t *w_sf,
                           const float *w_gs, int64_t M, int64_t N, int64_t K, int out_bf16,
                           void *y, void *ws, unsigned flags, cudaStream_t s, nvfp4_status *st)
@@ -2329,23 +2430,23 @@ cudaError_t launch_linear(const LinearPlan &pl, const uint8_t *a_codes, const ui
         sp.resident_w = (flags & NVFP4_LINEAR_RESIDENT_WEIGHTS) ? 1 : 0;
         sp.status = device_status_ptr();
         switch (pl.bn) {
-        case 8: return launch_smallm<8>(pl, ca, sa, cb, sb, K, sp, s, st);
-        case 16: return launch_smallm<16>(pl, ca, sa, cb, sb, K, sp, s, st);
-        case 32: return launch_smallm<32>(pl, ca, sa, cb, sb, K, sp, s, st);
-        case 64: return launch_smallm<64>(pl, ca, sa, cb, sb, K, sp, s, st);
-        default: return launch_smallm<128>(pl, ca, sa, cb, sb, K, sp, s, st);
+        case 8: return launch_smallm<8, false, F>(pl, ca, sa, cb, sb, K, sp, s, st);
+        case 16: return launch_smallm<16, false, F>(pl, ca, sa, cb, sb, K, sp, s, st);
+        case 32: return launch_smallm<32, false, F>(pl, ca, sa, cb, sb, K, sp, s, st);
+        case 64: return launch_smallm<64, false, F>(pl, ca, sa, cb, sb, K, sp, s, st);
+        default: return launch_smallm<128, false, F>(pl, ca, sa, cb, sb, K, sp, s, st);
         }
     }
     if (!pl.swap_ab && pl.splits == 1 && out_bf16 && N % 8 == 0 &&
         (reinterpret_cast<uintptr_t>(y) & 15u) == 0 && kUsePairKernel)
-        return launch_pair<false>(a_codes, a_sf, w_codes, w_sf, M, N, K, gp, s, st);
+        return launch_pair<false, false, F>(a_codes, a_sf, w_codes, w_sf, M, N, K, gp, s, st);
     switch (pl.bn) {
-    case 8: e = launch_bn<8>(pl, ca, sa, cb, sb, K, gp, s, st); break;
-    case 16: e = launch_bn<16>(pl, ca, sa, cb, sb, K, gp, s, st); break;
-    case 32: e = launch_bn<32>(pl, ca, sa, cb, sb, K, gp, s, st); break;
-    case 64: e = launch_bn<64>(pl, ca, sa, cb, sb, K, gp, s, st); break;
-    case 128: e = launch_bn<128>(pl, ca, sa, cb, sb, K, gp, s, st); break;
-    default: e = launch_bn<256>(pl, ca, sa, cb, sb, K, gp, s, st); break;
+    case 8: e = launch_bn<8, F>(pl, ca, sa, cb, sb, K, gp, s, st); break;
+    case 16: e = launch_bn<16, F>(pl, ca, sa, cb, sb, K, gp, s, st); break;
+    case 32: e = launch_bn<32, F>(pl, ca, sa, cb, sb, K, gp, s, st); break;
+    case 64: e = launch_bn<64, F>(pl, ca, sa, cb, sb, K, gp, s, st); break;
+    case 128: e = launch_bn<128, F>(pl, ca, sa, cb, sb, K, gp, s, st); break;
+    default: e = launch_bn<256, F>(pl, ca, sa, cb, sb, K, gp, s, st); break;
     }
     if (e != cudaSuccess || pl.splits == 1)
         return e;
@@ -2358,6 +2459,26 @@ cudaError_t launch_linear(const LinearPlan &pl, const uint8_t *a_codes, const ui
         reinterpret_cast<const float *>(ws), pl.splits, pl.rows_a, pl.rows_b, pl.tiles_a * 128,
         pl.tiles_b * pl.bn, a_gs, w_gs, y, N, out_bf16, pl.swap_ab ? 1 : 0);
     return cudaGetLastError();
+}
+
+} // namespace
+
+cudaError_t launch_linear(const LinearPlan &pl, const uint8_t *a_codes, const uint8_t *a_sf,
+                          const float *a_gs, const uint8_t *w_codes, const uint8_t *w_sf,
+                          const float *w_gs, int64_t M, int64_t N, int64_t K, int out_bf16,
+                          void *y, void *ws, unsigned flags, cudaStream_t s, nvfp4_status *st)
+{
+    return launch_linear_fmt<FmtNvfp4>(pl, a_codes, a_sf, a_gs, w_codes, w_sf, w_gs, M, N, K,
+                                       out_bf16, y, ws, flags, s, st);
+}
+
+cudaError_t launch_linear_mx(const LinearPlan &pl, const uint8_t *a_codes, const uint8_t *a_sf,
+                             const uint8_t *w_codes, const uint8_t *w_sf, int64_t M, int64_t N,
+                             int64_t K, int out_bf16, void *y, void *ws, unsigned flags,
+                             cudaStream_t s, nvfp4_status *st)
+{
+    return launch_linear_fmt<FmtMxfp4>(pl, a_codes, a_sf, nullptr, w_codes, w_sf, nullptr, M, N, K,
+                                       out_bf16, y, ws, flags, s, st);
 }
 
 // Fused dynamic-activation linear (M <= 16): the small-M plan with a cluster split whose
@@ -2429,10 +2550,14 @@ cudaError_t launch_linear_lowrank(const uint8_t *a_codes, const uint8_t *a_sf, c
                                     rank);
 }
 
-cudaError_t launch_linear_xq(const LinearPlan &pl, const void *x, int x_bf16,
-                             const uint8_t *w_codes, const uint8_t *w_sf, const float *w_gs,
-                             int64_t M, int64_t N, int64_t K, int out_bf16, void *y,
-                             float *x_gs_out, unsigned flags, cudaStream_t s, nvfp4_status *st)
+namespace {
+
+template <class F>
+cudaError_t launch_linear_xq_fmt(const LinearPlan &pl, const void *x, int x_bf16,
+                                 const uint8_t *w_codes, const uint8_t *w_sf, const float *w_gs,
+                                 int64_t M, int64_t N, int64_t K, int out_bf16, void *y,
+                                 float *x_gs_out, unsigned flags, cudaStream_t s,
+                                 nvfp4_status *st)
 {
     SmallParams sp{};
     sp.rows_a = pl.rows_a;
@@ -2452,10 +2577,30 @@ cudaError_t launch_linear_xq(const LinearPlan &pl, const void *x, int x_bf16,
     sp.x_gs_out = x_gs_out;
     (void)M;
     switch (pl.bn) {
-    case 8: return launch_smallm<8, true>(pl, w_codes, w_sf, nullptr, nullptr, K, sp, s, st);
-    case 16: return launch_smallm<16, true>(pl, w_codes, w_sf, nullptr, nullptr, K, sp, s, st);
-    default: return launch_smallm<32, true>(pl, w_codes, w_sf, nullptr, nullptr, K, sp, s, st);
+    case 8: return launch_smallm<8, true, F>(pl, w_codes, w_sf, nullptr, nullptr, K, sp, s, st);
+    case 16: return launch_smallm<16, true, F>(pl, w_codes, w_sf, nullptr, nullptr, K, sp, s, st);
+    default: return launch_smallm<32, true, F>(pl, w_codes, w_sf, nullptr, nullptr, K, sp, s, st);
     }
+}
+
+} // namespace
+
+cudaError_t launch_linear_xq(const LinearPlan &pl, const void *x, int x_bf16,
+                             const uint8_t *w_codes, const uint8_t *w_sf, const float *w_gs,
+                             int64_t M, int64_t N, int64_t K, int out_bf16, void *y,
+                             float *x_gs_out, unsigned flags, cudaStream_t s, nvfp4_status *st)
+{
+    return launch_linear_xq_fmt<FmtNvfp4>(pl, x, x_bf16, w_codes, w_sf, w_gs, M, N, K, out_bf16, y,
+                                          x_gs_out, flags, s, st);
+}
+
+cudaError_t launch_linear_xq_mx(const LinearPlan &pl, const void *x, int x_bf16,
+                                const uint8_t *w_codes, const uint8_t *w_sf, int64_t M, int64_t N,
+                                int64_t K, int out_bf16, void *y, unsigned flags, cudaStream_t s,
+                                nvfp4_status *st)
+{
+    return launch_linear_xq_fmt<FmtMxfp4>(pl, x, x_bf16, w_codes, w_sf, nullptr, M, N, K, out_bf16,
+                                          y, nullptr, flags, s, st);
 }
 
 // ---------------------------------------------------------------------------------------

@@ -1,0 +1,335 @@
+// mxfp4.cu -- MXFP4 quantize (along rows, columns or both in one read) and dequantize on sm_100a.
+//
+// The arithmetic is in mxfp4_encode.cuh. A block's scale depends on its own 32 values only, so
+// there is no tensor-wide pass: one read, one write, HBM-bound.
+//
+// Quantize: one CTA per 128 x 128 tile of x, because both outputs of such a tile are whole units
+// of the operand layout: along the rows, 128 rows x 64 code bytes and one 512-byte scale atom
+// (128 rows x 4 blocks); along the columns the same of x^T. Every atom, padding included, is
+// written by exactly one CTA, as one 512-byte run. A row's 128 values are 8 lanes x 16 bf16 (16
+// lanes x 8 fp32): two 16-byte loads a lane, the block maximum by one (two) shuffles. The column
+// side keeps the tile in shared memory; a thread takes 32 rows of two adjacent bf16 columns (of
+// one fp32 column), reading words that are contiguous across the warp, and the codes go through
+// shared memory so that they leave as whole 64-byte row pieces.
+#include "mxfp4_encode.cuh"
+#include "nvfp4_internal.cuh"
+
+namespace nvfp4 {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kTile = 128;
+constexpr int kColPitch = 80; // staged transposed codes: 64 bytes a column, conflict-free pitch
+
+struct MxQuantParams {
+    const void *x;
+    int64_t rows, cols;
+    int64_t tiles_c;      // 128-column tiles
+    int ceil_rule;
+    uint8_t *codes, *swz, *lin;       // along rows (may be null)
+    uint8_t *codes_t, *swz_t, *lin_t; // along columns
+};
+
+// The tile's 128 x 4 scale bytes (s_sf, in atom order) to the swizzled atom and the linear array
+// [rows x nblk] at rows r0.., blocks b0...
+__device__ __forceinline__ void store_scales(const uint32_t *s_sf, uint8_t *swz_atom, uint8_t *lin,
+                                             int64_t r0, int64_t rows, int64_t b0, int64_t nblk)
+{
+    const int t = threadIdx.x;
+    if (swz_atom && t < 32)
+        reinterpret_cast<uint4 *>(swz_atom)[t] = reinterpret_cast<const uint4 *>(s_sf)[t];
+    if (lin && t >= 128 && r0 + t - 128 < rows) {
+        const int r = t - 128;
+        const uint32_t w = s_sf[4 * (r & 31) + (r >> 5)];
+        uint8_t *dst = lin + (r0 + r) * nblk + b0;
+        if ((nblk & 3) == 0) {
+            *reinterpret_cast<uint32_t *>(dst) = w;
+        } else {
+#pragma unroll
+            for (int b = 0; b < 4; ++b)
+                if (b0 + b < nblk)
+                    dst[b] = (uint8_t)(w >> (8 * b));
+        }
+    }
+}
+
+template <bool BF16, bool ROWS, bool COLS>
+__global__ void __launch_bounds__(kThreads)
+    mx_quantize_kernel(const MxQuantParams p)
+{
+    constexpr int kEsz = BF16 ? 2 : 4;
+    constexpr int kLanesPerRow = BF16 ? 8 : 16;             // 32 bytes a lane
+    constexpr int kRowsPerPass = kThreads / kLanesPerRow;   // 32 or 16
+    constexpr int kPasses = kTile / kRowsPerPass;           // 4 or 8
+    constexpr int kPitch = kTile * kEsz;                    // shared tile row, bytes
+    extern __shared__ __align__(16) uint8_t dyn[];          // COLS: tile, then staged codes
+    __shared__ __align__(16) uint32_t s_sf[128];
+    __shared__ __align__(16) uint32_t s_sft[128];
+
+    const int tid = threadIdx.x;
+    const int64_t tr = blockIdx.x / p.tiles_c, tc = blockIdx.x % p.tiles_c;
+    const int64_t r0 = tr * kTile, c0 = tc * kTile;
+    const int lane_r = tid / kLanesPerRow, lane_c = tid % kLanesPerRow;
+    const int col = lane_c * (32 / kEsz); // this lane's first column of the tile
+    const bool col_ok = c0 + col < p.cols;
+
+    uint4 v[kPasses][2];
+#pragma unroll
+    for (int i = 0; i < kPasses; ++i) {
+        const int64_t r = r0 + i * kRowsPerPass + lane_r;
+        v[i][0] = v[i][1] = make_uint4(0u, 0u, 0u, 0u);
+        if (col_ok && r < p.rows) {
+            const uint4 *src = reinterpret_cast<const uint4 *>(
+                reinterpret_cast<const uint8_t *>(p.x) + (r * p.cols + c0 + col) * kEsz);
+            v[i][0] = __ldg(src);
+            v[i][1] = __ldg(src + 1);
+        }
+    }
+    if constexpr (COLS) {
+#pragma unroll
+        for (int i = 0; i < kPasses; ++i) {
+            uint4 *dst =
+                reinterpret_cast<uint4 *>(dyn + (i * kRowsPerPass + lane_r) * kPitch + lane_c * 32);
+            dst[0] = v[i][0];
+            dst[1] = v[i][1];
+        }
+    }
+    if constexpr (ROWS) {
+#pragma unroll
+        for (int i = 0; i < kPasses; ++i) {
+            const int row = i * kRowsPerPass + lane_r;
+            const uint4 a = v[i][0], b = v[i][1];
+            uint32_t m;
+            if constexpr (BF16) {
+                m = max_u16x2(max_u16x2(max_u16x2(a.x & kAbs16x2, a.y & kAbs16x2),
+                                        max_u16x2(a.z & kAbs16x2, a.w & kAbs16x2)),
+                              max_u16x2(max_u16x2(b.x & kAbs16x2, b.y & kAbs16x2),
+                                        max_u16x2(b.z & kAbs16x2, b.w & kAbs16x2)));
+                m = max_u16x2(m, __shfl_xor_sync(0xFFFFFFFFu, m, 1));
+                m = max(m & 0xFFFFu, m >> 16) << 16;
+            } else {
+                m = max(max(max(a.x & 0x7FFFFFFFu, a.y & 0x7FFFFFFFu),
+                            max(a.z & 0x7FFFFFFFu, a.w & 0x7FFFFFFFu)),
+                        max(max(b.x & 0x7FFFFFFFu, b.y & 0x7FFFFFFFu),
+                            max(b.z & 0x7FFFFFFFu, b.w & 0x7FFFFFFFu)));
+                m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 1));
+                m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 2));
+            }
+            const uint32_t sb = mx_scale_byte(m, p.ceil_rule != 0);
+            const float inv = mx_inverse(sb);
+            const bool live = col_ok && r0 + row < p.rows;
+            uint8_t *dst = p.codes + ((r0 + row) * p.cols + c0 + col) / 2;
+            if constexpr (BF16) {
+                const uint32_t lo = mx_codes_bf16x8(a.x, a.y, a.z, a.w, inv);
+                const uint32_t hi = mx_codes_bf16x8(b.x, b.y, b.z, b.w, inv);
+                if (live)
+                    *reinterpret_cast<uint2 *>(dst) =
+                        sb == kMxNan ? make_uint2(0u, 0u) : make_uint2(lo, hi);
+            } else {
+                const uint32_t w = mx_codes_f32x8(a, b, inv);
+                if (live)
+                    *reinterpret_cast<uint32_t *>(dst) = sb == kMxNan ? 0u : w;
+            }
+            // the row's four scale bytes (padding rows and blocks: 0) into the atom's word
+            constexpr int kLpb = BF16 ? 2 : 4; // lanes per block
+            uint32_t w = live ? sb << (8 * (lane_c / kLpb)) : 0u;
+            w |= __shfl_xor_sync(0xFFFFFFFFu, w, kLpb);
+            w |= __shfl_xor_sync(0xFFFFFFFFu, w, 2 * kLpb);
+            if (lane_c == 0)
+                s_sf[4 * (row & 31) + (row >> 5)] = w;
+        }
+    }
+    __syncthreads();
+    if constexpr (ROWS) {
+        const int64_t atom = tr * p.tiles_c + tc;
+        store_scales(s_sf, p.swz ? p.swz + atom * 512 : nullptr, p.lin, r0, p.rows, c0 / 32,
+                     p.cols / 32);
+    }
+    if constexpr (COLS) {
+        uint8_t *stage = dyn + kTile * kPitch;
+        uint8_t *sft = reinterpret_cast<uint8_t *>(s_sft);
+        auto put = [&](int c, int blk, const uint32_t (&w)[4], uint32_t sb) {
+            const bool nan = sb == kMxNan;
+            *reinterpret_cast<uint4 *>(stage + c * kColPitch + blk * 16) =
+                nan ? make_uint4(0u, 0u, 0u, 0u) : make_uint4(w[0], w[1], w[2], w[3]);
+            // blocks past the last row and columns past the last are padding: 0
+            const bool live = c0 + c < p.cols && r0 + blk * 32 < p.rows;
+            sft[16 * (c & 31) + 4 * (c >> 5) + blk] = live ? (uint8_t)sb : (uint8_t)0;
+        };
+        if constexpr (BF16) {
+            // 64 column pairs x 4 blocks = 256 threads
+            const int cp = tid & 63, blk = tid >> 6;
+            uint32_t u[32], m = 0u;
+#pragma unroll
+            for (int k = 0; k < 32; ++k) {
+                u[k] = *reinterpret_cast<const uint32_t *>(dyn + (blk * 32 + k) * kPitch + cp * 4);
+                m = max_u16x2(m, u[k] & kAbs16x2);
+            }
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const uint32_t sb =
+                    mx_scale_byte(h ? m & 0xFFFF0000u : m << 16, p.ceil_rule != 0);
+                const float inv = mx_inverse(sb);
+                uint32_t w[4];
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    float y[8];
+#pragma unroll
+                    for (int k = 0; k < 8; ++k)
+                        y[k] = __fmul_rn(__uint_as_float(h ? u[8 * q + k] & 0xFFFF0000u
+                                                           : u[8 * q + k] << 16),
+                                         inv);
+                    w[q] = cvt_e2m1x8(y);
+                }
+                put(2 * cp + h, blk, w, sb);
+            }
+        } else {
+#pragma unroll 1
+            for (int i = 0; i < 2; ++i) { // 128 columns x 4 blocks
+                const int c = tid & 127, blk = (tid >> 7) + 2 * i;
+                float u[32];
+                uint32_t m = 0u;
+#pragma unroll
+                for (int k = 0; k < 32; ++k) {
+                    u[k] = *reinterpret_cast<const float *>(dyn + (blk * 32 + k) * kPitch + c * 4);
+                    m = max(m, __float_as_uint(u[k]) & 0x7FFFFFFFu);
+                }
+                const uint32_t sb = mx_scale_byte(m, p.ceil_rule != 0);
+                const float inv = mx_inverse(sb);
+                uint32_t w[4];
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    float y[8];
+#pragma unroll
+                    for (int k = 0; k < 8; ++k)
+                        y[k] = __fmul_rn(u[8 * q + k], inv);
+                    w[q] = cvt_e2m1x8(y);
+                }
+                put(c, blk, w, sb);
+            }
+        }
+        __syncthreads();
+        const int64_t tiles_r = (p.rows + kTile - 1) / kTile;
+        const int64_t nblk = (p.rows + 31) / 32; // blocks of a row of x^T
+        const int64_t atom = tc * tiles_r + tr;
+        store_scales(s_sft, p.swz_t ? p.swz_t + atom * 512 : nullptr, p.lin_t, c0, p.cols,
+                     r0 / 32, nblk);
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const int idx = i * kThreads + tid, c = idx >> 2, q = idx & 3;
+            if (c0 + c < p.cols && r0 / 32 + q < nblk)
+                *reinterpret_cast<uint4 *>(p.codes_t + ((c0 + c) * nblk + r0 / 32 + q) * 16) =
+                    *reinterpret_cast<const uint4 *>(stage + c * kColPitch + q * 16);
+        }
+    }
+}
+
+template <bool BF16, bool ROWS, bool COLS>
+cudaError_t launch_mx_quantize_t(const MxQuantParams &p, unsigned grid, cudaStream_t s)
+{
+    const int smem = COLS ? kTile * kTile * (BF16 ? 2 : 4) + kTile * kColPitch : 0;
+    if (COLS && !BF16) {
+        const cudaError_t e = cudaFuncSetAttribute(mx_quantize_kernel<BF16, ROWS, COLS>,
+                                                   cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                                   smem);
+        if (e != cudaSuccess)
+            return e;
+    }
+    mx_quantize_kernel<BF16, ROWS, COLS><<<grid, kThreads, smem, s>>>(p);
+    return cudaGetLastError();
+}
+
+// ---- dequantize ----------------------------------------------------------------------
+
+// A lane decodes half a block (8 code bytes, 16 values) per step: a warp's loads are contiguous
+// (256 bytes of codes) and so are its stores (1 KB of bf16); four steps' loads in flight.
+template <bool BF16>
+__global__ void __launch_bounds__(kThreads)
+    mx_dequantize_kernel(const uint8_t *__restrict__ codes, const uint8_t *__restrict__ lin,
+                         int64_t halves, void *__restrict__ out)
+{
+    constexpr int kSteps = 4;
+    const uint2 *cb = reinterpret_cast<const uint2 *>(codes);
+    const int64_t stride = (int64_t)gridDim.x * kThreads * kSteps;
+    for (int64_t h0 = (int64_t)blockIdx.x * kThreads * kSteps + threadIdx.x; h0 < halves;
+         h0 += stride) {
+        uint2 c[kSteps];
+        uint32_t sb[kSteps];
+#pragma unroll
+        for (int i = 0; i < kSteps; ++i) {
+            const int64_t h = h0 + (int64_t)i * kThreads;
+            c[i] = h < halves ? __ldg(cb + h) : make_uint2(0u, 0u);
+            sb[i] = h < halves ? __ldg(lin + (h >> 1)) : 0u;
+        }
+#pragma unroll
+        for (int i = 0; i < kSteps; ++i) {
+            const int64_t h = h0 + (int64_t)i * kThreads;
+            if (h >= halves)
+                break;
+            const float s = mx_scale_f32(sb[i]);
+            float v[16];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const float2 e = e2m1x2_to_f32x2(((j < 4 ? c[i].x : c[i].y) >> (8 * (j & 3))) & 0xFFu);
+                v[2 * j] = __fmul_rn(e.x, s);
+                v[2 * j + 1] = __fmul_rn(e.y, s);
+            }
+            if constexpr (BF16) {
+                uint32_t w[8];
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    const __nv_bfloat162 b = __floats2bfloat162_rn(v[2 * j], v[2 * j + 1]);
+                    w[j] = *reinterpret_cast<const uint32_t *>(&b);
+                }
+                uint4 *o = reinterpret_cast<uint4 *>(out) + 2 * h;
+                o[0] = make_uint4(w[0], w[1], w[2], w[3]);
+                o[1] = make_uint4(w[4], w[5], w[6], w[7]);
+            } else {
+                float4 *o = reinterpret_cast<float4 *>(out) + 4 * h;
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    o[j] = make_float4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
+            }
+        }
+    }
+}
+
+} // namespace
+
+cudaError_t launch_quantize_mx(const void *x, int src_bf16, int64_t rows, int64_t cols,
+                               int ceil_rule, uint8_t *codes, uint8_t *swz, uint8_t *lin,
+                               uint8_t *codes_t, uint8_t *swz_t, uint8_t *lin_t, cudaStream_t s)
+{
+    if (rows == 0 || cols == 0)
+        return cudaSuccess;
+    MxQuantParams p{x, rows, cols, (cols + kTile - 1) / kTile, ceil_rule, codes, swz, lin,
+                    codes_t, swz_t, lin_t};
+    const unsigned grid = (unsigned)(((rows + kTile - 1) / kTile) * p.tiles_c);
+    if (codes && codes_t)
+        return src_bf16 ? launch_mx_quantize_t<true, true, true>(p, grid, s)
+                        : launch_mx_quantize_t<false, true, true>(p, grid, s);
+    if (codes_t)
+        return src_bf16 ? launch_mx_quantize_t<true, false, true>(p, grid, s)
+                        : launch_mx_quantize_t<false, false, true>(p, grid, s);
+    return src_bf16 ? launch_mx_quantize_t<true, true, false>(p, grid, s)
+                    : launch_mx_quantize_t<false, true, false>(p, grid, s);
+}
+
+cudaError_t launch_dequantize_mx(const uint8_t *codes, const uint8_t *lin, int64_t rows,
+                                 int64_t cols, int out_bf16, void *out, cudaStream_t s)
+{
+    const int64_t halves = rows * (cols / 16);
+    if (halves == 0)
+        return cudaSuccess;
+    int64_t g = (halves + kThreads * 4 - 1) / (kThreads * 4);
+    const int64_t cap = (int64_t)num_sms() * 8;
+    if (g > cap)
+        g = cap;
+    if (out_bf16)
+        mx_dequantize_kernel<true><<<(unsigned)g, kThreads, 0, s>>>(codes, lin, halves, out);
+    else
+        mx_dequantize_kernel<false><<<(unsigned)g, kThreads, 0, s>>>(codes, lin, halves, out);
+    return cudaGetLastError();
+}
+
+} // namespace nvfp4

@@ -113,6 +113,25 @@ cudaError_t launch_linear_xq(const LinearPlan &pl, const void *x, int x_bf16,
                              int64_t M, int64_t N, int64_t K, int out_bf16, void *y,
                              float *x_gs_out, unsigned flags, cudaStream_t s, nvfp4_status *st);
 
+// The same linear layer on MXFP4 operands (plan_linear plans both formats).
+cudaError_t launch_linear_mx(const LinearPlan &p, const uint8_t *a_codes, const uint8_t *a_sf,
+                             const uint8_t *w_codes, const uint8_t *w_sf, int64_t M, int64_t N,
+                             int64_t K, int out_bf16, void *y, void *ws, unsigned flags,
+                             cudaStream_t s, nvfp4_status *st);
+cudaError_t launch_linear_xq_mx(const LinearPlan &pl, const void *x, int x_bf16,
+                                const uint8_t *w_codes, const uint8_t *w_sf, int64_t M, int64_t N,
+                                int64_t K, int out_bf16, void *y, unsigned flags, cudaStream_t s,
+                                nvfp4_status *st);
+
+// ---- mxfp4.cu ------------------------------------------------------------------------
+// codes / swz / lin: x along its rows; *_t: x^T (its rows padded to whole blocks). Either set of
+// codes may be null (not both); the scale arrays of a set that is written may be null.
+cudaError_t launch_quantize_mx(const void *x, int src_bf16, int64_t rows, int64_t cols,
+                               int ceil_rule, uint8_t *codes, uint8_t *swz, uint8_t *lin,
+                               uint8_t *codes_t, uint8_t *swz_t, uint8_t *lin_t, cudaStream_t s);
+cudaError_t launch_dequantize_mx(const uint8_t *codes, const uint8_t *lin, int64_t rows,
+                                 int64_t cols, int out_bf16, void *out, cudaStream_t s);
+
 // ---- lowrank_sm100.cu ----------------------------------------------------------------
 // bf16 [rows x cols] row-major tensor map: box 64 columns x box_rows rows, 128B swizzle.
 bool make_bf16_kmajor_map(CUtensorMap *m, const void *base, int64_t rows, int64_t cols,
