@@ -63,7 +63,8 @@ typedef enum {
     NVFP4_OP_LINEAR_DYNAMIC = 4, /* m = M, n = N, k = K of nvfp4_linear_dynamic */
     NVFP4_OP_QUANTIZE_E4M3 = 5,  /* nvfp4_quantize_e4m3 (m, n, k ignored) */
     NVFP4_OP_LINEAR_LOWRANK = 6, /* nvfp4_linear_lowrank: m = M, n = rank (k ignored) */
-    NVFP4_OP_LINEAR_DYNAMIC_MXFP4 = 7 /* nvfp4_linear_dynamic_mxfp4: m = M, n = N, k = K */
+    NVFP4_OP_LINEAR_DYNAMIC_MXFP4 = 7, /* nvfp4_linear_dynamic_mxfp4: m = M, n = N, k = K */
+    NVFP4_OP_MOE_EXPERTS = 8     /* nvfp4_moe_experts: m = T, n = F, k = top_k */
 } nvfp4_op;
 
 /* Human-readable name of a status. Never NULL. */
@@ -420,6 +421,49 @@ nvfp4_status nvfp4_linear_dynamic_mxfp4(const void *x, nvfp4_dtype x_dt, const u
                                         const uint8_t *w_scales_swz, int64_t M, int64_t N,
                                         int64_t K, nvfp4_dtype out_dt, void *y, void *ws,
                                         size_t ws_bytes, uint32_t flags, cudaStream_t stream);
+
+/*
+ * Router of a mixture-of-experts layer: z = x . W^T + bias (x: T x H bf16, W: E x H bf16, bias:
+ * E fp32 or NULL; bf16 products summed in fp32 in groups of eight and in fp64 above), and for
+ * each token the top_k largest z in decreasing order, equal ones by the lower expert:
+ *   ids[t, s]     the expert (int32);
+ *   weights[t, s] its softmax weight (fp32): exp(z) over the sum of exp(z) of the chosen experts
+ *                 (renormalize != 0) or of all.
+ * A z of -infinity (a bias of -infinity shuts an expert off) or NaN is never chosen: where fewer
+ * than top_k experts are left, the remaining slots hold id -1 and weight 0.
+ * T: any. H: multiple of 32. E: 1..512. top_k: 1..min(E, 32). No workspace.
+ */
+nvfp4_status nvfp4_moe_route(const void *x_bf16, const void *w_bf16, const float *bias, int64_t T,
+                             int64_t H, int64_t E, int64_t top_k, int renormalize, int32_t *ids,
+                             float *weights, cudaStream_t stream);
+
+/* Format of the experts' weights in nvfp4_moe_experts (both with linear scales). */
+typedef enum { NVFP4_EXPERTS_NVFP4 = 0, NVFP4_EXPERTS_MXFP4 = 1 } nvfp4_experts_format;
+
+/*
+ * Experts of a mixture-of-experts layer for a few tokens (T <= 64):
+ *   y[t] = sum_s weights[t, s] * Wd_e . (silu(Wg_e . x[t]) * (Wu_e . x[t])),  e = ids[t, s],
+ * silu(v) = v / (1 + exp(-v)). x: T x H bf16; y: T x H bf16 (rounded once from fp32). ids, weights:
+ * T x top_k, as nvfp4_moe_route gives them or the caller's own: an id outside 0..E-1 names no
+ * expert (a token whose ids all do gets zeros), and an expert that a token names twice counts with
+ * both weights.
+ * Weights, in 4 bits with linear scales, stacked by expert: up_codes E x 2F x H/2 (rows 0..F-1 Wg,
+ * F..2F-1 Wu) with up_scales E x 2F x H/b; down_codes E x H x F/2 with down_scales E x H x F/b;
+ * b = 16 and up_gs, down_gs E fp32 global scales for NVFP4, b = 32 and NULL for MXFP4.
+ * The activations are not quantized: products of the exact 4-bit values with x to f16 precision or
+ * better (11 bits at a power-of-two scale per 32 values; bf16 x exactly down to 2^-14 of its
+ * block's largest value), fp32 sums, silu(.) * (.) rounded to 11 bits before the down product.
+ * Sums run in a fixed order: the same call gives the same bits. Two kernels; an expert that no
+ * token names is not read.
+ * H, F: multiples of 32. E: 1..512. top_k: 1..32.
+ * ws: nvfp4_workspace_bytes(NVFP4_OP_MOE_EXPERTS, T, F, top_k) bytes.
+ */
+nvfp4_status nvfp4_moe_experts(const void *x_bf16, int64_t T, int64_t H, int64_t F, int64_t E,
+                               int64_t top_k, const int32_t *ids, const float *weights, int format,
+                               const uint8_t *up_codes, const uint8_t *up_scales,
+                               const float *up_gs, const uint8_t *down_codes,
+                               const uint8_t *down_scales, const float *down_gs, void *y_bf16,
+                               void *ws, size_t ws_bytes, cudaStream_t stream);
 
 /*
  * Test of the failure-detection path. No counterpart in the paper. Launches one small kernel

@@ -14,6 +14,8 @@ device memory and the current stream, nothing else.
     y_lr = linear_lowrank(q_x, q_w, x_bf16, down, up)  # FP4 + BF16 rank-r branch
     m_x, m_xt = quantize_mxfp4(x_bf16, orient="both")  # MXFP4 along the rows and the columns
     y_mx = linear_mxfp4(m_x, m_w)             # microscaled product, no global scale
+    ids, p = moe_route(x_bf16, w_router, 4)   # mixture-of-experts layer, up to 64 tokens
+    y_moe = moe_experts(x_bf16, ids, p, gate_up, down)  # NVFP4 or MXFP4 expert weights
 
 The C entry points are also available under their own names (``nvfp4_quantize`` ...).
 """
@@ -29,7 +31,7 @@ from ._lib import (NVFP4_BF16, NVFP4_F32, NVFP4_LINEAR_DEFAULT, NVFP4_LINEAR_RES
 __all__ = ["NVFP4Tensor", "quantize", "quantize_fp8", "quantize_batch", "dequantize", "linear",
            "linear_dynamic", "linear_nvfp4_out", "linear_lowrank", "E4M3Tensor", "quantize_e4m3", "linear_e4m3",
            "MXFP4Tensor", "quantize_mxfp4", "dequantize_mxfp4", "linear_mxfp4",
-           "linear_dynamic_mxfp4",
+           "linear_dynamic_mxfp4", "ExpertWeights", "stack_experts", "moe_route", "moe_experts",
            "calib_percentile_amax", "sync_status", "free_workspaces", "load", "NVFP4Error"]
 
 
@@ -541,6 +543,114 @@ def linear_dynamic_mxfp4(x: torch.Tensor, w: MXFP4Tensor, out_dtype=torch.bfloat
                                           _ptr(w.scales_swz), M, N, K, _OUT_TYPES[out_dtype],
                                           _ptr(out), _ptr(ws), ws_bytes, flags, _stream(dev))
     check(st, "nvfp4_linear_dynamic_mxfp4")
+    return out
+
+
+@dataclass
+class ExpertWeights:
+    """The 4-bit weights [rows x cols] of E experts, stacked: codes [E, rows, cols/2] u8, linear
+    block scales [E, rows, cols/16] (NVFP4) or [E, rows, cols/32] (MXFP4) u8, and for NVFP4 the
+    global scales [E] fp32 (None: MXFP4). stack_experts() builds one from quantized matrices."""
+    codes: torch.Tensor
+    scales: torch.Tensor
+    global_scale: torch.Tensor = None
+
+
+def stack_experts(experts) -> ExpertWeights:
+    """ExpertWeights of a list of NVFP4Tensor or MXFP4Tensor matrices (one per expert, all of one
+    kind and size, quantized with linear=True)."""
+    experts = list(experts)
+    if not experts or any(type(q) is not type(experts[0]) or (q.rows, q.cols) !=
+                          (experts[0].rows, experts[0].cols) for q in experts) or \
+            not isinstance(experts[0], (NVFP4Tensor, MXFP4Tensor)):
+        raise TypeError("stack_experts expects NVFP4Tensor or MXFP4Tensor matrices of one size")
+    if any(q.scales_lin is None for q in experts):
+        raise ValueError("stack_experts needs the linear scales (quantize(..., linear=True))")
+    gs = torch.cat([q.global_scale for q in experts]) if isinstance(experts[0], NVFP4Tensor) \
+        else None
+    return ExpertWeights(torch.stack([q.codes for q in experts]),
+                         torch.stack([q.scales_lin for q in experts]), gs)
+
+
+def moe_route(x: torch.Tensor, w: torch.Tensor, top_k: int, bias: torch.Tensor = None,
+              renormalize: bool = True):
+    """Router: (ids int32 [T, top_k], weights fp32 [T, top_k]) of the top_k largest x . w^T + bias
+    of each token (equal ones: the lower expert), x [T, H] and w [E, H] bf16, bias [E] fp32. The
+    weights are the softmax over the chosen experts (renormalize) or over all. An expert whose
+    logit is -inf or NaN is never chosen; slots left over hold id -1 and weight 0."""
+    if not isinstance(x, torch.Tensor) or x.dtype != torch.bfloat16 or x.dim() != 2 or \
+            not x.is_cuda:
+        raise TypeError("moe_route expects 2-D CUDA bfloat16 activations")
+    if not isinstance(w, torch.Tensor) or w.dtype != torch.bfloat16 or w.dim() != 2:
+        raise TypeError("moe_route expects a 2-D bfloat16 router weight")
+    dev = x.device
+    x, w = x.contiguous(), w.contiguous()
+    T, H = x.shape
+    E = w.shape[0]
+    _check_arrays("moe_route", dev, w=(w, None, (E, H)), bias=(bias, torch.float32, (E,)))
+    if not 1 <= top_k <= min(E, 32):
+        raise ValueError("moe_route: top_k must be 1..min(experts, 32)")
+    ids = torch.empty((T, top_k), dtype=torch.int32, device=dev)
+    weights = torch.empty((T, top_k), dtype=torch.float32, device=dev)
+    with _on_device(dev):
+        st = load().nvfp4_moe_route(_ptr(x), _ptr(w), _ptr(bias), T, H, E, top_k,
+                                    int(renormalize), _ptr(ids), _ptr(weights), _stream(dev))
+    check(st, "nvfp4_moe_route")
+    return ids, weights
+
+
+def moe_experts(x: torch.Tensor, ids: torch.Tensor, weights: torch.Tensor,
+                gate_up: ExpertWeights, down: ExpertWeights,
+                out: torch.Tensor = None) -> torch.Tensor:
+    """Experts of a mixture-of-experts layer for up to 64 tokens, bf16 [T, H]:
+    y[t] = sum_s weights[t, s] * down_e (silu(gate_e x[t]) * (up_e x[t])), e = ids[t, s].
+
+    x [T, H] bf16; ids int32 and weights fp32 [T, k] (an id outside the experts names none);
+    gate_up: E x [2F, H] (gate rows first); down: E x [H, F]; both NVFP4 or both MXFP4."""
+    if not isinstance(x, torch.Tensor) or x.dtype != torch.bfloat16 or x.dim() != 2 or \
+            not x.is_cuda:
+        raise TypeError("moe_experts expects 2-D CUDA bfloat16 activations")
+    if not isinstance(gate_up, ExpertWeights) or not isinstance(down, ExpertWeights):
+        raise TypeError("moe_experts expects ExpertWeights")
+    if (gate_up.global_scale is None) != (down.global_scale is None):
+        raise ValueError("moe_experts: gate_up and down must have the same format")
+    dev = x.device
+    x = x.contiguous()
+    T, H = x.shape
+    if gate_up.codes.dim() != 3 or ids.dim() != 2:
+        raise ValueError("moe_experts: codes must be [experts, rows, cols / 2], ids [T, k]")
+    E, F = gate_up.codes.shape[0], gate_up.codes.shape[1] // 2
+    k = ids.shape[1]
+    if T > 64:
+        raise ValueError("moe_experts takes up to 64 tokens")
+    if H % 32 or F % 32 or H == 0 or F == 0:
+        raise ValueError("moe_experts: H and F must be multiples of 32")
+    mx = gate_up.global_scale is None
+    b = 32 if mx else 16
+    u8 = torch.uint8
+    _check_arrays("moe_experts", dev, ids=(ids, torch.int32, (T, k)),
+                  weights=(weights, torch.float32, (T, k)),
+                  gate_up_codes=(gate_up.codes, u8, (E, 2 * F, H // 2)),
+                  gate_up_scales=(gate_up.scales, u8, (E, 2 * F, H // b)),
+                  gate_up_global_scale=(gate_up.global_scale, torch.float32, (E,)),
+                  down_codes=(down.codes, u8, (E, H, F // 2)),
+                  down_scales=(down.scales, u8, (E, H, F // b)),
+                  down_global_scale=(down.global_scale, torch.float32, (E,)))
+    if out is None:
+        out = torch.empty((T, H), dtype=torch.bfloat16, device=dev)
+    else:
+        _check_arrays("moe_experts", dev, out=(out, torch.bfloat16, (T, H)))
+    L = load()
+    with _on_device(dev):
+        ws_bytes = L.nvfp4_workspace_bytes(_lib.NVFP4_OP_MOE_EXPERTS, T, F, k)
+        ws = _scratch(dev, ws_bytes)
+        st = L.nvfp4_moe_experts(_ptr(x), T, H, F, E, k, _ptr(ids), _ptr(weights),
+                                 _lib.NVFP4_EXPERTS_MXFP4 if mx else _lib.NVFP4_EXPERTS_NVFP4,
+                                 _ptr(gate_up.codes), _ptr(gate_up.scales),
+                                 _ptr(gate_up.global_scale), _ptr(down.codes), _ptr(down.scales),
+                                 _ptr(down.global_scale), _ptr(out), _ptr(ws), ws_bytes,
+                                 _stream(dev))
+    check(st, "nvfp4_moe_experts")
     return out
 
 

@@ -342,6 +342,10 @@ size_t nvfp4_workspace_bytes(int op, int64_t m, int64_t n, int64_t k)
         if (m <= 0 || n <= 0 || k <= 0)
             return 0;
         return linear_dynamic_mx_ws(m, n, k).total;
+    case NVFP4_OP_MOE_EXPERTS:
+        if (m <= 0 || m > kMoeMaxTokens || n <= 0 || n >= kMaxDim || k <= 0 || k > kMoeMaxTopK)
+            return 0;
+        return moe_workspace_bytes(m, k, n);
     case NVFP4_OP_CALIB_BF16: return calib_workspace_bytes(1);
     case NVFP4_OP_CALIB_F32: return calib_workspace_bytes(0);
     }
@@ -608,6 +612,62 @@ nvfp4_status nvfp4_linear_dynamic_mxfp4(const void *x, nvfp4_dtype x_dt, const u
         return st;
     return nvfp4_linear_mxfp4(w + d.codes, w + d.scales, w_codes, w_scales_swz, M, N, K, out_dt, y,
                               w + d.lws, ws_bytes - d.lws, flags, stream);
+}
+
+nvfp4_status nvfp4_moe_route(const void *x_bf16, const void *w_bf16, const float *bias, int64_t T,
+                             int64_t H, int64_t E, int64_t top_k, int renormalize, int32_t *ids,
+                             float *weights, cudaStream_t stream)
+{
+    if (T < 0 || T >= kMaxDim || H < 0 || H >= kMaxDim || H % 32 != 0 || E < 1 ||
+        E > kMoeMaxExperts || top_k < 1 || top_k > E || top_k > kMoeMaxTopK)
+        return NVFP4_ERR_SHAPE;
+    if (T == 0)
+        return NVFP4_OK;
+    if (!ids || !weights || (H > 0 && (!x_bf16 || !w_bf16)))
+        return NVFP4_ERR_INVALID_ARG;
+    if (!aligned16(x_bf16) || !aligned16(w_bf16) || (reinterpret_cast<uintptr_t>(bias) & 3u) ||
+        (reinterpret_cast<uintptr_t>(ids) & 3u) || (reinterpret_cast<uintptr_t>(weights) & 3u))
+        return NVFP4_ERR_ALIGNMENT;
+    const nvfp4_status st = check_device();
+    if (st != NVFP4_OK)
+        return st;
+    return map_cuda(launch_moe_route(x_bf16, w_bf16, bias, T, H, (int)E, (int)top_k,
+                                     renormalize != 0, ids, weights, stream));
+}
+
+nvfp4_status nvfp4_moe_experts(const void *x_bf16, int64_t T, int64_t H, int64_t F, int64_t E,
+                               int64_t top_k, const int32_t *ids, const float *weights, int format,
+                               const uint8_t *up_codes, const uint8_t *up_scales,
+                               const float *up_gs, const uint8_t *down_codes,
+                               const uint8_t *down_scales, const float *down_gs, void *y_bf16,
+                               void *ws, size_t ws_bytes, cudaStream_t stream)
+{
+    if (format != NVFP4_EXPERTS_NVFP4 && format != NVFP4_EXPERTS_MXFP4)
+        return NVFP4_ERR_INVALID_ARG;
+    if (T < 0 || T > kMoeMaxTokens || H < 32 || H >= kMaxDim || H % 32 != 0 || F < 32 ||
+        F >= kMaxDim / 2 || F % 32 != 0 || E < 1 || E > kMoeMaxExperts || top_k < 1 ||
+        top_k > kMoeMaxTopK)
+        return NVFP4_ERR_SHAPE;
+    if (T == 0)
+        return NVFP4_OK;
+    const bool nv = format == NVFP4_EXPERTS_NVFP4;
+    if (!x_bf16 || !ids || !weights || !up_codes || !up_scales || !down_codes || !down_scales ||
+        !y_bf16 || (nv && (!up_gs || !down_gs)))
+        return NVFP4_ERR_INVALID_ARG;
+    if (!aligned16(x_bf16) || !aligned16(up_codes) || !aligned16(up_scales) ||
+        !aligned16(down_codes) || !aligned16(down_scales) || !aligned16(y_bf16) ||
+        !aligned16(ws) || (reinterpret_cast<uintptr_t>(ids) & 3u) ||
+        (reinterpret_cast<uintptr_t>(weights) & 3u) || (reinterpret_cast<uintptr_t>(up_gs) & 3u) ||
+        (reinterpret_cast<uintptr_t>(down_gs) & 3u))
+        return NVFP4_ERR_ALIGNMENT;
+    if (!ws || ws_bytes < moe_workspace_bytes(T, top_k, F))
+        return NVFP4_ERR_WORKSPACE;
+    const nvfp4_status st = check_device();
+    if (st != NVFP4_OK)
+        return st;
+    return map_cuda(launch_moe_experts(x_bf16, T, H, F, (int)E, (int)top_k, ids, weights, !nv,
+                                       up_codes, up_scales, up_gs, down_codes, down_scales,
+                                       down_gs, y_bf16, ws, stream));
 }
 
 nvfp4_status nvfp4_calib_percentile_amax(const void *const *batches, int num_batches,

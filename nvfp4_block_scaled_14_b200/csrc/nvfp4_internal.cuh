@@ -132,6 +132,18 @@ cudaError_t launch_quantize_mx(const void *x, int src_bf16, int64_t rows, int64_
 cudaError_t launch_dequantize_mx(const uint8_t *codes, const uint8_t *lin, int64_t rows,
                                  int64_t cols, int out_bf16, void *out, cudaStream_t s);
 
+// ---- moe.cu --------------------------------------------------------------------------
+constexpr int64_t kMoeMaxTokens = 64, kMoeMaxExperts = 512, kMoeMaxTopK = 32;
+size_t moe_workspace_bytes(int64_t T, int64_t k, int64_t F);
+cudaError_t launch_moe_route(const void *x, const void *w, const float *bias, int64_t T, int64_t H,
+                             int E, int k, int renorm, int *ids, float *weights, cudaStream_t s);
+cudaError_t launch_moe_experts(const void *x, int64_t T, int64_t H, int64_t F, int E, int k,
+                               const int *ids, const float *weights, int mx,
+                               const uint8_t *up_codes, const uint8_t *up_scales,
+                               const float *up_gs, const uint8_t *down_codes,
+                               const uint8_t *down_scales, const float *down_gs, void *y, void *ws,
+                               cudaStream_t s);
+
 // ---- lowrank_sm100.cu ----------------------------------------------------------------
 // bf16 [rows x cols] row-major tensor map: box 64 columns x box_rows rows, 128B swizzle.
 bool make_bf16_kmajor_map(CUtensorMap *m, const void *base, int64_t rows, int64_t cols,
