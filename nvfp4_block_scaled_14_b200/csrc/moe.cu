@@ -178,6 +178,7 @@ struct MoeParams {
     uint4 *h;        // f16 [rows][F]: silu(gate) * up of each (expert, token) pair, scaled
     uint8_t *h_exp;  // [rows][exp_pitch]: biased exponent of each 32-block's scale
     int64_t exp_pitch;
+    int panel;       // values of a token kept in shared memory at a time (moe_up_kernel)
     __nv_bfloat16 *y; // [T x H]
 };
 
@@ -357,13 +358,23 @@ template <int I> __device__ __forceinline__ uint32_t e2m1x2_to_f16x2(uint32_t w)
     return h;
 }
 
-__device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
-                                        uint32_t a3, uint32_t b0, uint32_t b1)
+// c = A B (16 x 8, K 16), and c += A B.
+__device__ __forceinline__ void mma_f16_first(float (&c)[4], const uint32_t (&a)[4], uint32_t b0,
+                                              uint32_t b1)
+{
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, "
+                 "{%4, %5, %6, %7}, {%8, %9}, {%10, %10, %10, %10};"
+                 : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
+                 : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.0f));
+}
+
+__device__ __forceinline__ void mma_f16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0,
+                                        uint32_t b1)
 {
     asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, "
                  "{%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
                  : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-                 : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+                 : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
 __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi)
@@ -381,308 +392,397 @@ __device__ __forceinline__ uint32_t block_exponent(uint32_t m)
     return e < 1u ? 1u : e > 253u ? 253u : e;
 }
 
-// Warp-private ring of weight tiles: MT x 16 rows x 128 codes (64 bytes at an 80-byte pitch: the
-// fragment loads of eight rows x four lanes hit 32 banks) and the rows' scale bytes of the tile
-// (4 MXFP4, 8 NVFP4), fetched as the aligned words that hold them, since a row of scales may start
-// at any byte.
-template <int MT, bool NV> struct Tile {
-    static constexpr int kRows = MT * 16;
-    static constexpr int kPitch = 80;
-    static constexpr int kSlot = NV ? 16 : 8;
-    static constexpr int kScaleBytes = NV ? 8 : 4; // of one row and tile
-    static constexpr int kOffScales = kRows * kPitch;
-    static constexpr int kBytes = kOffScales + kRows * kSlot;
+// A warp's weight tile: 16 rows x 256 codes (128 bytes at a 144-byte pitch: the fragment loads of
+// eight rows x four lanes hit 32 banks) and the rows' scale bytes of the tile (8 MXFP4, 16 NVFP4),
+// fetched as the aligned words that hold them, since a row of scales may start at any byte.
+constexpr int kTileK = 256, kTileBlocks = kTileK / 32;
+
+template <bool NV> struct Tile {
+    static constexpr int kPitch = 144;
+    static constexpr int kScaleBytes = NV ? 16 : 8; // of one row and tile
+    static constexpr int kWords = kScaleBytes / 4 + 1;
+    static constexpr int kSlot = NV ? 32 : 16;
+    static constexpr int kOffScales = 16 * kPitch;
+    static constexpr int kBytes = kOffScales + 16 * kSlot;
 };
 
-// One tile's copies: local row r is row row_of(r) of the expert's matrix (K columns).
-template <int MT, bool NV, typename RowOf>
-__device__ __forceinline__ void load_tile(uint32_t dst, const uint8_t *codes, const uint8_t *scales,
-                                          int64_t K, int kt, int lane, RowOf row_of)
+// Where a lane reads its share of a warp's rows. Local rows 0..7 are rows row..row + 7 of the
+// expert's matrix, 8..15 the same `half` rows further down.
+struct TileSource {
+    const uint8_t *codes;  // row + lane / 8, at the lane's 16-byte chunk
+    const uint8_t *scales; // the expert's
+    int64_t srow;          // byte offset of row (row + lane % 8 (+ half))'s scales
+};
+
+template <bool NV>
+__device__ __forceinline__ TileSource tile_source(const uint8_t *codes, const uint8_t *scales,
+                                                  int64_t K, int64_t row, int64_t half, int lane)
 {
-    using L = Tile<MT, NV>;
-    const int nblk = (int)(K >> 5);
-#pragma unroll
-    for (int j = 0; j < MT * 2; ++j) {
-        const int r = j * 8 + (lane >> 2), c = lane & 3;
-        if (kt * 4 + c < nblk)
-            cp_async16(dst + r * L::kPitch + c * 16, codes + row_of(r) * (K >> 1) + kt * 64 + c * 16);
+    TileSource s;
+    s.codes = codes + (row + (lane >> 3)) * (K >> 1) + (lane & 7) * 16;
+    s.scales = scales;
+    s.srow = (row + (lane & 7) + ((lane & 8) ? half : 0)) * (NV ? K >> 4 : K >> 5);
+    return s;
+}
+
+// Tile kt of the K codes of each row -> shared memory (cp.async; 16-byte pieces past the row's end
+// are left out, and so are scale words that hold none of the row's bytes).
+template <bool NV>
+__device__ __forceinline__ void load_tile(uint32_t dst, const TileSource &s, int64_t K, int64_t half,
+                                          int kt, int lane)
+{
+    using L = Tile<NV>;
+    const int64_t krow = K >> 1;
+    const int c = lane & 7;
+    if (kt * kTileBlocks + c < (int)(K >> 5)) {
+        const uint8_t *src = s.codes + (int64_t)kt * (kTileK / 2);
+        const uint32_t d = dst + (lane >> 3) * L::kPitch + c * 16;
+        cp_async16(d, src);
+        cp_async16(d + 4 * L::kPitch, src + 4 * krow);
+        cp_async16(d + 8 * L::kPitch, src + half * krow);
+        cp_async16(d + 12 * L::kPitch, src + (half + 4) * krow);
     }
-    const int64_t srow = NV ? K >> 4 : K >> 5;
     const int64_t k0 = (int64_t)kt * L::kScaleBytes;
-    const int64_t left = srow - k0;
-    const int nb = left < L::kScaleBytes ? (int)left : L::kScaleBytes;
+    const int64_t left = (NV ? K >> 4 : K >> 5) - k0;
+    const int64_t off = s.srow + k0, a = off & ~(int64_t)3;
+    const int64_t end = off + (left < L::kScaleBytes ? left : L::kScaleBytes);
+    const uint32_t d = dst + L::kOffScales + (lane & 15) * L::kSlot;
 #pragma unroll
-    for (int j = 0; j < (L::kRows + 31) / 32; ++j) {
-        const int r = j * 32 + lane;
-        if (r < L::kRows) {
-            const int64_t off = row_of(r) * srow + k0;
-            const int64_t a = off & ~(int64_t)3;
-#pragma unroll
-            for (int w = 0; w < (NV ? 3 : 2); ++w)
-                if (a + 4 * w < off + nb)
-                    cp_async4(dst + L::kOffScales + r * L::kSlot + 4 * w, scales + a + 4 * w);
-        }
+    for (int w = 0; w < L::kWords; w += 2) { // lanes 16.. take the odd words
+        const int q = w + (lane >> 4);
+        if (a + 4 * q < end)
+            cp_async4(d + 4 * q, s.scales + a + 4 * q);
     }
 }
 
-// Scale bytes of local row r (whose row of scales starts at byte offset sh8 / 8 of a word):
-// MXFP4 one word, NVFP4 two.
-template <int MT, bool NV>
-__device__ __forceinline__ void tile_scales(uint32_t tile, int r, uint32_t sh8, uint32_t (&s)[NV ? 2 : 1])
+// Scale bytes of local row r as whole words; sh8: 8 x the byte in its word at which they start.
+template <bool NV>
+__device__ __forceinline__ void tile_scales(uint32_t tile, int r, uint32_t sh8, uint32_t (&s)[NV ? 4 : 2])
 {
-    using L = Tile<MT, NV>;
-    const uint32_t a = tile + L::kOffScales + r * L::kSlot;
-    const uint32_t w0 = lds32(a), w1 = lds32(a + 4);
-    s[0] = __funnelshift_r(w0, w1, sh8);
-    if constexpr (NV)
-        s[1] = __funnelshift_r(w1, lds32(a + 8), sh8);
+    const uint32_t a = tile + Tile<NV>::kOffScales + r * Tile<NV>::kSlot;
+    const uint4 w = lds128(a);
+    s[0] = __funnelshift_r(w.x, w.y, sh8);
+    s[1] = __funnelshift_r(w.y, w.z, sh8);
+    if constexpr (NV) {
+        s[2] = __funnelshift_r(w.z, w.w, sh8);
+        s[3] = __funnelshift_r(w.w, lds32(a + 16), sh8);
+    }
 }
 
-// Activations of one column tile and one 32-block as MMA B fragments: f16 pairs, and the scales of
-// this lane's two accumulator columns.
-struct BFrag {
-    uint32_t u[4];
-    float s0, s1;
-};
-
-// acc += tile x activations, over the tile's nb 32-blocks. frag(nt, b) gives the B fragments.
-template <int MT, int NT, bool NV, typename Frag>
-__device__ __forceinline__ void tile_product(float (&acc)[MT][NT][4], uint32_t tile, int nb, int lane,
-                                             const uint32_t (&sh)[MT][2], Frag frag)
+// Whether a word has a byte 0 or 255 (MXFP4 scales that are not a shifted exponent field).
+__device__ __forceinline__ bool odd_scale(uint32_t w)
 {
-    using L = Tile<MT, NV>;
+    return ((((w - 0x01010101u) & ~w) | ((~w - 0x01010101u) & w)) & 0x80808080u) != 0u;
+}
+
+// acc += tile x activations over the tile's nb 32-blocks. frag(n, b) gives the activations of
+// column tile n as MMA B fragments; colscale(n, b, j) the scale of this lane's j-th accumulator
+// column (1 where COLS is not set). SPECIAL: MXFP4 scale bytes 0 and 255 occur.
+template <int NT, bool NV, bool COLS, bool SPECIAL, typename Frag, typename ColScale>
+__device__ __forceinline__ void tile_blocks(float (&acc)[NT][4], uint32_t tile, int nb, int nt,
+                                            int lane, const uint32_t (&s0)[NV ? 4 : 2],
+                                            const uint32_t (&s1)[NV ? 4 : 2], Frag frag,
+                                            ColScale colscale)
+{
     const int g = lane >> 2, t = lane & 3;
-    uint32_t sc[MT][2][NV ? 2 : 1];
+    const uint32_t ra = tile + g * Tile<NV>::kPitch, rb = ra + 8 * Tile<NV>::kPitch;
 #pragma unroll
-    for (int m = 0; m < MT; ++m) {
-        tile_scales<MT, NV>(tile, m * 16 + g, sh[m][0], sc[m][0]);
-        tile_scales<MT, NV>(tile, m * 16 + g + 8, sh[m][1], sc[m][1]);
-    }
-#pragma unroll
-    for (int b = 0; b < 4; ++b) {
+    for (int b = 0; b < kTileBlocks; ++b) {
         if (b >= nb)
             break;
-        BFrag f[NT];
+        const uint32_t w0 = lane_codes<NV>(ra + b * 16, t), w1 = lane_codes<NV>(rb + b * 16, t);
+        // k16 step, fragment: rows g and g + 8, k indices 2t.. and 2t + 8..
+        const uint32_t a[2][4] = {{e2m1x2_to_f16x2<0>(w0), e2m1x2_to_f16x2<0>(w1),
+                                   e2m1x2_to_f16x2<1>(w0), e2m1x2_to_f16x2<1>(w1)},
+                                  {e2m1x2_to_f16x2<2>(w0), e2m1x2_to_f16x2<2>(w1),
+                                   e2m1x2_to_f16x2<3>(w0), e2m1x2_to_f16x2<3>(w1)}};
+        float f0[2], f1[2]; // block scales of rows g, g + 8 (NVFP4: of each 16-block)
+        if constexpr (NV) {
+            const float2 p0 = e4m3x2_to_f32x2(s0[b >> 1] >> (16 * (b & 1)));
+            const float2 p1 = e4m3x2_to_f32x2(s1[b >> 1] >> (16 * (b & 1)));
+            f0[0] = p0.x;
+            f0[1] = p0.y;
+            f1[0] = p1.x;
+            f1[1] = p1.y;
+        } else if constexpr (SPECIAL) {
+            f0[0] = mx_scale_f32((s0[b >> 2] >> (8 * (b & 3))) & 0xFFu);
+            f1[0] = mx_scale_f32((s1[b >> 2] >> (8 * (b & 3))) & 0xFFu);
+        } else { // the byte into bits 23..30
+            f0[0] = __uint_as_float(__byte_perm(s0[b >> 2], 0u, 0x0444u | (b & 3) << 12) >> 1);
+            f1[0] = __uint_as_float(__byte_perm(s1[b >> 2], 0u, 0x0444u | (b & 3) << 12) >> 1);
+        }
 #pragma unroll
-        for (int n = 0; n < NT; ++n)
-            f[n] = frag(n, b);
-#pragma unroll
-        for (int m = 0; m < MT; ++m) {
-            const uint32_t ra = tile + (m * 16 + g) * L::kPitch + b * 16;
-            const uint32_t rb = ra + 8 * L::kPitch;
-            const uint32_t w0 = lane_codes<NV>(ra, t), w1 = lane_codes<NV>(rb, t);
-            // k16 step, fragment: rows g and g + 8, k indices 2t.. and 2t + 8..
-            const uint32_t a[2][4] = {
-                {e2m1x2_to_f16x2<0>(w0), e2m1x2_to_f16x2<0>(w1), e2m1x2_to_f16x2<1>(w0),
-                 e2m1x2_to_f16x2<1>(w1)},
-                {e2m1x2_to_f16x2<2>(w0), e2m1x2_to_f16x2<2>(w1), e2m1x2_to_f16x2<3>(w0),
-                 e2m1x2_to_f16x2<3>(w1)}};
+        for (int n = 0; n < NT; ++n) {
+            if (n > 0 && n >= nt)
+                break;
+            const uint4 u = frag(n, b);
+            float q0 = 1.0f, q1 = 1.0f;
+            if constexpr (COLS) {
+                q0 = colscale(n, b, 0);
+                q1 = colscale(n, b, 1);
+            }
+            float c[4];
+            mma_f16_first(c, a[0], u.x, u.y);
             if constexpr (NV) {
-                const uint32_t sa = sc[m][0][b >> 1] >> (16 * (b & 1));
-                const uint32_t sb = sc[m][1][b >> 1] >> (16 * (b & 1));
-#pragma unroll
-                for (int k = 0; k < 2; ++k) {
-                    const float s0 = e4m3_to_f32(sa >> (8 * k)), s1 = e4m3_to_f32(sb >> (8 * k));
-#pragma unroll
-                    for (int n = 0; n < NT; ++n) {
-                        float c[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-                        mma_f16(c, a[k][0], a[k][1], a[k][2], a[k][3], f[n].u[2 * k],
-                                f[n].u[2 * k + 1]);
-                        acc[m][n][0] = fmaf(c[0] * f[n].s0, s0, acc[m][n][0]);
-                        acc[m][n][1] = fmaf(c[1] * f[n].s1, s0, acc[m][n][1]);
-                        acc[m][n][2] = fmaf(c[2] * f[n].s0, s1, acc[m][n][2]);
-                        acc[m][n][3] = fmaf(c[3] * f[n].s1, s1, acc[m][n][3]);
-                    }
-                }
+                float d[4];
+                mma_f16_first(d, a[1], u.z, u.w);
+                acc[n][0] = fmaf(COLS ? c[0] * q0 : c[0], f0[0], acc[n][0]);
+                acc[n][1] = fmaf(COLS ? c[1] * q1 : c[1], f0[0], acc[n][1]);
+                acc[n][2] = fmaf(COLS ? c[2] * q0 : c[2], f1[0], acc[n][2]);
+                acc[n][3] = fmaf(COLS ? c[3] * q1 : c[3], f1[0], acc[n][3]);
+                acc[n][0] = fmaf(COLS ? d[0] * q0 : d[0], f0[1], acc[n][0]);
+                acc[n][1] = fmaf(COLS ? d[1] * q1 : d[1], f0[1], acc[n][1]);
+                acc[n][2] = fmaf(COLS ? d[2] * q0 : d[2], f1[1], acc[n][2]);
+                acc[n][3] = fmaf(COLS ? d[3] * q1 : d[3], f1[1], acc[n][3]);
             } else {
-                const float s0 = mx_scale_f32((sc[m][0][0] >> (8 * b)) & 0xFFu);
-                const float s1 = mx_scale_f32((sc[m][1][0] >> (8 * b)) & 0xFFu);
-#pragma unroll
-                for (int n = 0; n < NT; ++n) {
-                    float c[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-                    mma_f16(c, a[0][0], a[0][1], a[0][2], a[0][3], f[n].u[0], f[n].u[1]);
-                    mma_f16(c, a[1][0], a[1][1], a[1][2], a[1][3], f[n].u[2], f[n].u[3]);
-                    acc[m][n][0] = fmaf(c[0] * f[n].s0, s0, acc[m][n][0]);
-                    acc[m][n][1] = fmaf(c[1] * f[n].s1, s0, acc[m][n][1]);
-                    acc[m][n][2] = fmaf(c[2] * f[n].s0, s1, acc[m][n][2]);
-                    acc[m][n][3] = fmaf(c[3] * f[n].s1, s1, acc[m][n][3]);
-                }
+                mma_f16(c, a[1], u.z, u.w);
+                acc[n][0] = fmaf(COLS ? c[0] * q0 : c[0], f0[0], acc[n][0]);
+                acc[n][1] = fmaf(COLS ? c[1] * q1 : c[1], f0[0], acc[n][1]);
+                acc[n][2] = fmaf(COLS ? c[2] * q0 : c[2], f1[0], acc[n][2]);
+                acc[n][3] = fmaf(COLS ? c[3] * q1 : c[3], f1[0], acc[n][3]);
             }
         }
     }
 }
 
-// The 8 activations (16 bits each) of lane t's k indices of block blk of a row: consecutive
-// (MXFP4), or 4 of each 16-block (NVFP4).
-template <bool NV>
-__device__ __forceinline__ uint4 load_b(const uint4 *row, int blk, int t)
+template <int NT, bool NV, bool COLS, typename Frag, typename ColScale>
+__device__ __forceinline__ void tile_product(float (&acc)[NT][4], uint32_t tile, int nb, int nt,
+                                             int lane, uint32_t sh0, uint32_t sh1, Frag frag,
+                                             ColScale colscale)
 {
-    if constexpr (NV) {
-        const uint2 *r = reinterpret_cast<const uint2 *>(row + 4 * blk);
-        const uint2 a = r[t], b = r[4 + t];
-        return make_uint4(a.x, a.y, b.x, b.y);
-    } else {
-        return row[4 * blk + t];
+    uint32_t s0[NV ? 4 : 2], s1[NV ? 4 : 2];
+    tile_scales<NV>(tile, lane >> 2, sh0, s0);
+    tile_scales<NV>(tile, (lane >> 2) + 8, sh1, s1);
+    if constexpr (!NV) {
+        if (__any_sync(0xFFFFFFFFu, odd_scale(s0[0]) || odd_scale(s0[1]) || odd_scale(s1[0]) ||
+                                        odd_scale(s1[1]))) {
+            tile_blocks<NT, NV, COLS, true>(acc, tile, nb, nt, lane, s0, s1, frag, colscale);
+            return;
+        }
     }
+    tile_blocks<NT, NV, COLS, false>(acc, tile, nb, nt, lane, s0, s1, frag, colscale);
 }
 
-constexpr int kUpWarps = 4, kUpStages = 4, kUpMt = 4;
-
-// h = silu(gate) * up for 32 columns of F (64 weight rows) of one column tile. The warps split the
-// k-tiles and their sums meet in shared memory. m-tile i holds gate rows f0 + 8i.. in its first
-// eight rows and the same up rows in the other eight, so a lane's accumulators hold both sides of
-// its products.
-template <int NT, bool NV>
-__global__ void __launch_bounds__(kUpWarps * 32, 2) moe_up_kernel(const MoeParams p)
+// Place of value v (0..31) of a 32-block in the activations' layout: each lane's 8 values are
+// consecutive (MXFP4: v itself; NVFP4: lane t takes 4t.. of both 16-blocks).
+template <bool NV> __device__ __forceinline__ int lane_order(int v)
 {
-    using L = Tile<kUpMt, NV>;
+    if constexpr (NV)
+        return (((v >> 2) & 3) * 2 + (v >> 4)) * 4 + (v & 3);
+    else
+        return v;
+}
+
+constexpr int kMaxSmem = 232448; // per CTA
+constexpr int kUpWarps = 16, kUpStages = 3, kUpGroups = kUpWarps / 4;
+constexpr int kHPitch = 36; // floats between columns of the h exchange: conflict-free
+
+// Shared memory of moe_up_kernel: rings, then h exchange, x panel, lists.
+template <int NT, bool NV> struct UpLayout {
+    static constexpr int kRing = kUpWarps * kUpStages * Tile<NV>::kBytes;
+    static constexpr int kH = 2 * kUpGroups * 8 * NT * kHPitch * 4;
+    static constexpr int kOffH = kRing;
+    static constexpr int kOffExp = kOffH + kH;
+    static constexpr int kOffX = kOffExp + 128;
+    // bytes between columns of the x panel: 64 past a multiple of 128, so that the 16-byte
+    // fragment loads of two columns x four lanes hit 32 banks
+    __host__ __device__ static int x_pitch(int panel)
+    {
+        return panel * 2 + (panel * 2 % 128 == 0 ? 64 : 0);
+    }
+};
+
+// h = silu(gate) * up. Work is cut into items of 32 columns of F of one column tile; a group of four
+// warps takes an item, a warp 8 of its columns: 8 gate rows and the same 8 up rows are its 16 MMA
+// rows, so a lane's accumulators hold both sides of its products, and a warp needs no other until
+// the block exponents of h. One CTA per SM takes a run of items; each warp's ring of weight tiles
+// runs on across them. The tokens of the column tile are kept in shared memory as f16, each
+// divided by its power of two (whole rows, or panels of them where they do not fit).
+template <int NT, bool NV>
+__global__ void __launch_bounds__(kUpWarps * 32, 1) moe_up_kernel(const MoeParams p)
+{
+    using L = Tile<NV>;
+    using U = UpLayout<NT, NV>;
     constexpr int NC = 8 * NT;
     extern __shared__ __align__(16) uint8_t smem[];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
-    uint8_t *ring = smem;
-    const MoeLists l = moe_lists(smem + kUpWarps * kUpStages * L::kBytes, p.T, p.k, p.E);
+    const int grp = warp >> 2, w4 = warp & 3;
+    const int pitch = U::x_pitch(p.panel);
+    const MoeLists l = moe_lists(smem + U::kOffX + min(NC, p.T) * pitch, p.T, p.k, p.E);
     pdl_wait();
     build_lists<false>(l, p, NC);
     pdl_launch_dependents(); // everything before this kernel is complete: see moe_down_kernel
-    if ((int)blockIdx.y >= *l.n_units)
+
+    const int nf = (int)(p.F >> 5); // items per column tile
+    const int64_t items = (int64_t)*l.n_units * nf;
+    const int i0 = (int)(items * blockIdx.x / gridDim.x);
+    const int i1 = (int)(items * (blockIdx.x + 1) / gridDim.x);
+    if (i0 >= i1)
         return;
-    const int unit = l.unit[blockIdx.y];
-    const int e = unit & 0xFFFF, c0 = unit >> 16;
-    const int row0 = l.base[e] + c0;
-    const int ncol = min(NC, mask_count(l.mask + 2 * e) - c0);
-    const int64_t f0 = (int64_t)blockIdx.x * 32;
-    const int nblk = (int)(p.H >> 5), nkt = (nblk + 3) >> 2;
-    const int64_t srow = NV ? p.H >> 4 : p.H >> 5;
-    const uint8_t *codes = p.up_codes + (int64_t)e * 2 * p.F * (p.H >> 1);
-    const uint8_t *scales = p.up_scales + (int64_t)e * 2 * p.F * srow;
-    auto row_of = [&](int r) {
-        return f0 + (r >> 4) * 8 + (r & 7) + ((r & 8) ? p.F : (int64_t)0);
+    const int nblk = (int)(p.H >> 5), nkt = (nblk + kTileBlocks - 1) / kTileBlocks;
+    const int64_t erow = NV ? p.H >> 4 : p.H >> 5;
+
+    // the tiles to load, in the order in which they are used
+    const uint32_t ring = smem_u32(smem) + warp * kUpStages * L::kBytes;
+    int lu = i0 / nf, li = i0 + grp, lkt = 0, lslot = 0;
+    bool more = true;
+    TileSource src;
+    auto seek = [&]() { // to the next item of this group, its unit's or a later one's
+        while (more && li >= min(i1, (lu + 1) * nf)) {
+            ++lu;
+            li = lu * nf + grp;
+            more = lu * nf < i1;
+        }
+        if (more) {
+            const int64_t e = l.unit[lu] & 0xFFFF;
+            src = tile_source<NV>(p.up_codes + e * 2 * p.F * (p.H >> 1),
+                                  p.up_scales + e * 2 * p.F * erow, p.H,
+                                  (int64_t)(li - lu * nf) * 32 + w4 * 8, p.F, lane);
+        }
     };
-    const uint32_t my = smem_u32(ring) + warp * kUpStages * L::kBytes;
-    const int mine = nkt > warp ? (nkt - warp + kUpWarps - 1) / kUpWarps : 0;
-    auto issue = [&](int i) {
-        if (i < mine)
-            load_tile<kUpMt, NV>(my + (i % kUpStages) * L::kBytes, codes, scales, p.H,
-                                 warp + i * kUpWarps, lane, row_of);
+    seek();
+    auto issue = [&]() {
+        if (more) {
+            load_tile<NV>(ring + lslot * L::kBytes, src, p.H, p.F, lkt, lane);
+            if (++lkt == nkt) {
+                lkt = 0;
+                li += kUpGroups;
+                seek();
+            }
+        }
         cp_async_commit();
+        lslot = lslot + 1 == kUpStages ? 0 : lslot + 1;
     };
 #pragma unroll
     for (int i = 0; i < kUpStages - 1; ++i)
-        issue(i);
-    const uint4 *xrow[NT];
+        issue();
+
+    uint8_t *sx = smem + U::kOffX;
+    uint32_t *s_ex = reinterpret_cast<uint32_t *>(smem + U::kOffExp);
+    float *s_h = reinterpret_cast<float *>(smem + U::kOffH);
+    uint32_t xaddr[NT]; // this lane's column of each column tile (past the last kept: that one)
 #pragma unroll
     for (int n = 0; n < NT; ++n)
-        xrow[n] = n * 8 + g < ncol ? p.x + (int64_t)l.tok[row0 + n * 8 + g] * (p.H >> 3) : nullptr;
-    uint4 bv[NT][4];
-    auto fetch = [&](int i) {
-        const int kt = warp + i * kUpWarps;
+        xaddr[n] = smem_u32(sx) + min(n * 8 + g, min(NC, p.T) - 1) * pitch + t * 16;
+    int slot = 0, buf = 0;
+    for (int u = i0 / nf; u * nf < i1; ++u) {
+        const int unit = l.unit[u];
+        const int e = unit & 0xFFFF, c0 = unit >> 16;
+        const int row0 = l.base[e] + c0;
+        const int ncol = min(NC, mask_count(l.mask + 2 * e) - c0);
+        const int nt = (ncol + 7) >> 3;
+        const int a = max(i0, u * nf), b = min(i1, (u + 1) * nf);
+        const float gs = NV ? __ldg(p.up_gs + e) : 1.0f;
+        for (int r = a; r < b; r += kUpGroups) {
+            const int it = r + grp;
+            const bool on = it < b;
+            const int64_t f0 = (int64_t)(it - u * nf) * 32;
+            const uint32_t sh0 = (uint32_t)(((f0 + w4 * 8 + g) * erow) & 3) * 8u;
+            const uint32_t sh1 = (uint32_t)(((p.F + f0 + w4 * 8 + g) * erow) & 3) * 8u;
+            float acc[NT][4] = {};
+            for (int k0 = 0; k0 < (int)p.H; k0 += p.panel) {
+                const int k1 = min((int)p.H, k0 + p.panel);
+                if (r == a || p.panel < (int)p.H) {
+                    __syncthreads(); // the last panel has been used
+                    for (int c = warp; c < ncol; c += kUpWarps) {
+                        const uint4 *x = p.x + (int64_t)l.tok[row0 + c] * (p.H >> 3);
+                        uint32_t m = 0u;
+#pragma unroll 4
+                        for (int i = lane; i < (int)(p.H >> 3); i += 32) {
+                            const uint4 v = __ldg(x + i);
+                            m = max_u16x2(m, max_u16x2(max_u16x2(v.x & kAbs16x2, v.y & kAbs16x2),
+                                                       max_u16x2(v.z & kAbs16x2, v.w & kAbs16x2)));
+                        }
+                        m = __reduce_max_sync(0xFFFFFFFFu, max(m & 0xFFFFu, m >> 16));
+                        const uint32_t ex = block_exponent(m << 16);
+                        const float inv = __uint_as_float((254u - ex) << 23);
+                        if (lane == 0)
+                            s_ex[c] = ex;
+#pragma unroll 4
+                        for (int i = (k0 >> 3) + lane; i < k1 >> 3; i += 32) {
+                            const uint4 v = __ldg(x + i);
+                            const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+                            uint32_t h[4];
 #pragma unroll
-        for (int n = 0; n < NT; ++n)
+                            for (int q = 0; q < 4; ++q)
+                                h[q] = pack_f16x2(__uint_as_float(w[q] << 16) * inv,
+                                                  __uint_as_float(w[q] & 0xFFFF0000u) * inv);
+                            // eight values: two groups of four at their lanes' places
+                            uint8_t *d = sx + c * pitch + ((i - (k0 >> 3)) >> 2) * 64;
+                            const int v0 = (i & 3) * 8;
+                            *reinterpret_cast<uint2 *>(d + lane_order<NV>(v0) * 2) =
+                                make_uint2(h[0], h[1]);
+                            *reinterpret_cast<uint2 *>(d + lane_order<NV>(v0 + 4) * 2) =
+                                make_uint2(h[2], h[3]);
+                        }
+                    }
+                    __syncthreads();
+                }
+                if (on) {
+                    for (int kt = k0 / kTileK; kt * kTileK < k1; ++kt) {
+                        issue();
+                        cp_async_wait<kUpStages - 1>();
+                        __syncwarp();
+                        const uint32_t xt = (kt * kTileK - k0) * 2;
+                        tile_product<NT, NV, false>(
+                            acc, ring + slot * L::kBytes, min(kTileBlocks, nblk - kt * kTileBlocks),
+                            nt, lane, sh0, sh1,
+                            [&](int n, int blk) { return lds128(xaddr[n] + xt + blk * 64); },
+                            [](int, int, int) { return 1.0f; });
+                        __syncwarp(); // the tile is read before its slot is filled again
+                        slot = slot + 1 == kUpStages ? 0 : slot + 1;
+                    }
+                }
+            }
+            if (on) {
+                float *hx = s_h + (buf * kUpGroups + grp) * NC * kHPitch;
 #pragma unroll
-            for (int b = 0; b < 4; ++b)
-                bv[n][b] = xrow[n] && i < mine && kt * 4 + b < nblk ? load_b<NV>(xrow[n], kt * 4 + b, t)
-                                                                   : make_uint4(0u, 0u, 0u, 0u);
-    };
-    fetch(0);
-    uint32_t sh[kUpMt][2];
+                for (int n = 0; n < NT; ++n)
 #pragma unroll
-    for (int m = 0; m < kUpMt; ++m) {
-        sh[m][0] = (uint32_t)((row_of(m * 16 + g) * srow) & 3) * 8u;
-        sh[m][1] = (uint32_t)((row_of(m * 16 + g + 8) * srow) & 3) * 8u;
-    }
-    float acc[kUpMt][NT][4] = {};
-    for (int i = 0; i < mine; ++i) {
-        issue(i + kUpStages - 1);
-        cp_async_wait<kUpStages - 1>();
-        __syncwarp();
-        uint4 cur[NT][4];
-#pragma unroll
-        for (int n = 0; n < NT; ++n)
-#pragma unroll
-            for (int b = 0; b < 4; ++b)
-                cur[n][b] = bv[n][b];
-        fetch(i + 1);
-        const int nb = min(4, nblk - (warp + i * kUpWarps) * 4);
-        tile_product<kUpMt, NT, NV>(
-            acc, my + (i % kUpStages) * L::kBytes, nb, lane, sh, [&](int n, int b) {
-                const uint4 v = cur[n][b];
-                uint32_t m = max_u16x2(max_u16x2(v.x & kAbs16x2, v.y & kAbs16x2),
-                                       max_u16x2(v.z & kAbs16x2, v.w & kAbs16x2));
-                m = max_u16x2(m, __shfl_xor_sync(0xFFFFFFFFu, m, 1));
-                m = max_u16x2(m, __shfl_xor_sync(0xFFFFFFFFu, m, 2));
-                const uint32_t ex = block_exponent(max(m & 0xFFFFu, m >> 16) << 16);
-                const float inv = __uint_as_float((254u - ex) << 23);
-                BFrag f;
-                const uint32_t u[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-                for (int q = 0; q < 4; ++q)
-                    f.u[q] = pack_f16x2(__uint_as_float(u[q] << 16) * inv,
-                                        __uint_as_float(u[q] & 0xFFFF0000u) * inv);
-                // this lane's accumulator columns are 2t and 2t + 1
-                f.s0 = __uint_as_float(__shfl_sync(0xFFFFFFFFu, ex, 8 * t) << 23);
-                f.s1 = __uint_as_float(__shfl_sync(0xFFFFFFFFu, ex, 8 * t + 4) << 23);
-                return f;
-            });
-        __syncwarp(); // the tile is read before its slot is filled again
+                    for (int j = 0; j < 2; ++j) {
+                        const int c = n * 8 + 2 * t + j;
+                        if (c < ncol) {
+                            const float sc = __uint_as_float(s_ex[c] << 23);
+                            const float ga = acc[n][j] * sc * gs, up = acc[n][2 + j] * sc * gs;
+                            hx[c * kHPitch + w4 * 8 + g] = ga / (1.0f + __expf(-ga)) * up;
+                        }
+                    }
+                // one barrier an item: the next item uses the other buffer
+                named_bar_sync(1 + grp, 128);
+                for (int c = w4; c < ncol; c += 4) {
+                    const float v = hx[c * kHPitch + lane];
+                    const uint32_t m =
+                        __reduce_max_sync(0xFFFFFFFFu, __float_as_uint(v) & 0x7FFFFFFFu);
+                    const uint32_t ex = block_exponent(m);
+                    const int64_t row = row0 + c;
+                    reinterpret_cast<__half *>(p.h)[row * p.F + f0 + lane_order<NV>(lane)] =
+                        __float2half_rn(v * __uint_as_float((254u - ex) << 23));
+                    if (lane == 0)
+                        p.h_exp[row * p.exp_pitch + (f0 >> 5)] = (uint8_t)ex;
+                }
+                buf ^= 1;
+            }
+        }
     }
     cp_async_wait<0>();
-    __syncthreads();
-    // sums of the warps, in warp order
-    float4 *red = reinterpret_cast<float4 *>(ring); // [warp][m][n][lane]
-#pragma unroll
-    for (int m = 0; m < kUpMt; ++m)
-#pragma unroll
-        for (int n = 0; n < NT; ++n)
-            red[((warp * kUpMt + m) * NT + n) * 32 + lane] =
-                make_float4(acc[m][n][0], acc[m][n][1], acc[m][n][2], acc[m][n][3]);
-    float *s_h = reinterpret_cast<float *>(red + kUpWarps * kUpMt * NT * 32); // [NC][32]
-    __syncthreads();
-    const float gs = NV ? __ldg(p.up_gs + e) : 1.0f;
-#pragma unroll
-    for (int n = 0; n < NT; ++n) { // warp = m-tile
-        float4 s = red[(warp * NT + n) * 32 + lane];
-#pragma unroll
-        for (int w = 1; w < kUpWarps; ++w) {
-            const float4 q = red[((w * kUpMt + warp) * NT + n) * 32 + lane];
-            s.x += q.x;
-            s.y += q.y;
-            s.z += q.z;
-            s.w += q.w;
-        }
-        auto gated = [&](float a, float b) {
-            const float ga = a * gs;
-            return ga / (1.0f + __expf(-ga)) * (b * gs);
-        };
-        s_h[(n * 8 + 2 * t) * 32 + warp * 8 + g] = gated(s.x, s.z);
-        s_h[(n * 8 + 2 * t + 1) * 32 + warp * 8 + g] = gated(s.y, s.w);
-    }
-    __syncthreads();
-    for (int c = warp; c < ncol; c += kUpWarps) {
-        const float v = s_h[c * 32 + lane];
-        const uint32_t m =
-            __reduce_max_sync(0xFFFFFFFFu, __float_as_uint(v) & 0x7FFFFFFFu);
-        const uint32_t ex = block_exponent(m);
-        const __half hv = __float2half_rn(v * __uint_as_float((254u - ex) << 23));
-        const int64_t row = row0 + c;
-        reinterpret_cast<__half *>(p.h)[row * p.F + f0 + lane] = hv;
-        if (lane == 0)
-            p.h_exp[row * p.exp_pitch + (f0 >> 5)] = (uint8_t)ex;
-    }
 }
 
-constexpr int kDownWarps = 8, kDownStages = 8;
+constexpr int kDownRowWarps = 4, kDownKWarps = 2, kDownWarps = kDownRowWarps * kDownKWarps;
+constexpr int kDownStages = 3, kDownCluster = 8, kDownRows = kDownRowWarps * 16;
 
-// y for 16 columns of H: the (column tile, k-tile) pairs of all met experts are shared out over
-// the warps in runs; a warp's sums of one column tile are weighted and added to its own
-// [16 x T] array, and the warps' arrays are added in warp order.
+// y for 64 columns of H by a cluster of 8 CTAs: each row warp takes 16 columns, and the flat list of
+// (column tile, k-tile) pairs of all met experts is cut into 16 runs, one per CTA and k-warp. A
+// warp's sums of one column tile are weighted and added to its own [16 x T] array; the arrays are
+// added over the k-warps and then over the cluster's CTAs, in order.
 template <int NT, bool NV>
-__global__ void __launch_bounds__(kDownWarps * 32) moe_down_kernel(const MoeParams p)
+__global__ void __cluster_dims__(kDownCluster, 1, 1) __launch_bounds__(kDownWarps * 32, 2)
+    moe_down_kernel(const MoeParams p)
 {
-    using L = Tile<1, NV>;
+    using L = Tile<NV>;
     constexpr int NC = 8 * NT;
     extern __shared__ __align__(16) uint8_t smem[];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
-    uint8_t *ring = smem;
+    const int rank = (int)cluster_ctarank();
     float *ysum = reinterpret_cast<float *>(smem + kDownWarps * kDownStages * L::kBytes);
     const MoeLists l = moe_lists(reinterpret_cast<uint8_t *>(ysum + kDownWarps * 16 * p.T), p.T,
                                  p.k, p.E);
@@ -692,117 +792,142 @@ __global__ void __launch_bounds__(kDownWarps * 32) moe_down_kernel(const MoePara
     // earlier work, so the ids, the weights and the experts' codes are already complete; only h
     // (and y's readers) need the wait below.
     build_lists<true>(l, p, NC);
-    const int64_t r0 = (int64_t)blockIdx.x * 16;
-    const int nblk = (int)(p.F >> 5), nkt = (nblk + 3) >> 2;
-    const int64_t srow = NV ? p.F >> 4 : p.F >> 5;
-    const int total = *l.n_units * nkt;
-    const int u0 = (int)((int64_t)total * warp / kDownWarps);
-    const int u1 = (int)((int64_t)total * (warp + 1) / kDownWarps);
-    const uint32_t my = smem_u32(ring) + warp * kDownStages * L::kBytes;
-    auto row_of = [&](int r) { return r0 + r; };
-    auto issue = [&](int u) {
-        if (u < u1) {
-            const int64_t e = l.unit[u / nkt] & 0xFFFF;
-            load_tile<1, NV>(my + ((u - u0) % kDownStages) * L::kBytes,
-                             p.down_codes + e * p.H * (p.F >> 1), p.down_scales + e * p.H * srow,
-                             p.F, u % nkt, lane, row_of);
+    const int64_t r0 = (int64_t)(blockIdx.x / kDownCluster) * kDownRows +
+                       (warp % kDownRowWarps) * 16;
+    const bool rows_on = r0 < p.H;
+    const int nblk = (int)(p.F >> 5), nkt = (nblk + kTileBlocks - 1) / kTileBlocks;
+    const int64_t erow = NV ? p.F >> 4 : p.F >> 5;
+    const int64_t total = rows_on ? (int64_t)*l.n_units * nkt : 0;
+    const int run = rank * kDownKWarps + warp / kDownRowWarps;
+    const int u0 = (int)(total * run / (kDownCluster * kDownKWarps));
+    const int u1 = (int)(total * (run + 1) / (kDownCluster * kDownKWarps));
+
+    const uint32_t ring = smem_u32(smem) + warp * kDownStages * L::kBytes;
+    int lu = u0 / nkt, lkt = u0 % nkt, left = u1 - u0, lslot = 0;
+    TileSource src;
+    auto seek = [&]() {
+        const int64_t e = l.unit[lu] & 0xFFFF;
+        src = tile_source<NV>(p.down_codes + e * p.H * (p.F >> 1), p.down_scales + e * p.H * erow,
+                              p.F, r0, 8, lane);
+    };
+    if (left > 0)
+        seek();
+    auto issue = [&]() {
+        if (left > 0) {
+            load_tile<NV>(ring + lslot * L::kBytes, src, p.F, 8, lkt, lane);
+            --left;
+            if (++lkt == nkt) {
+                lkt = 0;
+                ++lu;
+                if (left > 0)
+                    seek();
+            }
         }
         cp_async_commit();
+        lslot = lslot + 1 == kDownStages ? 0 : lslot + 1;
     };
 #pragma unroll
     for (int i = 0; i < kDownStages - 1; ++i)
-        issue(u0 + i);
+        issue();
     pdl_wait(); // h
-    uint4 bv[NT][4];
-    uint32_t ev[NT][2]; // exponents of this lane's accumulator columns, one byte per block
-    auto fetch = [&](int u) {
-        const bool on = u < u1;
-        const int unit = on ? l.unit[u / nkt] : 0, kt = on ? u % nkt : 0;
+
+    const uint32_t sh0 = (uint32_t)(((r0 + g) * erow) & 3) * 8u;
+    const uint32_t sh1 = (uint32_t)(((r0 + g + 8) * erow) & 3) * 8u;
+    float acc[NT][4] = {};
+    float *mysum = ysum + warp * 16 * p.T;
+    int slot = 0;
+    for (int u = u0 / nkt, kt = u0 % nkt, n_left = u1 - u0; n_left > 0; ++u, kt = 0) {
+        const int unit = l.unit[u];
         const int e = unit & 0xFFFF, c0 = unit >> 16;
         const int row = l.base[e] + c0;
-        const int ncol = on ? min(NC, mask_count(l.mask + 2 * e) - c0) : 0;
+        const int ncol = min(NC, mask_count(l.mask + 2 * e) - c0);
+        const int nt = (ncol + 7) >> 3;
+        const int kend = min(nkt, kt + n_left);
+        n_left -= kend - kt;
+        const uint4 *hp[NT];
+        const uint8_t *ep[NT][2];
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
-            const uint4 *hr = p.h + (int64_t)(row + n * 8 + g) * (p.F >> 3);
+            const int64_t r = row + min(n * 8 + g, ncol - 1); // dead columns read a live one's
+            hp[n] = p.h + r * (p.F >> 3) + t;
 #pragma unroll
-            for (int b = 0; b < 4; ++b)
-                bv[n][b] = n * 8 + g < ncol && kt * 4 + b < nblk ? load_b<NV>(hr, kt * 4 + b, t)
-                                                                : make_uint4(0u, 0u, 0u, 0u);
+            for (int j = 0; j < 2; ++j)
+                ep[n][j] = p.h_exp + (int64_t)(row + min(n * 8 + 2 * t + j, ncol - 1)) * p.exp_pitch;
+        }
+        for (; kt < kend; ++kt) {
+            issue();
+            uint4 hv[NT][kTileBlocks];
+            uint2 ev[NT][2];
+            const int nb = min(kTileBlocks, nblk - kt * kTileBlocks);
+#pragma unroll
+            for (int n = 0; n < NT; ++n) {
+                if (n > 0 && n >= nt)
+                    break;
+#pragma unroll
+                for (int b = 0; b < kTileBlocks; ++b)
+                    if (b < nb)
+                        hv[n][b] = hp[n][(kt * kTileBlocks + b) * 4];
+#pragma unroll
+                for (int j = 0; j < 2; ++j)
+                    ev[n][j] = *reinterpret_cast<const uint2 *>(ep[n][j] + kt * kTileBlocks);
+            }
+            cp_async_wait<kDownStages - 1>();
+            __syncwarp();
+            tile_product<NT, NV, true>(
+                acc, ring + slot * L::kBytes, nb, nt, lane, sh0, sh1,
+                [&](int n, int b) { return hv[n][b]; },
+                [&](int n, int b, int j) {
+                    return __uint_as_float(
+                        __byte_perm(b < 4 ? ev[n][j].x : ev[n][j].y, 0u, 0x0444u | (b & 3) << 12) >>
+                        1);
+                });
+            __syncwarp();
+            slot = slot + 1 == kDownStages ? 0 : slot + 1;
+        }
+        // the column tile's sums of this run
+        const float gs = NV ? __ldg(p.down_gs + e) : 1.0f;
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
                 const int c = n * 8 + 2 * t + j;
-                ev[n][j] = c < ncol ? *reinterpret_cast<const uint32_t *>(
-                                          p.h_exp + (int64_t)(row + c) * p.exp_pitch + kt * 4)
-                                    : 0u;
-            }
-        }
-    };
-    fetch(u0);
-    uint32_t sh[1][2];
-    sh[0][0] = (uint32_t)(((r0 + g) * srow) & 3) * 8u;
-    sh[0][1] = (uint32_t)(((r0 + g + 8) * srow) & 3) * 8u;
-    float acc[1][NT][4] = {};
-    float *mysum = ysum + warp * 16 * p.T;
-    for (int u = u0; u < u1; ++u) {
-        issue(u + kDownStages - 1);
-        cp_async_wait<kDownStages - 1>();
-        __syncwarp();
-        uint4 cur[NT][4];
-        uint32_t ec[NT][2];
-#pragma unroll
-        for (int n = 0; n < NT; ++n) {
-#pragma unroll
-            for (int b = 0; b < 4; ++b)
-                cur[n][b] = bv[n][b];
-            ec[n][0] = ev[n][0];
-            ec[n][1] = ev[n][1];
-        }
-        fetch(u + 1);
-        const int kt = u % nkt;
-        tile_product<1, NT, NV>(acc, my + ((u - u0) % kDownStages) * L::kBytes,
-                                min(4, nblk - kt * 4), lane, sh, [&](int n, int b) {
-                                    BFrag f;
-                                    f.u[0] = cur[n][b].x;
-                                    f.u[1] = cur[n][b].y;
-                                    f.u[2] = cur[n][b].z;
-                                    f.u[3] = cur[n][b].w;
-                                    f.s0 = __uint_as_float(((ec[n][0] >> (8 * b)) & 0xFFu) << 23);
-                                    f.s1 = __uint_as_float(((ec[n][1] >> (8 * b)) & 0xFFu) << 23);
-                                    return f;
-                                });
-        if (kt == nkt - 1 || u == u1 - 1) { // the column tile's last k-tile of this warp
-            const int unit = l.unit[u / nkt];
-            const int e = unit & 0xFFFF, c0 = unit >> 16;
-            const int row = l.base[e] + c0;
-            const int ncol = min(NC, mask_count(l.mask + 2 * e) - c0);
-            const float gs = NV ? __ldg(p.down_gs + e) : 1.0f;
-#pragma unroll
-            for (int n = 0; n < NT; ++n)
-#pragma unroll
-                for (int j = 0; j < 2; ++j) {
-                    const int c = n * 8 + 2 * t + j;
-                    if (c < ncol) {
-                        const float w = l.wt[row + c];
-                        const int tok = l.tok[row + c];
-                        mysum[g * p.T + tok] = fmaf(acc[0][n][j] * gs, w, mysum[g * p.T + tok]);
-                        mysum[(g + 8) * p.T + tok] =
-                            fmaf(acc[0][n][2 + j] * gs, w, mysum[(g + 8) * p.T + tok]);
-                    }
-                    acc[0][n][j] = acc[0][n][2 + j] = 0.0f;
+                if (c < ncol) {
+                    const float w = l.wt[row + c];
+                    const int tok = l.tok[row + c];
+                    mysum[g * p.T + tok] = fmaf(acc[n][j] * gs, w, mysum[g * p.T + tok]);
+                    mysum[(g + 8) * p.T + tok] =
+                        fmaf(acc[n][2 + j] * gs, w, mysum[(g + 8) * p.T + tok]);
                 }
-        }
-        __syncwarp();
+                acc[n][j] = acc[n][2 + j] = 0.0f;
+            }
+        __syncwarp(); // the next tile's columns may be other lanes' tokens
     }
     cp_async_wait<0>();
     __syncthreads();
-    for (int i = tid; i < 16 * p.T; i += kDownWarps * 32) {
-        const int r = i & 15, tk = i >> 4;
+    // the k-warps' arrays into the first ones: [64 rows x T]
+    for (int i = tid; i < kDownRows * p.T; i += kDownWarps * 32) {
+        float s = ysum[i];
+#pragma unroll
+        for (int w = 1; w < kDownKWarps; ++w)
+            s += ysum[w * kDownRows * p.T + i];
+        ysum[i] = s;
+    }
+    cluster_sync();
+    // this CTA's eight rows over the cluster, then y
+    constexpr int kOwn = kDownRows / kDownCluster;
+    const uint32_t yaddr = smem_u32(ysum);
+    for (int i = tid; i < kOwn * p.T; i += kDownWarps * 32) {
+        const int r = rank * kOwn + i % kOwn, tk = i / kOwn;
+        const int64_t col = (int64_t)(blockIdx.x / kDownCluster) * kDownRows + r;
         float s = 0.0f;
 #pragma unroll
-        for (int w = 0; w < kDownWarps; ++w)
-            s += ysum[(w * 16 + r) * p.T + tk];
-        p.y[tk * p.H + r0 + r] = __float2bfloat16_rn(s);
+        for (int c = 0; c < kDownCluster; ++c)
+            s += ld_shared_cluster_f32(mapa_shared(yaddr + 4u * (uint32_t)(r * p.T + tk), c));
+        if (col < p.H)
+            p.y[tk * p.H + col] = __float2bfloat16_rn(s);
     }
+    __syncwarp();
+    cluster_sync(); // no CTA leaves while another reads its sums
 }
 
 template <typename K>
@@ -826,22 +951,21 @@ cudaError_t launch_pdl(K kernel, dim3 grid, int threads, size_t smem, cudaStream
     return cudaLaunchKernelEx(&cfg, kernel, p);
 }
 
-template <int NT, bool NV> cudaError_t launch_experts(const MoeParams &p, cudaStream_t s)
+template <int NT, bool NV> cudaError_t launch_experts(MoeParams p, cudaStream_t s)
 {
-    const size_t lists = moe_lists_bytes(p.T, p.k, p.E);
-    // column tiles there can be at most: one per (token, expert) pair, and per expert the pairs
-    // it may have beyond whole tiles
-    const int n = p.T * p.k;
-    const int units = n < p.E ? n : p.E + n / (8 * NT);
-    cudaError_t e = launch_pdl(moe_up_kernel<NT, NV>,
-                               dim3((unsigned)(p.F / 32), (unsigned)(units < n ? units : n), 1),
-                               kUpWarps * 32,
-                               kUpWarps * kUpStages * Tile<kUpMt, NV>::kBytes + lists, s, p);
+    using U = UpLayout<NT, NV>;
+    const int lists = (int)moe_lists_bytes(p.T, p.k, p.E);
+    const int cols = p.T < 8 * NT ? p.T : 8 * NT;
+    // the x panel: all of H where it fits beside the rings
+    const int room = (kMaxSmem - U::kOffX - lists) / cols;
+    p.panel = U::x_pitch((int)p.H) <= room ? (int)p.H : (room - 64) / 2 / kTileK * kTileK;
+    cudaError_t e = launch_pdl(moe_up_kernel<NT, NV>, dim3((unsigned)num_sms(), 1, 1),
+                               kUpWarps * 32, U::kOffX + cols * U::x_pitch(p.panel) + lists, s, p);
     if (e != cudaSuccess)
         return e;
-    return launch_pdl(moe_down_kernel<NT, NV>, dim3((unsigned)(p.H / 16), 1, 1), kDownWarps * 32,
-                      kDownWarps * kDownStages * Tile<1, NV>::kBytes +
-                          (size_t)kDownWarps * 16 * p.T * 4 + lists,
+    const unsigned groups = (unsigned)((p.H + kDownRows - 1) / kDownRows);
+    return launch_pdl(moe_down_kernel<NT, NV>, dim3(groups * kDownCluster, 1, 1), kDownWarps * 32,
+                      (size_t)kDownWarps * (kDownStages * Tile<NV>::kBytes + 16 * p.T * 4) + lists,
                       s, p);
 }
 
@@ -851,7 +975,7 @@ size_t moe_workspace_bytes(int64_t T, int64_t k, int64_t F)
 {
     const size_t rows = (size_t)T * (size_t)k;
     const size_t h = (rows * (size_t)F * 2 + 255) & ~(size_t)255;
-    return h + rows * (size_t)((F / 32 + 3) / 4 * 4);
+    return h + rows * (size_t)((F / 32 + 7) / 8 * 8);
 }
 
 cudaError_t launch_moe_route(const void *x, const void *w, const float *bias, int64_t T, int64_t H,
@@ -901,10 +1025,10 @@ cudaError_t launch_moe_experts(const void *x, int64_t T, int64_t H, int64_t F, i
     p.down_gs = down_gs;
     p.h = reinterpret_cast<uint4 *>(ws);
     p.h_exp = reinterpret_cast<uint8_t *>(ws) + (((size_t)T * k * F * 2 + 255) & ~(size_t)255);
-    p.exp_pitch = (F / 32 + 3) / 4 * 4;
+    p.exp_pitch = (F / 32 + 7) / 8 * 8;
     p.y = reinterpret_cast<__nv_bfloat16 *>(y);
-    // one column tile of 8 tokens per expert, two where an expert meets more than that on average
-    const bool wide = T * k > 8 * (int64_t)E;
+    // one column tile of 8 tokens per expert, two where an expert may well meet more than that
+    const bool wide = T > 8 && T * k > 4 * (int64_t)E;
     if (mx)
         return wide ? launch_experts<2, false>(p, s) : launch_experts<1, false>(p, s);
     return wide ? launch_experts<2, true>(p, s) : launch_experts<1, true>(p, s);
