@@ -63,8 +63,7 @@ typedef enum {
     NVFP4_OP_LINEAR_DYNAMIC = 4, /* m = M, n = N, k = K of nvfp4_linear_dynamic */
     NVFP4_OP_QUANTIZE_E4M3 = 5,  /* nvfp4_quantize_e4m3 (m, n, k ignored) */
     NVFP4_OP_LINEAR_LOWRANK = 6, /* nvfp4_linear_lowrank: m = M, n = rank (k ignored) */
-    NVFP4_OP_LINEAR_DYNAMIC_MXFP4 = 7, /* nvfp4_linear_dynamic_mxfp4: m = M, n = N, k = K */
-    NVFP4_OP_MOE_EXPERTS = 8     /* nvfp4_moe_experts: m = T, n = F, k = top_k */
+    NVFP4_OP_LINEAR_DYNAMIC_MXFP4 = 7 /* nvfp4_linear_dynamic_mxfp4: m = M, n = N, k = K */
 } nvfp4_op;
 
 /* Human-readable name of a status. Never NULL. */
@@ -453,11 +452,13 @@ typedef enum { NVFP4_EXPERTS_NVFP4 = 0, NVFP4_EXPERTS_MXFP4 = 1 } nvfp4_experts_
  * The activations are not quantized: products of the exact 4-bit values with x to f16 precision or
  * better (11 bits at a power-of-two scale per 32 values; bf16 x exactly down to 2^-14 of its
  * block's largest value), fp32 sums, silu(.) * (.) rounded to 11 bits before the down product.
- * Sums run in a fixed order: the same call gives the same bits. Two kernels; an expert that no
- * token names is not read.
+ * Sums run in a fixed order: the same call gives the same bits. One cooperative kernel with a
+ * bounded grid barrier of the library's (as the single-pass quantizers); an expert that no token
+ * names is not read.
  * H, F: multiples of 32. E: 1..512. top_k: 1..32.
- * ws: nvfp4_workspace_bytes(NVFP4_OP_MOE_EXPERTS, T, F, top_k) bytes.
+ * ws: nvfp4_moe_workspace_bytes(T, H, F, top_k) bytes (any contents).
  */
+size_t nvfp4_moe_workspace_bytes(int64_t T, int64_t H, int64_t F, int64_t top_k);
 nvfp4_status nvfp4_moe_experts(const void *x_bf16, int64_t T, int64_t H, int64_t F, int64_t E,
                                int64_t top_k, const int32_t *ids, const float *weights, int format,
                                const uint8_t *up_codes, const uint8_t *up_scales,

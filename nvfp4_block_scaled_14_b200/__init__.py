@@ -642,7 +642,7 @@ def moe_experts(x: torch.Tensor, ids: torch.Tensor, weights: torch.Tensor,
         _check_arrays("moe_experts", dev, out=(out, torch.bfloat16, (T, H)))
     L = load()
     with _on_device(dev):
-        ws_bytes = L.nvfp4_workspace_bytes(_lib.NVFP4_OP_MOE_EXPERTS, T, F, k)
+        ws_bytes = L.nvfp4_moe_workspace_bytes(T, H, F, k)
         ws = _scratch(dev, ws_bytes)
         st = L.nvfp4_moe_experts(_ptr(x), T, H, F, E, k, _ptr(ids), _ptr(weights),
                                  _lib.NVFP4_EXPERTS_MXFP4 if mx else _lib.NVFP4_EXPERTS_NVFP4,

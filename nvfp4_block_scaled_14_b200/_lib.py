@@ -34,7 +34,6 @@ NVFP4_OP_LINEAR_DYNAMIC = 4
 NVFP4_OP_QUANTIZE_E4M3 = 5
 NVFP4_OP_LINEAR_LOWRANK = 6
 NVFP4_OP_LINEAR_DYNAMIC_MXFP4 = 7
-NVFP4_OP_MOE_EXPERTS = 8
 NVFP4_EXPERTS_NVFP4 = 0
 NVFP4_EXPERTS_MXFP4 = 1
 NVFP4_MX_SCALE_FLOOR = 0
@@ -100,6 +99,7 @@ _SIGNATURES = {
     "nvfp4_linear_dynamic_mxfp4": ([_vp, _int, _vp, _vp, _i64, _i64, _i64, _int, _vp, _vp, _sz,
                                     _u32, _vp], _int),
     "nvfp4_moe_route": ([_vp, _vp, _vp, _i64, _i64, _i64, _i64, _int, _vp, _vp, _vp], _int),
+    "nvfp4_moe_workspace_bytes": ([_i64, _i64, _i64, _i64], _sz),
     "nvfp4_moe_experts": ([_vp, _i64, _i64, _i64, _i64, _i64, _vp, _vp, _int, _vp, _vp, _vp, _vp,
                            _vp, _vp, _vp, _vp, _sz, _vp], _int),
     "nvfp4_selftest_wait_timeout": ([_vp], _int),

@@ -342,10 +342,6 @@ size_t nvfp4_workspace_bytes(int op, int64_t m, int64_t n, int64_t k)
         if (m <= 0 || n <= 0 || k <= 0)
             return 0;
         return linear_dynamic_mx_ws(m, n, k).total;
-    case NVFP4_OP_MOE_EXPERTS:
-        if (m <= 0 || m > kMoeMaxTokens || n <= 0 || n >= kMaxDim || k <= 0 || k > kMoeMaxTopK)
-            return 0;
-        return moe_workspace_bytes(m, k, n);
     case NVFP4_OP_CALIB_BF16: return calib_workspace_bytes(1);
     case NVFP4_OP_CALIB_F32: return calib_workspace_bytes(0);
     }
@@ -635,6 +631,14 @@ nvfp4_status nvfp4_moe_route(const void *x_bf16, const void *w_bf16, const float
                                      renormalize != 0, ids, weights, stream));
 }
 
+size_t nvfp4_moe_workspace_bytes(int64_t T, int64_t H, int64_t F, int64_t top_k)
+{
+    if (T <= 0 || T > kMoeMaxTokens || H <= 0 || H >= kMaxDim || F <= 0 || F >= kMaxDim / 2 ||
+        top_k <= 0 || top_k > kMoeMaxTopK)
+        return 0;
+    return moe_workspace_bytes(T, top_k, F, H);
+}
+
 nvfp4_status nvfp4_moe_experts(const void *x_bf16, int64_t T, int64_t H, int64_t F, int64_t E,
                                int64_t top_k, const int32_t *ids, const float *weights, int format,
                                const uint8_t *up_codes, const uint8_t *up_scales,
@@ -660,7 +664,7 @@ nvfp4_status nvfp4_moe_experts(const void *x_bf16, int64_t T, int64_t H, int64_t
         (reinterpret_cast<uintptr_t>(weights) & 3u) || (reinterpret_cast<uintptr_t>(up_gs) & 3u) ||
         (reinterpret_cast<uintptr_t>(down_gs) & 3u))
         return NVFP4_ERR_ALIGNMENT;
-    if (!ws || ws_bytes < moe_workspace_bytes(T, top_k, F))
+    if (!ws || ws_bytes < moe_workspace_bytes(T, top_k, F, H))
         return NVFP4_ERR_WORKSPACE;
     const nvfp4_status st = check_device();
     if (st != NVFP4_OK)

@@ -19,6 +19,9 @@
 // A k order that suits the loads: an MMA sums 16 products whatever their order, so lane t of a
 // quad takes 4 consecutive code bytes of a 32-code block (8 values, MXFP4; 2 + 2 bytes of the two
 // 16-code blocks, NVFP4) as its k indices, and the same 8 activations, 16 bytes, of its column.
+#include <mutex>
+
+#include "grid_exchange.cuh"
 #include "mxfp4_encode.cuh"
 #include "nvfp4_internal.cuh"
 #include "sm100_ptx.cuh"
@@ -178,8 +181,13 @@ struct MoeParams {
     uint4 *h;        // f16 [rows][F]: silu(gate) * up of each (expert, token) pair, scaled
     uint8_t *h_exp;  // [rows][exp_pitch]: biased exponent of each 32-block's scale
     int64_t exp_pitch;
-    int panel;       // values of a token kept in shared memory at a time (moe_up_kernel)
     __nv_bfloat16 *y; // [T x H]
+    int panel;        // values of a token kept in shared memory at a time
+    int splits;       // CTAs that share a 64-column block of y
+    float *partial;   // [64-column blocks][splits][T][64] sums of each (splits > 1)
+    int *arrived;     // [64-column blocks] CTAs whose sums are in place
+    GridBarrier *barrier;
+    int *status;
 };
 
 // What the ids say, in shared memory: for each expert the set of its tokens; the (expert, token)
@@ -189,17 +197,17 @@ struct MoeParams {
 struct MoeLists {
     uint32_t *mask;   // [E][2]
     int *base;        // [E] first row of each expert
-    int *unit;        // [tiles] expert | first column of the tile << 16
-    uint8_t *tok;     // [rows]
     float *wt;        // [rows]
-    int *ids;         // [T k]
     int *n_units;
+    uint16_t *unit;   // [tiles] expert | first column of the tile << 9
+    int16_t *ids;     // [T k], -1: no expert
+    uint8_t *tok;     // [rows]
 };
 
 __host__ __device__ inline size_t moe_lists_bytes(int T, int k, int E)
 {
     const size_t n = (size_t)T * k;
-    return 8 * (size_t)E + 4 * (size_t)E + 4 * n + 4 * n + 4 * n + 16 + (n + 15) / 16 * 16;
+    return (12 * (size_t)E + 9 * n + 4 + 15) / 16 * 16;
 }
 
 __device__ __forceinline__ MoeLists moe_lists(uint8_t *s, int T, int k, int E)
@@ -208,11 +216,11 @@ __device__ __forceinline__ MoeLists moe_lists(uint8_t *s, int T, int k, int E)
     MoeLists l;
     l.mask = reinterpret_cast<uint32_t *>(s);
     l.base = reinterpret_cast<int *>(l.mask + 2 * E);
-    l.unit = l.base + E;
-    l.wt = reinterpret_cast<float *>(l.unit + n);
-    l.ids = reinterpret_cast<int *>(l.wt + n);
-    l.n_units = l.ids + n;
-    l.tok = reinterpret_cast<uint8_t *>(l.n_units + 4);
+    l.wt = reinterpret_cast<float *>(l.base + E);
+    l.n_units = reinterpret_cast<int *>(l.wt + n);
+    l.unit = reinterpret_cast<uint16_t *>(l.n_units + 1);
+    l.ids = reinterpret_cast<int16_t *>(l.unit + n);
+    l.tok = reinterpret_cast<uint8_t *>(l.ids + n);
     return l;
 }
 
@@ -225,7 +233,9 @@ __device__ __forceinline__ int mask_before(const uint32_t *m, int t)
                   : __popc(m[0]) + __popc(m[1] & ((1u << (t - 32)) - 1u));
 }
 
-template <bool WEIGHTS>
+__device__ __forceinline__ int unit_expert(uint32_t u) { return (int)(u & 0x1FFu); }
+__device__ __forceinline__ int unit_column(uint32_t u) { return (int)(u >> 9); }
+
 __device__ __forceinline__ void build_lists(const MoeLists &l, const MoeParams &p, int cols)
 {
     const int tid = threadIdx.x, nthr = blockDim.x, n = p.T * p.k;
@@ -234,8 +244,9 @@ __device__ __forceinline__ void build_lists(const MoeLists &l, const MoeParams &
     __syncthreads();
     for (int i = tid; i < n; i += nthr) {
         const int e = __ldg(p.ids + i), t = i / p.k;
-        l.ids[i] = e;
-        if (e >= 0 && e < p.E)
+        const bool on = e >= 0 && e < p.E;
+        l.ids[i] = on ? (int16_t)e : (int16_t)-1;
+        if (on)
             atomicOr(&l.mask[2 * e + (t >> 5)], 1u << (t & 31));
     }
     __syncthreads();
@@ -269,28 +280,26 @@ __device__ __forceinline__ void build_lists(const MoeLists &l, const MoeParams &
             const int c = mask_count(l.mask + 2 * e);
             l.base[e] = r0;
             for (int c0 = 0; c0 < c; c0 += cols)
-                l.unit[u0++] = e | c0 << 16;
+                l.unit[u0++] = (uint16_t)(e | c0 << 9);
             r0 += c;
         }
     }
     __syncthreads();
     for (int i = tid; i < n; i += nthr) {
         const int e = l.ids[i], t = i / p.k;
-        if (e < 0 || e >= p.E)
+        if (e < 0)
             continue;
         bool first = true; // of the token's slots that name e
         float w = 0.0f;
         for (int s = t * p.k; s < (t + 1) * p.k; ++s)
             if (l.ids[s] == e) {
                 first = first && s >= i;
-                if (WEIGHTS)
-                    w += __ldg(p.weights + s);
+                w += __ldg(p.weights + s);
             }
         if (first) {
             const int row = l.base[e] + mask_before(l.mask + 2 * e, t);
             l.tok[row] = (uint8_t)t;
-            if (WEIGHTS)
-                l.wt[row] = w;
+            l.wt[row] = w;
         }
     }
     __syncthreads();
@@ -320,23 +329,15 @@ template <int N> __device__ __forceinline__ void cp_async_wait()
     asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
-__device__ __forceinline__ uint32_t lds32(uint32_t a)
-{
-    uint32_t v;
-    asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(a));
-    return v;
-}
-
 // Lane t's four code bytes of the 32-code block at `a`: bytes 4t.. (MXFP4), or bytes 2t, 2t + 1 of
 // each of its two 16-code blocks (NVFP4).
-template <bool NV> __device__ __forceinline__ uint32_t lane_codes(uint32_t a, int t)
+template <bool NV> __device__ __forceinline__ uint32_t lane_codes(const uint8_t *a, int t)
 {
-    if constexpr (NV) {
-        const uint32_t h = a + 4 * (t >> 1);
-        return __byte_perm(lds32(h), lds32(h + 8), (t & 1) ? 0x7632 : 0x5410);
-    } else {
-        return lds32(a + 4 * t);
-    }
+    const uint32_t *w = reinterpret_cast<const uint32_t *>(a);
+    if constexpr (NV)
+        return __byte_perm(w[t >> 1], w[2 + (t >> 1)], (t & 1) ? 0x7632 : 0x5410);
+    else
+        return w[t];
 }
 
 // Code byte i of a word -> its two values as f16x2 (exact).
@@ -362,7 +363,7 @@ template <int I> __device__ __forceinline__ uint32_t e2m1x2_to_f16x2(uint32_t w)
 __device__ __forceinline__ void mma_f16_first(float (&c)[4], const uint32_t (&a)[4], uint32_t b0,
                                               uint32_t b1)
 {
-    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, "
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, "
                  "{%4, %5, %6, %7}, {%8, %9}, {%10, %10, %10, %10};"
                  : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
                  : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.0f));
@@ -371,7 +372,7 @@ __device__ __forceinline__ void mma_f16_first(float (&c)[4], const uint32_t (&a)
 __device__ __forceinline__ void mma_f16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0,
                                         uint32_t b1)
 {
-    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, "
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, "
                  "{%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
                  : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
                  : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
@@ -457,15 +458,17 @@ __device__ __forceinline__ void load_tile(uint32_t dst, const TileSource &s, int
 
 // Scale bytes of local row r as whole words; sh8: 8 x the byte in its word at which they start.
 template <bool NV>
-__device__ __forceinline__ void tile_scales(uint32_t tile, int r, uint32_t sh8, uint32_t (&s)[NV ? 4 : 2])
+__device__ __forceinline__ void tile_scales(const uint8_t *tile, int r, uint32_t sh8,
+                                            uint32_t (&s)[NV ? 4 : 2])
 {
-    const uint32_t a = tile + Tile<NV>::kOffScales + r * Tile<NV>::kSlot;
-    const uint4 w = lds128(a);
+    const uint4 *a =
+        reinterpret_cast<const uint4 *>(tile + Tile<NV>::kOffScales + r * Tile<NV>::kSlot);
+    const uint4 w = a[0];
     s[0] = __funnelshift_r(w.x, w.y, sh8);
     s[1] = __funnelshift_r(w.y, w.z, sh8);
     if constexpr (NV) {
         s[2] = __funnelshift_r(w.z, w.w, sh8);
-        s[3] = __funnelshift_r(w.w, lds32(a + 16), sh8);
+        s[3] = __funnelshift_r(w.w, a[1].x, sh8);
     }
 }
 
@@ -475,20 +478,21 @@ __device__ __forceinline__ bool odd_scale(uint32_t w)
     return ((((w - 0x01010101u) & ~w) | ((~w - 0x01010101u) & w)) & 0x80808080u) != 0u;
 }
 
-// acc += tile x activations over the tile's nb 32-blocks. frag(n, b) gives the activations of
-// column tile n as MMA B fragments; colscale(n, b, j) the scale of this lane's j-th accumulator
-// column (1 where COLS is not set). SPECIAL: MXFP4 scale bytes 0 and 255 occur.
-template <int NT, bool NV, bool COLS, bool SPECIAL, typename Frag, typename ColScale>
-__device__ __forceinline__ void tile_blocks(float (&acc)[NT][4], uint32_t tile, int nb, int nt,
-                                            int lane, const uint32_t (&s0)[NV ? 4 : 2],
-                                            const uint32_t (&s1)[NV ? 4 : 2], Frag frag,
-                                            ColScale colscale)
+// acc += half a tile (four 32-blocks, nb of them live) x activations. frag(n, b) gives the
+// activations of column tile n as MMA B fragments; colscale(n, b, j) the scale of this lane's j-th
+// accumulator column (COLS). NL live column tiles. SPECIAL: the general form, for short tiles and
+// for MXFP4 scale bytes 0 and 255; the other has no branch, so that the loads and MMAs of
+// neighbouring blocks interleave.
+template <int NT, int NL, bool NV, bool COLS, bool SPECIAL, typename Frag, typename ColScale>
+__device__ __forceinline__ void half_blocks(float (&acc)[NT][4], const uint8_t *codes, int nb,
+                                            int lane, const uint32_t *s0, const uint32_t *s1,
+                                            Frag frag, ColScale colscale)
 {
     const int g = lane >> 2, t = lane & 3;
-    const uint32_t ra = tile + g * Tile<NV>::kPitch, rb = ra + 8 * Tile<NV>::kPitch;
+    const uint8_t *ra = codes + g * Tile<NV>::kPitch, *rb = ra + 8 * Tile<NV>::kPitch;
 #pragma unroll
-    for (int b = 0; b < kTileBlocks; ++b) {
-        if (b >= nb)
+    for (int b = 0; b < 4; ++b) {
+        if (SPECIAL && b >= nb)
             break;
         const uint32_t w0 = lane_codes<NV>(ra + b * 16, t), w1 = lane_codes<NV>(rb + b * 16, t);
         // k16 step, fragment: rows g and g + 8, k indices 2t.. and 2t + 8..
@@ -505,16 +509,14 @@ __device__ __forceinline__ void tile_blocks(float (&acc)[NT][4], uint32_t tile, 
             f1[0] = p1.x;
             f1[1] = p1.y;
         } else if constexpr (SPECIAL) {
-            f0[0] = mx_scale_f32((s0[b >> 2] >> (8 * (b & 3))) & 0xFFu);
-            f1[0] = mx_scale_f32((s1[b >> 2] >> (8 * (b & 3))) & 0xFFu);
+            f0[0] = mx_scale_f32((s0[0] >> (8 * b)) & 0xFFu);
+            f1[0] = mx_scale_f32((s1[0] >> (8 * b)) & 0xFFu);
         } else { // the byte into bits 23..30
-            f0[0] = __uint_as_float(__byte_perm(s0[b >> 2], 0u, 0x0444u | (b & 3) << 12) >> 1);
-            f1[0] = __uint_as_float(__byte_perm(s1[b >> 2], 0u, 0x0444u | (b & 3) << 12) >> 1);
+            f0[0] = __uint_as_float(__byte_perm(s0[0], 0u, 0x0444u | b << 12) >> 1);
+            f1[0] = __uint_as_float(__byte_perm(s1[0], 0u, 0x0444u | b << 12) >> 1);
         }
 #pragma unroll
-        for (int n = 0; n < NT; ++n) {
-            if (n > 0 && n >= nt)
-                break;
+        for (int n = 0; n < NL; ++n) {
             const uint4 u = frag(n, b);
             float q0 = 1.0f, q1 = 1.0f;
             if constexpr (COLS) {
@@ -545,22 +547,40 @@ __device__ __forceinline__ void tile_blocks(float (&acc)[NT][4], uint32_t tile, 
     }
 }
 
-template <int NT, bool NV, bool COLS, typename Frag, typename ColScale>
-__device__ __forceinline__ void tile_product(float (&acc)[NT][4], uint32_t tile, int nb, int nt,
-                                             int lane, uint32_t sh0, uint32_t sh1, Frag frag,
+// The scales of a tile's rows g and g + 8, and whether they (or a short tile) need the general form.
+template <bool NV> struct TileScales {
+    uint32_t s0[NV ? 4 : 2], s1[NV ? 4 : 2];
+    bool special;
+
+    __device__ __forceinline__ void load(const uint8_t *tile, int nb, int lane, uint32_t sh0,
+                                         uint32_t sh1)
+    {
+        tile_scales<NV>(tile, lane >> 2, sh0, s0);
+        tile_scales<NV>(tile, (lane >> 2) + 8, sh1, s1);
+        special = nb < kTileBlocks;
+        if constexpr (!NV)
+            special = special || __any_sync(0xFFFFFFFFu, odd_scale(s0[0]) || odd_scale(s0[1]) ||
+                                                             odd_scale(s1[0]) || odd_scale(s1[1]));
+    }
+};
+
+// Half HALF of a tile, nt live column tiles.
+template <int HALF, int NT, bool NV, bool COLS, typename Frag, typename ColScale>
+__device__ __forceinline__ void half_product(float (&acc)[NT][4], const uint8_t *tile, int nb,
+                                             int nt, int lane, const TileScales<NV> &sc, Frag frag,
                                              ColScale colscale)
 {
-    uint32_t s0[NV ? 4 : 2], s1[NV ? 4 : 2];
-    tile_scales<NV>(tile, lane >> 2, sh0, s0);
-    tile_scales<NV>(tile, (lane >> 2) + 8, sh1, s1);
-    if constexpr (!NV) {
-        if (__any_sync(0xFFFFFFFFu, odd_scale(s0[0]) || odd_scale(s0[1]) || odd_scale(s1[0]) ||
-                                        odd_scale(s1[1]))) {
-            tile_blocks<NT, NV, COLS, true>(acc, tile, nb, nt, lane, s0, s1, frag, colscale);
-            return;
-        }
-    }
-    tile_blocks<NT, NV, COLS, false>(acc, tile, nb, nt, lane, s0, s1, frag, colscale);
+    constexpr int kW = NV ? 2 * HALF : HALF; // first scale word
+    const uint8_t *codes = tile + HALF * 64;
+    if (sc.special)
+        half_blocks<NT, NT, NV, COLS, true>(acc, codes, nb - 4 * HALF, lane, sc.s0 + kW, sc.s1 + kW,
+                                            frag, colscale);
+    else if (nt == 1)
+        half_blocks<NT, 1, NV, COLS, false>(acc, codes, 4, lane, sc.s0 + kW, sc.s1 + kW, frag,
+                                            colscale);
+    else
+        half_blocks<NT, NT, NV, COLS, false>(acc, codes, 4, lane, sc.s0 + kW, sc.s1 + kW, frag,
+                                             colscale);
 }
 
 // Place of value v (0..31) of a 32-block in the activations' layout: each lane's 8 values are
@@ -573,16 +593,19 @@ template <bool NV> __device__ __forceinline__ int lane_order(int v)
         return v;
 }
 
-constexpr int kMaxSmem = 232448; // per CTA
-constexpr int kUpWarps = 16, kUpStages = 3, kUpGroups = kUpWarps / 4;
-constexpr int kHPitch = 36; // floats between columns of the h exchange: conflict-free
+constexpr int kMaxSmem = 232448 - 64; // per CTA, beside the static part
+constexpr int kWarps = 16, kGroups = kWarps / 4, kStages = 3;
+constexpr int kRowBlock = 64;  // columns of y a CTA sums at a time: 16 a warp of a group
+constexpr int kHPitch = 36;    // floats between columns of the h exchange: conflict-free
+constexpr uint32_t kBarrierLimit = 1u << 21;
 
-// Shared memory of moe_up_kernel: rings, then h exchange, x panel, lists.
-template <int NT, bool NV> struct UpLayout {
-    static constexpr int kRing = kUpWarps * kUpStages * Tile<NV>::kBytes;
-    static constexpr int kH = 2 * kUpGroups * 8 * NT * kHPitch * 4;
-    static constexpr int kOffH = kRing;
-    static constexpr int kOffExp = kOffH + kH;
+// Shared memory: rings; sums of the K-split; h exchange; token exponents; x panel (gate/up) or y
+// sums (down); lists.
+template <int NT, bool NV, int KS> struct Layout {
+    static constexpr int kRed = (kGroups / KS) * KS * (KS - 1) * 4 * NT * 32 * 16;
+    static constexpr int kOffRed = kWarps * kStages * Tile<NV>::kBytes;
+    static constexpr int kOffH = kOffRed + kRed;
+    static constexpr int kOffExp = kOffH + kGroups * 8 * NT * kHPitch * 4;
     static constexpr int kOffX = kOffExp + 128;
     // bytes between columns of the x panel: 64 past a multiple of 128, so that the 16-byte
     // fragment loads of two columns x four lanes hit 32 banks
@@ -590,392 +613,526 @@ template <int NT, bool NV> struct UpLayout {
     {
         return panel * 2 + (panel * 2 % 128 == 0 ? 64 : 0);
     }
+    __host__ __device__ static int x_bytes(int T, int panel)
+    {
+        const int x = (T < 8 * NT ? T : 8 * NT) * x_pitch(panel), y = kWarps * 16 * T * 4;
+        return x > y ? x : y;
+    }
 };
 
-// h = silu(gate) * up. Work is cut into items of 32 columns of F of one column tile; a group of four
-// warps takes an item, a warp 8 of its columns: 8 gate rows and the same 8 up rows are its 16 MMA
-// rows, so a lane's accumulators hold both sides of its products, and a warp needs no other until
-// the block exponents of h. One CTA per SM takes a run of items; each warp's ring of weight tiles
-// runs on across them. The tokens of the column tile are kept in shared memory as f16, each
-// divided by its power of two (whole rows, or panels of them where they do not fit).
-template <int NT, bool NV>
-__global__ void __launch_bounds__(kUpWarps * 32, 1) moe_up_kernel(const MoeParams p)
+// The whole layer's experts in one cooperative launch, one CTA of 16 warps per SM.
+//
+// Gate/up: an item is 32 columns of F (64 weight rows) of one column tile. A team of KS groups of
+// four warps takes an item; a warp has 8 of its columns, 8 gate rows and the same 8 up rows as its 16
+// MMA rows, so that a lane's accumulators hold both sides of its products; the team's groups split
+// the k-tiles, and take turns in adding the others' sums and finishing an item (h and its block
+// exponents, to the workspace). A CTA's items are a run, so its tokens change seldom; they are kept in
+// shared memory as f16, each divided by its power of two (whole rows, or panels of them where they
+// do not fit).
+//
+// Grid barrier (every h is in place), behind which the rings already fill with the next tiles.
+//
+// Down: a CTA sums 64 columns of y, its groups' and `splits` CTAs' shares being runs of the flat list
+// of (column tile, k-tile) pairs of all met experts. A warp weights its sums of a column tile into
+// its own [T x 16] array; the arrays are added group by group, the CTAs' sums split by split by the
+// CTA that comes last, so the order of every sum is fixed.
+//
+// Bound by the decode (35-40 issue slots per 16 x 32 codes and column tile, about the time HBM takes
+// for them), so both have to run at once: the rings are private to the warps and run on across items.
+template <int NT, bool NV, int KS>
+__global__ void __launch_bounds__(kWarps * 32, 1) moe_experts_kernel(const MoeParams p)
 {
     using L = Tile<NV>;
-    using U = UpLayout<NT, NV>;
-    constexpr int NC = 8 * NT;
+    using U = Layout<NT, NV, KS>;
+    constexpr int NC = 8 * NT, kTeams = kGroups / KS;
     extern __shared__ __align__(16) uint8_t smem[];
+    __shared__ int s_flag;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
-    const int grp = warp >> 2, w4 = warp & 3;
-    const int pitch = U::x_pitch(p.panel);
-    const MoeLists l = moe_lists(smem + U::kOffX + min(NC, p.T) * pitch, p.T, p.k, p.E);
+    const int grp = warp >> 2, w4 = warp & 3, team = grp / KS, kg = grp % KS;
+    const MoeLists l = moe_lists(smem + U::kOffX + U::x_bytes(p.T, p.panel), p.T, p.k, p.E);
+    const int nrb = (int)((p.H + kRowBlock - 1) / kRowBlock);
     pdl_wait();
-    build_lists<false>(l, p, NC);
-    pdl_launch_dependents(); // everything before this kernel is complete: see moe_down_kernel
+    if (blockIdx.x == 0)
+        for (int i = tid; i < nrb; i += kWarps * 32)
+            p.arrived[i] = 0;
+    build_lists(l, p, NC);
 
     const int nf = (int)(p.F >> 5); // items per column tile
-    const int64_t items = (int64_t)*l.n_units * nf;
+    const int n_units = *l.n_units;
+    const int64_t items = (int64_t)n_units * nf;
     const int i0 = (int)(items * blockIdx.x / gridDim.x);
     const int i1 = (int)(items * (blockIdx.x + 1) / gridDim.x);
-    if (i0 >= i1)
-        return;
-    const int nblk = (int)(p.H >> 5), nkt = (nblk + kTileBlocks - 1) / kTileBlocks;
-    const int64_t erow = NV ? p.H >> 4 : p.H >> 5;
+    const int upblk = (int)(p.H >> 5), upkt = (upblk + kTileBlocks - 1) / kTileBlocks;
+    const int dnblk = (int)(p.F >> 5), dnkt = (dnblk + kTileBlocks - 1) / kTileBlocks;
+    const int64_t uprow = NV ? p.H >> 4 : p.H >> 5, dnrow = NV ? p.F >> 4 : p.F >> 5;
 
-    // the tiles to load, in the order in which they are used
-    const uint32_t ring = smem_u32(smem) + warp * kUpStages * L::kBytes;
-    int lu = i0 / nf, li = i0 + grp, lkt = 0, lslot = 0;
-    bool more = true;
+    // ---- the tiles this warp loads, in the order in which it uses them -------------------------
+    uint8_t *ring = smem + warp * kStages * L::kBytes;
+    const uint32_t ring_addr = smem_u32(ring);
+    int phase = 0;                      // 0 gate/up, 1 down, 2 none left
+    int lu, li, lkt, left = 0, lslot = 0, job = 0;
     TileSource src;
-    auto seek = [&]() { // to the next item of this group, its unit's or a later one's
-        while (more && li >= min(i1, (lu + 1) * nf)) {
+    // the warp's run of (column tile, k-tile) pairs in down job j: [a, b)
+    auto down_run = [&](int j, int &a, int &b) {
+        const int64_t row = (int64_t)(j / p.splits) * kRowBlock + w4 * 16;
+        const int64_t total = row < p.H ? (int64_t)n_units * dnkt : 0;
+        const int run = (j % p.splits) * kGroups + grp, runs = p.splits * kGroups;
+        a = (int)(total * run / runs);
+        b = (int)(total * (run + 1) / runs);
+    };
+    auto down_source = [&]() {
+        const int64_t e = unit_expert(l.unit[lu]);
+        src = tile_source<NV>(p.down_codes + e * p.H * (p.F >> 1), p.down_scales + e * p.H * dnrow,
+                              p.F, (int64_t)(job / p.splits) * kRowBlock + w4 * 16, 8, lane);
+    };
+    auto down_seek = [&]() { // to the first down job from `job` on with tiles for this warp
+        phase = 2;
+        for (; job < nrb * p.splits; job += gridDim.x) {
+            int a, b;
+            down_run(job, a, b);
+            if (a < b) {
+                left = b - a;
+                lu = a / dnkt;
+                lkt = a % dnkt;
+                phase = 1;
+                down_source();
+                return;
+            }
+        }
+    };
+    auto up_seek = [&]() { // to this team's next item, of the same column tile or a later one
+        while (li >= min(i1, (lu + 1) * nf)) {
             ++lu;
-            li = lu * nf + grp;
-            more = lu * nf < i1;
+            li = lu * nf + team;
+            if (lu * nf >= i1) {
+                job = blockIdx.x;
+                down_seek();
+                return;
+            }
         }
-        if (more) {
-            const int64_t e = l.unit[lu] & 0xFFFF;
-            src = tile_source<NV>(p.up_codes + e * 2 * p.F * (p.H >> 1),
-                                  p.up_scales + e * 2 * p.F * erow, p.H,
-                                  (int64_t)(li - lu * nf) * 32 + w4 * 8, p.F, lane);
-        }
+        const int64_t e = unit_expert(l.unit[lu]);
+        src = tile_source<NV>(p.up_codes + e * 2 * p.F * (p.H >> 1),
+                              p.up_scales + e * 2 * p.F * uprow, p.H,
+                              (int64_t)(li - lu * nf) * 32 + w4 * 8, p.F, lane);
     };
-    seek();
     auto issue = [&]() {
-        if (more) {
-            load_tile<NV>(ring + lslot * L::kBytes, src, p.H, p.F, lkt, lane);
-            if (++lkt == nkt) {
-                lkt = 0;
-                li += kUpGroups;
-                seek();
+        const uint32_t dst = ring_addr + lslot * L::kBytes;
+        if (phase == 0) {
+            load_tile<NV>(dst, src, p.H, p.F, lkt, lane);
+            lkt += KS;
+            if (lkt >= upkt) {
+                lkt = kg;
+                li += kTeams;
+                up_seek();
             }
-        }
-        cp_async_commit();
-        lslot = lslot + 1 == kUpStages ? 0 : lslot + 1;
-    };
-#pragma unroll
-    for (int i = 0; i < kUpStages - 1; ++i)
-        issue();
-
-    uint8_t *sx = smem + U::kOffX;
-    uint32_t *s_ex = reinterpret_cast<uint32_t *>(smem + U::kOffExp);
-    float *s_h = reinterpret_cast<float *>(smem + U::kOffH);
-    uint32_t xaddr[NT]; // this lane's column of each column tile (past the last kept: that one)
-#pragma unroll
-    for (int n = 0; n < NT; ++n)
-        xaddr[n] = smem_u32(sx) + min(n * 8 + g, min(NC, p.T) - 1) * pitch + t * 16;
-    int slot = 0, buf = 0;
-    for (int u = i0 / nf; u * nf < i1; ++u) {
-        const int unit = l.unit[u];
-        const int e = unit & 0xFFFF, c0 = unit >> 16;
-        const int row0 = l.base[e] + c0;
-        const int ncol = min(NC, mask_count(l.mask + 2 * e) - c0);
-        const int nt = (ncol + 7) >> 3;
-        const int a = max(i0, u * nf), b = min(i1, (u + 1) * nf);
-        const float gs = NV ? __ldg(p.up_gs + e) : 1.0f;
-        for (int r = a; r < b; r += kUpGroups) {
-            const int it = r + grp;
-            const bool on = it < b;
-            const int64_t f0 = (int64_t)(it - u * nf) * 32;
-            const uint32_t sh0 = (uint32_t)(((f0 + w4 * 8 + g) * erow) & 3) * 8u;
-            const uint32_t sh1 = (uint32_t)(((p.F + f0 + w4 * 8 + g) * erow) & 3) * 8u;
-            float acc[NT][4] = {};
-            for (int k0 = 0; k0 < (int)p.H; k0 += p.panel) {
-                const int k1 = min((int)p.H, k0 + p.panel);
-                if (r == a || p.panel < (int)p.H) {
-                    __syncthreads(); // the last panel has been used
-                    for (int c = warp; c < ncol; c += kUpWarps) {
-                        const uint4 *x = p.x + (int64_t)l.tok[row0 + c] * (p.H >> 3);
-                        uint32_t m = 0u;
-#pragma unroll 4
-                        for (int i = lane; i < (int)(p.H >> 3); i += 32) {
-                            const uint4 v = __ldg(x + i);
-                            m = max_u16x2(m, max_u16x2(max_u16x2(v.x & kAbs16x2, v.y & kAbs16x2),
-                                                       max_u16x2(v.z & kAbs16x2, v.w & kAbs16x2)));
-                        }
-                        m = __reduce_max_sync(0xFFFFFFFFu, max(m & 0xFFFFu, m >> 16));
-                        const uint32_t ex = block_exponent(m << 16);
-                        const float inv = __uint_as_float((254u - ex) << 23);
-                        if (lane == 0)
-                            s_ex[c] = ex;
-#pragma unroll 4
-                        for (int i = (k0 >> 3) + lane; i < k1 >> 3; i += 32) {
-                            const uint4 v = __ldg(x + i);
-                            const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-                            uint32_t h[4];
-#pragma unroll
-                            for (int q = 0; q < 4; ++q)
-                                h[q] = pack_f16x2(__uint_as_float(w[q] << 16) * inv,
-                                                  __uint_as_float(w[q] & 0xFFFF0000u) * inv);
-                            // eight values: two groups of four at their lanes' places
-                            uint8_t *d = sx + c * pitch + ((i - (k0 >> 3)) >> 2) * 64;
-                            const int v0 = (i & 3) * 8;
-                            *reinterpret_cast<uint2 *>(d + lane_order<NV>(v0) * 2) =
-                                make_uint2(h[0], h[1]);
-                            *reinterpret_cast<uint2 *>(d + lane_order<NV>(v0 + 4) * 2) =
-                                make_uint2(h[2], h[3]);
-                        }
-                    }
-                    __syncthreads();
-                }
-                if (on) {
-                    for (int kt = k0 / kTileK; kt * kTileK < k1; ++kt) {
-                        issue();
-                        cp_async_wait<kUpStages - 1>();
-                        __syncwarp();
-                        const uint32_t xt = (kt * kTileK - k0) * 2;
-                        tile_product<NT, NV, false>(
-                            acc, ring + slot * L::kBytes, min(kTileBlocks, nblk - kt * kTileBlocks),
-                            nt, lane, sh0, sh1,
-                            [&](int n, int blk) { return lds128(xaddr[n] + xt + blk * 64); },
-                            [](int, int, int) { return 1.0f; });
-                        __syncwarp(); // the tile is read before its slot is filled again
-                        slot = slot + 1 == kUpStages ? 0 : slot + 1;
-                    }
-                }
-            }
-            if (on) {
-                float *hx = s_h + (buf * kUpGroups + grp) * NC * kHPitch;
-#pragma unroll
-                for (int n = 0; n < NT; ++n)
-#pragma unroll
-                    for (int j = 0; j < 2; ++j) {
-                        const int c = n * 8 + 2 * t + j;
-                        if (c < ncol) {
-                            const float sc = __uint_as_float(s_ex[c] << 23);
-                            const float ga = acc[n][j] * sc * gs, up = acc[n][2 + j] * sc * gs;
-                            hx[c * kHPitch + w4 * 8 + g] = ga / (1.0f + __expf(-ga)) * up;
-                        }
-                    }
-                // one barrier an item: the next item uses the other buffer
-                named_bar_sync(1 + grp, 128);
-                for (int c = w4; c < ncol; c += 4) {
-                    const float v = hx[c * kHPitch + lane];
-                    const uint32_t m =
-                        __reduce_max_sync(0xFFFFFFFFu, __float_as_uint(v) & 0x7FFFFFFFu);
-                    const uint32_t ex = block_exponent(m);
-                    const int64_t row = row0 + c;
-                    reinterpret_cast<__half *>(p.h)[row * p.F + f0 + lane_order<NV>(lane)] =
-                        __float2half_rn(v * __uint_as_float((254u - ex) << 23));
-                    if (lane == 0)
-                        p.h_exp[row * p.exp_pitch + (f0 >> 5)] = (uint8_t)ex;
-                }
-                buf ^= 1;
-            }
-        }
-    }
-    cp_async_wait<0>();
-}
-
-constexpr int kDownRowWarps = 4, kDownKWarps = 2, kDownWarps = kDownRowWarps * kDownKWarps;
-constexpr int kDownStages = 3, kDownCluster = 8, kDownRows = kDownRowWarps * 16;
-
-// y for 64 columns of H by a cluster of 8 CTAs: each row warp takes 16 columns, and the flat list of
-// (column tile, k-tile) pairs of all met experts is cut into 16 runs, one per CTA and k-warp. A
-// warp's sums of one column tile are weighted and added to its own [16 x T] array; the arrays are
-// added over the k-warps and then over the cluster's CTAs, in order.
-template <int NT, bool NV>
-__global__ void __cluster_dims__(kDownCluster, 1, 1) __launch_bounds__(kDownWarps * 32, 2)
-    moe_down_kernel(const MoeParams p)
-{
-    using L = Tile<NV>;
-    constexpr int NC = 8 * NT;
-    extern __shared__ __align__(16) uint8_t smem[];
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
-    const int rank = (int)cluster_ctarank();
-    float *ysum = reinterpret_cast<float *>(smem + kDownWarps * kDownStages * L::kBytes);
-    const MoeLists l = moe_lists(reinterpret_cast<uint8_t *>(ysum + kDownWarps * 16 * p.T), p.T,
-                                 p.k, p.E);
-    for (int i = tid; i < kDownWarps * 16 * p.T; i += kDownWarps * 32)
-        ysum[i] = 0.0f;
-    // This grid starts once every CTA of moe_up_kernel is past its own wait for the stream's
-    // earlier work, so the ids, the weights and the experts' codes are already complete; only h
-    // (and y's readers) need the wait below.
-    build_lists<true>(l, p, NC);
-    const int64_t r0 = (int64_t)(blockIdx.x / kDownCluster) * kDownRows +
-                       (warp % kDownRowWarps) * 16;
-    const bool rows_on = r0 < p.H;
-    const int nblk = (int)(p.F >> 5), nkt = (nblk + kTileBlocks - 1) / kTileBlocks;
-    const int64_t erow = NV ? p.F >> 4 : p.F >> 5;
-    const int64_t total = rows_on ? (int64_t)*l.n_units * nkt : 0;
-    const int run = rank * kDownKWarps + warp / kDownRowWarps;
-    const int u0 = (int)(total * run / (kDownCluster * kDownKWarps));
-    const int u1 = (int)(total * (run + 1) / (kDownCluster * kDownKWarps));
-
-    const uint32_t ring = smem_u32(smem) + warp * kDownStages * L::kBytes;
-    int lu = u0 / nkt, lkt = u0 % nkt, left = u1 - u0, lslot = 0;
-    TileSource src;
-    auto seek = [&]() {
-        const int64_t e = l.unit[lu] & 0xFFFF;
-        src = tile_source<NV>(p.down_codes + e * p.H * (p.F >> 1), p.down_scales + e * p.H * erow,
-                              p.F, r0, 8, lane);
-    };
-    if (left > 0)
-        seek();
-    auto issue = [&]() {
-        if (left > 0) {
-            load_tile<NV>(ring + lslot * L::kBytes, src, p.F, 8, lkt, lane);
-            --left;
-            if (++lkt == nkt) {
+        } else if (phase == 1) {
+            load_tile<NV>(dst, src, p.F, 8, lkt, lane);
+            if (--left == 0) {
+                job += gridDim.x;
+                down_seek();
+            } else if (++lkt == dnkt) {
                 lkt = 0;
                 ++lu;
-                if (left > 0)
-                    seek();
+                down_source();
             }
         }
         cp_async_commit();
-        lslot = lslot + 1 == kDownStages ? 0 : lslot + 1;
+        lslot = lslot + 1 == kStages ? 0 : lslot + 1;
     };
+    if (i0 < i1 && kg < upkt) {
+        lu = i0 / nf;
+        li = i0 + team;
+        lkt = kg;
+        up_seek();
+    } else {
+        job = blockIdx.x;
+        down_seek();
+    }
 #pragma unroll
-    for (int i = 0; i < kDownStages - 1; ++i)
+    for (int i = 0; i < kStages - 1; ++i)
         issue();
-    pdl_wait(); // h
-
-    const uint32_t sh0 = (uint32_t)(((r0 + g) * erow) & 3) * 8u;
-    const uint32_t sh1 = (uint32_t)(((r0 + g + 8) * erow) & 3) * 8u;
-    float acc[NT][4] = {};
-    float *mysum = ysum + warp * 16 * p.T;
     int slot = 0;
-    for (int u = u0 / nkt, kt = u0 % nkt, n_left = u1 - u0; n_left > 0; ++u, kt = 0) {
-        const int unit = l.unit[u];
-        const int e = unit & 0xFFFF, c0 = unit >> 16;
-        const int row = l.base[e] + c0;
-        const int ncol = min(NC, mask_count(l.mask + 2 * e) - c0);
-        const int nt = (ncol + 7) >> 3;
-        const int kend = min(nkt, kt + n_left);
-        n_left -= kend - kt;
-        const uint4 *hp[NT];
-        const uint8_t *ep[NT][2];
-#pragma unroll
-        for (int n = 0; n < NT; ++n) {
-            const int64_t r = row + min(n * 8 + g, ncol - 1); // dead columns read a live one's
-            hp[n] = p.h + r * (p.F >> 3) + t;
-#pragma unroll
-            for (int j = 0; j < 2; ++j)
-                ep[n][j] = p.h_exp + (int64_t)(row + min(n * 8 + 2 * t + j, ncol - 1)) * p.exp_pitch;
-        }
-        for (; kt < kend; ++kt) {
-            issue();
-            uint4 hv[NT][kTileBlocks];
-            uint2 ev[NT][2];
-            const int nb = min(kTileBlocks, nblk - kt * kTileBlocks);
-#pragma unroll
-            for (int n = 0; n < NT; ++n) {
-                if (n > 0 && n >= nt)
-                    break;
-#pragma unroll
-                for (int b = 0; b < kTileBlocks; ++b)
-                    if (b < nb)
-                        hv[n][b] = hp[n][(kt * kTileBlocks + b) * 4];
-#pragma unroll
-                for (int j = 0; j < 2; ++j)
-                    ev[n][j] = *reinterpret_cast<const uint2 *>(ep[n][j] + kt * kTileBlocks);
-            }
-            cp_async_wait<kDownStages - 1>();
-            __syncwarp();
-            tile_product<NT, NV, true>(
-                acc, ring + slot * L::kBytes, nb, nt, lane, sh0, sh1,
-                [&](int n, int b) { return hv[n][b]; },
-                [&](int n, int b, int j) {
-                    return __uint_as_float(
-                        __byte_perm(b < 4 ? ev[n][j].x : ev[n][j].y, 0u, 0x0444u | (b & 3) << 12) >>
-                        1);
-                });
-            __syncwarp();
-            slot = slot + 1 == kDownStages ? 0 : slot + 1;
-        }
-        // the column tile's sums of this run
-        const float gs = NV ? __ldg(p.down_gs + e) : 1.0f;
+    auto next_tile = [&]() -> const uint8_t * { // the oldest tile, once it has arrived
+        issue();
+        cp_async_wait<kStages - 1>();
+        __syncwarp();
+        return ring + slot * L::kBytes;
+    };
+    auto tile_done = [&]() {
+        __syncwarp(); // the tile is read before its slot is filled again
+        slot = slot + 1 == kStages ? 0 : slot + 1;
+    };
+
+    // ---- gate/up --------------------------------------------------------------------------------
+    {
+        const int pitch = U::x_pitch(p.panel);
+        uint8_t *sx = smem + U::kOffX;
+        uint32_t *s_ex = reinterpret_cast<uint32_t *>(smem + U::kOffExp);
+        float *hx = reinterpret_cast<float *>(smem + U::kOffH) + grp * NC * kHPitch;
+        // [team][turn][other group][w4][n][lane]
+        float4 *red = reinterpret_cast<float4 *>(smem + U::kOffRed) +
+                      team * KS * (KS - 1) * 4 * NT * 32;
+        const uint8_t *xcol[NT]; // this lane's column of each column tile (past the last: that one)
 #pragma unroll
         for (int n = 0; n < NT; ++n)
+            xcol[n] = sx + min(n * 8 + g, min(NC, p.T) - 1) * pitch + t * 16;
+        int turn = 0; // the team's group that finishes the item
+        for (int u = i0 / nf; u * nf < i1; ++u) {
+            const int e = unit_expert(l.unit[u]), c0 = unit_column(l.unit[u]);
+            const int row0 = l.base[e] + c0;
+            const int ncol = min(NC, mask_count(l.mask + 2 * e) - c0);
+            const int nt = (ncol + 7) >> 3;
+            const int a = max(i0, u * nf), b = min(i1, (u + 1) * nf);
+            const float gs = NV ? __ldg(p.up_gs + e) : 1.0f;
+            for (int r = a; r < b; r += kTeams) {
+                const int it = r + team;
+                const bool on = it < b;
+                const int64_t f0 = (int64_t)(it - u * nf) * 32;
+                const uint32_t sh0 = (uint32_t)(((f0 + w4 * 8 + g) * uprow) & 3) * 8u;
+                const uint32_t sh1 = (uint32_t)(((p.F + f0 + w4 * 8 + g) * uprow) & 3) * 8u;
+                float acc[NT][4] = {};
+                int kt = kg;
+                for (int k0 = 0; k0 < (int)p.H; k0 += p.panel) {
+                    const int k1 = min((int)p.H, k0 + p.panel);
+                    if (r == a || p.panel < (int)p.H) {
+                        __syncthreads(); // the last panel has been used
+                        for (int c = warp; c < ncol; c += kWarps) {
+                            const uint4 *x = p.x + (int64_t)l.tok[row0 + c] * (p.H >> 3);
+                            uint32_t m = 0u;
+#pragma unroll 4
+                            for (int i = lane; i < (int)(p.H >> 3); i += 32) {
+                                const uint4 v = __ldg(x + i);
+                                m = max_u16x2(
+                                    m, max_u16x2(max_u16x2(v.x & kAbs16x2, v.y & kAbs16x2),
+                                                 max_u16x2(v.z & kAbs16x2, v.w & kAbs16x2)));
+                            }
+                            m = __reduce_max_sync(0xFFFFFFFFu, max(m & 0xFFFFu, m >> 16));
+                            const uint32_t ex = block_exponent(m << 16);
+                            const float inv = __uint_as_float((254u - ex) << 23);
+                            if (lane == 0)
+                                s_ex[c] = ex;
+#pragma unroll 4
+                            for (int i = (k0 >> 3) + lane; i < k1 >> 3; i += 32) {
+                                const uint4 v = __ldg(x + i);
+                                const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+                                uint32_t h[4];
 #pragma unroll
-            for (int j = 0; j < 2; ++j) {
-                const int c = n * 8 + 2 * t + j;
-                if (c < ncol) {
-                    const float w = l.wt[row + c];
-                    const int tok = l.tok[row + c];
-                    mysum[g * p.T + tok] = fmaf(acc[n][j] * gs, w, mysum[g * p.T + tok]);
-                    mysum[(g + 8) * p.T + tok] =
-                        fmaf(acc[n][2 + j] * gs, w, mysum[(g + 8) * p.T + tok]);
+                                for (int q = 0; q < 4; ++q)
+                                    h[q] = pack_f16x2(__uint_as_float(w[q] << 16) * inv,
+                                                      __uint_as_float(w[q] & 0xFFFF0000u) * inv);
+                                // eight values: two groups of four at their lanes' places
+                                uint8_t *d = sx + c * pitch + ((i - (k0 >> 3)) >> 2) * 64;
+                                const int v0 = (i & 3) * 8;
+                                *reinterpret_cast<uint2 *>(d + lane_order<NV>(v0) * 2) =
+                                    make_uint2(h[0], h[1]);
+                                *reinterpret_cast<uint2 *>(d + lane_order<NV>(v0 + 4) * 2) =
+                                    make_uint2(h[2], h[3]);
+                            }
+                        }
+                        __syncthreads();
+                    }
+                    for (; on && kt * kTileK < k1; kt += KS) {
+                        const uint8_t *tile = next_tile();
+                        const int nb = min(kTileBlocks, upblk - kt * kTileBlocks);
+                        TileScales<NV> sc;
+                        sc.load(tile, nb, lane, sh0, sh1);
+                        const int xt = (kt * kTileK - k0) * 2;
+                        const auto one = [](int, int, int) { return 1.0f; };
+                        half_product<0, NT, NV, false>(
+                            acc, tile, nb, nt, lane, sc,
+                            [&](int n, int b_) {
+                                return *reinterpret_cast<const uint4 *>(xcol[n] + xt + b_ * 64);
+                            },
+                            one);
+                        half_product<1, NT, NV, false>(
+                            acc, tile, nb, nt, lane, sc,
+                            [&](int n, int b_) {
+                                return *reinterpret_cast<const uint4 *>(xcol[n] + xt + 256 +
+                                                                        b_ * 64);
+                            },
+                            one);
+                        tile_done();
+                    }
                 }
-                acc[n][j] = acc[n][2 + j] = 0.0f;
+                if (!on)
+                    continue;
+                // The others hand their sums to the group whose turn it is. A turn's buffer comes
+                // around after KS items: every other group has by then had its own turn, for which
+                // it waited for this one's next arrival, made after the buffer was read.
+                float4 *rt = red + turn * (KS - 1) * 4 * NT * 32;
+                if (kg != turn) {
+                    float4 *dst = rt + ((kg < turn ? kg : kg - 1) * 4 + w4) * NT * 32 + lane;
+#pragma unroll
+                    for (int n = 0; n < NT; ++n)
+                        dst[n * 32] = make_float4(acc[n][0], acc[n][1], acc[n][2], acc[n][3]);
+                    named_bar_arrive(1 + team * KS + turn, KS * 128);
+                } else {
+                    named_bar_sync(1 + team * KS + turn, KS * 128);
+#pragma unroll
+                    for (int n = 0; n < NT; ++n) {
+                        float4 s = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+                        for (int q = 0; q < KS; ++q) { // in group order
+                            float4 v = make_float4(acc[n][0], acc[n][1], acc[n][2], acc[n][3]);
+                            if (q != kg)
+                                v = rt[((q < kg ? q : q - 1) * 4 + w4) * NT * 32 + n * 32 + lane];
+                            s.x += v.x;
+                            s.y += v.y;
+                            s.z += v.z;
+                            s.w += v.w;
+                        }
+                        const float gate[2] = {s.x, s.y}, upv[2] = {s.z, s.w};
+#pragma unroll
+                        for (int j = 0; j < 2; ++j) {
+                            const int c = n * 8 + 2 * t + j;
+                            if (c < ncol) {
+                                const float q = __uint_as_float(s_ex[c] << 23);
+                                const float ga = gate[j] * q * gs, up = upv[j] * q * gs;
+                                hx[c * kHPitch + w4 * 8 + g] = ga / (1.0f + __expf(-ga)) * up;
+                            }
+                        }
+                    }
+                    named_bar_sync(9 + grp, 128);
+                    for (int c = w4; c < ncol; c += 4) {
+                        const float v = hx[c * kHPitch + lane];
+                        const uint32_t m =
+                            __reduce_max_sync(0xFFFFFFFFu, __float_as_uint(v) & 0x7FFFFFFFu);
+                        const uint32_t ex = block_exponent(m);
+                        const int64_t row = row0 + c;
+                        reinterpret_cast<__half *>(p.h)[row * p.F + f0 + lane_order<NV>(lane)] =
+                            __float2half_rn(v * __uint_as_float((254u - ex) << 23));
+                        if (lane == 0)
+                            p.h_exp[row * p.exp_pitch + (f0 >> 5)] = (uint8_t)ex;
+                    }
+                }
+                turn = turn + 1 == KS ? 0 : turn + 1;
             }
-        __syncwarp(); // the next tile's columns may be other lanes' tokens
+        }
+    }
+
+    // ---- every h in place -----------------------------------------------------------------------
+    __syncthreads();
+    if (tid == 0) {
+        s_flag = grid_barrier_sync(p.barrier, (int)gridDim.x, (int)blockIdx.x, kBarrierLimit) ? 1 : 0;
+        if (!s_flag)
+            atomicExch(p.status, (int)NVFP4_ERR_TIMEOUT);
+    }
+    __syncthreads();
+    if (!s_flag) {
+        cp_async_wait<0>();
+        return;
+    }
+
+    // ---- down -----------------------------------------------------------------------------------
+    float *ysum = reinterpret_cast<float *>(smem + U::kOffX); // [group][w4][T][16]
+    float *mysum = ysum + warp * 16 * p.T;
+    for (int jb = blockIdx.x; jb < nrb * p.splits; jb += gridDim.x) {
+        for (int i = lane; i < 16 * p.T; i += 32)
+            mysum[i] = 0.0f;
+        __syncwarp();
+        const int64_t r0 = (int64_t)(jb / p.splits) * kRowBlock + w4 * 16;
+        const uint32_t sh0 = (uint32_t)(((r0 + g) * dnrow) & 3) * 8u;
+        const uint32_t sh1 = (uint32_t)(((r0 + g + 8) * dnrow) & 3) * 8u;
+        int a, b;
+        down_run(jb, a, b);
+        float acc[NT][4] = {};
+        for (int u = a / dnkt, kt = a % dnkt, rest = b - a; rest > 0; ++u, kt = 0) {
+            const int e = unit_expert(l.unit[u]), c0 = unit_column(l.unit[u]);
+            const int row = l.base[e] + c0;
+            const int ncol = min(NC, mask_count(l.mask + 2 * e) - c0);
+            const int nt = (ncol + 7) >> 3;
+            const int kend = min(dnkt, kt + rest);
+            rest -= kend - kt;
+            const uint4 *hp[NT];
+            const uint8_t *ep[NT][2];
+#pragma unroll
+            for (int n = 0; n < NT; ++n) { // dead columns read a live one's
+                hp[n] = p.h + (int64_t)(row + min(n * 8 + g, ncol - 1)) * (p.F >> 3) + t;
+#pragma unroll
+                for (int j = 0; j < 2; ++j)
+                    ep[n][j] =
+                        p.h_exp + (int64_t)(row + min(n * 8 + 2 * t + j, ncol - 1)) * p.exp_pitch;
+            }
+            // half a tile's activations and their exponents
+            struct Half {
+                uint4 h[NT][4];
+                uint32_t e[NT][2];
+            };
+            auto fetch = [&](Half &f, int blk) {
+#pragma unroll
+                for (int n = 0; n < NT; ++n) {
+                    if (n > 0 && n >= nt)
+                        break;
+#pragma unroll
+                    for (int q = 0; q < 4; ++q)
+                        f.h[n][q] = hp[n][min(blk + q, dnblk - 1) * 4];
+#pragma unroll
+                    for (int j = 0; j < 2; ++j)
+                        f.e[n][j] = *reinterpret_cast<const uint32_t *>(ep[n][j] + blk);
+                }
+            };
+            auto scale_of = [](const Half &f, int n, int q, int j) {
+                return __uint_as_float(__byte_perm(f.e[n][j], 0u, 0x0444u | q << 12) >> 1);
+            };
+            Half f0, f1;
+            fetch(f0, kt * kTileBlocks);
+            for (; kt < kend; ++kt) {
+                const uint8_t *tile = next_tile();
+                const int nb = min(kTileBlocks, dnblk - kt * kTileBlocks);
+                TileScales<NV> sc;
+                sc.load(tile, nb, lane, sh0, sh1);
+                fetch(f1, kt * kTileBlocks + 4); // exponents past the row: its padding
+                half_product<0, NT, NV, true>(
+                    acc, tile, nb, nt, lane, sc, [&](int n, int q) { return f0.h[n][q]; },
+                    [&](int n, int q, int j) { return scale_of(f0, n, q, j); });
+                if (kt + 1 < kend)
+                    fetch(f0, (kt + 1) * kTileBlocks);
+                half_product<1, NT, NV, true>(
+                    acc, tile, nb, nt, lane, sc, [&](int n, int q) { return f1.h[n][q]; },
+                    [&](int n, int q, int j) { return scale_of(f1, n, q, j); });
+                tile_done();
+            }
+            // the column tile's sums of this run
+            const float gs = NV ? __ldg(p.down_gs + e) : 1.0f;
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    const int c = n * 8 + 2 * t + j;
+                    if (c < ncol) {
+                        const float w = l.wt[row + c];
+                        float *y = mysum + l.tok[row + c] * 16 + g;
+                        y[0] = fmaf(acc[n][j] * gs, w, y[0]);
+                        y[8] = fmaf(acc[n][2 + j] * gs, w, y[8]);
+                    }
+                    acc[n][j] = acc[n][2 + j] = 0.0f;
+                }
+            __syncwarp(); // the next tile's columns may be other lanes' tokens
+        }
+        __syncthreads();
+        // the groups' sums: y, or this split's share of it
+        const int rb = jb / p.splits;
+        float *part = p.partial + ((int64_t)rb * p.splits + jb % p.splits) * p.T * kRowBlock;
+        for (int i = tid; i < kRowBlock * p.T; i += kWarps * 32) {
+            const int r = i % kRowBlock, tk = i / kRowBlock;
+            float s = 0.0f;
+#pragma unroll
+            for (int q = 0; q < kGroups; ++q)
+                s += ysum[((q * 4 + (r >> 4)) * p.T + tk) * 16 + (r & 15)];
+            if (p.splits > 1)
+                part[i] = s;
+            else if ((int64_t)rb * kRowBlock + r < p.H)
+                p.y[tk * p.H + (int64_t)rb * kRowBlock + r] = __float2bfloat16_rn(s);
+        }
+        if (p.splits > 1) {
+            __threadfence();
+            __syncthreads();
+            if (tid == 0)
+                s_flag = atomicAdd(p.arrived + rb, 1);
+            __syncthreads();
+            if (s_flag == p.splits - 1) { // the last of the block's CTAs adds them up
+                __threadfence();
+                const float *all = p.partial + (int64_t)rb * p.splits * p.T * kRowBlock;
+                for (int i = tid; i < kRowBlock * p.T; i += kWarps * 32) {
+                    const int r = i % kRowBlock, tk = i / kRowBlock;
+                    float s = 0.0f;
+                    for (int q = 0; q < p.splits; ++q)
+                        s += __ldcg(all + (int64_t)q * p.T * kRowBlock + i);
+                    if ((int64_t)rb * kRowBlock + r < p.H)
+                        p.y[tk * p.H + (int64_t)rb * kRowBlock + r] = __float2bfloat16_rn(s);
+                }
+            }
+        }
+        __syncthreads(); // s_flag and the sums have been read
     }
     cp_async_wait<0>();
-    __syncthreads();
-    // the k-warps' arrays into the first ones: [64 rows x T]
-    for (int i = tid; i < kDownRows * p.T; i += kDownWarps * 32) {
-        float s = ysum[i];
-#pragma unroll
-        for (int w = 1; w < kDownKWarps; ++w)
-            s += ysum[w * kDownRows * p.T + i];
-        ysum[i] = s;
-    }
-    cluster_sync();
-    // this CTA's eight rows over the cluster, then y
-    constexpr int kOwn = kDownRows / kDownCluster;
-    const uint32_t yaddr = smem_u32(ysum);
-    for (int i = tid; i < kOwn * p.T; i += kDownWarps * 32) {
-        const int r = rank * kOwn + i % kOwn, tk = i / kOwn;
-        const int64_t col = (int64_t)(blockIdx.x / kDownCluster) * kDownRows + r;
-        float s = 0.0f;
-#pragma unroll
-        for (int c = 0; c < kDownCluster; ++c)
-            s += ld_shared_cluster_f32(mapa_shared(yaddr + 4u * (uint32_t)(r * p.T + tk), c));
-        if (col < p.H)
-            p.y[tk * p.H + col] = __float2bfloat16_rn(s);
-    }
-    __syncwarp();
-    cluster_sync(); // no CTA leaves while another reads its sums
 }
 
-template <typename K>
-cudaError_t launch_pdl(K kernel, dim3 grid, int threads, size_t smem, cudaStream_t s,
-                       const MoeParams &p)
+template <int NT, bool NV, int KS> cudaError_t launch_experts(MoeParams p, cudaStream_t s)
 {
-    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         (int)smem);
+    using U = Layout<NT, NV, KS>;
+    const int lists = (int)moe_lists_bytes(p.T, p.k, p.E);
+    // the x panel: all of H where it fits beside the rings
+    const int room = kMaxSmem - U::kOffX - lists;
+    if (U::x_bytes(p.T, (int)p.H) <= room)
+        p.panel = (int)p.H;
+    else
+        p.panel = (room / (p.T < 8 * NT ? p.T : 8 * NT) - 64) / 2 / kTileK * kTileK;
+    const size_t smem = U::kOffX + U::x_bytes(p.T, p.panel) + lists;
+    auto kernel = moe_experts_kernel<NT, NV, KS>;
+    static std::once_flag flags[64];
+    int dev = 0;
+    cudaGetDevice(&dev);
+    cudaError_t e = cudaSuccess;
+    std::call_once(flags[dev & 63], [&]() {
+        e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxSmem);
+    });
     if (e != cudaSuccess)
         return e;
     cudaLaunchConfig_t cfg{};
-    cfg.gridDim = grid;
-    cfg.blockDim = dim3(threads, 1, 1);
+    cfg.gridDim = dim3((unsigned)num_sms(), 1, 1);
+    cfg.blockDim = dim3(kWarps * 32, 1, 1);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = s;
-    cudaLaunchAttribute at[1];
-    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    at[0].val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchAttribute at[2];
+    at[0].id = cudaLaunchAttributeCooperative; // the CTAs wait for one another: all resident
+    at[0].val.cooperative = 1;
+    at[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[1].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = at;
-    cfg.numAttrs = 1;
+    cfg.numAttrs = 2;
     return cudaLaunchKernelEx(&cfg, kernel, p);
 }
 
-template <int NT, bool NV> cudaError_t launch_experts(MoeParams p, cudaStream_t s)
+// Whether a token panel of 16 whole rows fits.
+template <bool NV> bool wide_fits(const MoeParams &p)
 {
-    using U = UpLayout<NT, NV>;
-    const int lists = (int)moe_lists_bytes(p.T, p.k, p.E);
-    const int cols = p.T < 8 * NT ? p.T : 8 * NT;
-    // the x panel: all of H where it fits beside the rings
-    const int room = (kMaxSmem - U::kOffX - lists) / cols;
-    p.panel = U::x_pitch((int)p.H) <= room ? (int)p.H : (room - 64) / 2 / kTileK * kTileK;
-    cudaError_t e = launch_pdl(moe_up_kernel<NT, NV>, dim3((unsigned)num_sms(), 1, 1),
-                               kUpWarps * 32, U::kOffX + cols * U::x_pitch(p.panel) + lists, s, p);
-    if (e != cudaSuccess)
-        return e;
-    const unsigned groups = (unsigned)((p.H + kDownRows - 1) / kDownRows);
-    return launch_pdl(moe_down_kernel<NT, NV>, dim3(groups * kDownCluster, 1, 1), kDownWarps * 32,
-                      (size_t)kDownWarps * (kDownStages * Tile<NV>::kBytes + 16 * p.T * 4) + lists,
-                      s, p);
+    using U = Layout<2, NV, 2>;
+    return U::kOffX + U::x_bytes(p.T, (int)p.H) + (int)moe_lists_bytes(p.T, p.k, p.E) <=
+           kMaxSmem;
+}
+
+template <bool NV> cudaError_t launch_experts_fmt(const MoeParams &p, cudaStream_t s)
+{
+    if (p.T <= 4)
+        return launch_experts<1, NV, 4>(p, s);
+    // column tiles of 16 where an expert may well meet more than 8 tokens
+    if (p.T > 8 && p.T * p.k > 4 * p.E && wide_fits<NV>(p))
+        return launch_experts<2, NV, 2>(p, s);
+    return launch_experts<1, NV, 2>(p, s);
+}
+
+// CTAs per 64-column block of y.
+int moe_splits(int64_t H)
+{
+    const int64_t nrb = (H + kRowBlock - 1) / kRowBlock;
+    const int64_t s = num_sms() / nrb;
+    return (int)(s < 1 ? 1 : s);
+}
+
+// Workspace: h, its exponents, the splits' sums of y, the arrival counters.
+struct MoeWs {
+    size_t exps, partial, arrived, total;
+};
+
+MoeWs moe_ws(int64_t T, int64_t k, int64_t F, int64_t H)
+{
+    auto align = [](size_t v) { return (v + 255) & ~(size_t)255; };
+    const size_t rows = (size_t)T * (size_t)k, nrb = (size_t)((H + kRowBlock - 1) / kRowBlock);
+    const int splits = moe_splits(H);
+    MoeWs w;
+    w.exps = align(rows * (size_t)F * 2);
+    w.partial = w.exps + align(rows * (size_t)((F / 32 + 7) / 8 * 8));
+    w.arrived = w.partial + (splits > 1 ? align(nrb * splits * (size_t)T * kRowBlock * 4) : 0);
+    w.total = w.arrived + align(nrb * 4);
+    return w;
 }
 
 } // namespace
 
-size_t moe_workspace_bytes(int64_t T, int64_t k, int64_t F)
+size_t moe_workspace_bytes(int64_t T, int64_t k, int64_t F, int64_t H)
 {
-    const size_t rows = (size_t)T * (size_t)k;
-    const size_t h = (rows * (size_t)F * 2 + 255) & ~(size_t)255;
-    return h + rows * (size_t)((F / 32 + 7) / 8 * 8);
+    return moe_ws(T, k, F, H).total;
 }
 
 cudaError_t launch_moe_route(const void *x, const void *w, const float *bias, int64_t T, int64_t H,
@@ -1023,15 +1180,20 @@ cudaError_t launch_moe_experts(const void *x, int64_t T, int64_t H, int64_t F, i
     p.down_codes = down_codes;
     p.down_scales = down_scales;
     p.down_gs = down_gs;
-    p.h = reinterpret_cast<uint4 *>(ws);
-    p.h_exp = reinterpret_cast<uint8_t *>(ws) + (((size_t)T * k * F * 2 + 255) & ~(size_t)255);
+    const MoeWs w = moe_ws(T, k, F, H);
+    uint8_t *b = reinterpret_cast<uint8_t *>(ws);
+    p.h = reinterpret_cast<uint4 *>(b);
+    p.h_exp = b + w.exps;
     p.exp_pitch = (F / 32 + 7) / 8 * 8;
     p.y = reinterpret_cast<__nv_bfloat16 *>(y);
-    // one column tile of 8 tokens per expert, two where an expert may well meet more than that
-    const bool wide = T > 8 && T * k > 4 * (int64_t)E;
-    if (mx)
-        return wide ? launch_experts<2, false>(p, s) : launch_experts<1, false>(p, s);
-    return wide ? launch_experts<2, true>(p, s) : launch_experts<1, true>(p, s);
+    p.splits = moe_splits(H);
+    p.partial = reinterpret_cast<float *>(b + w.partial);
+    p.arrived = reinterpret_cast<int *>(b + w.arrived);
+    p.status = device_status_ptr();
+    p.barrier = grid_barrier_for(s);
+    if (!p.status || !p.barrier)
+        return cudaErrorInvalidValue;
+    return mx ? launch_experts_fmt<false>(p, s) : launch_experts_fmt<true>(p, s);
 }
 
 } // namespace nvfp4

@@ -134,7 +134,7 @@ cudaError_t launch_dequantize_mx(const uint8_t *codes, const uint8_t *lin, int64
 
 // ---- moe.cu --------------------------------------------------------------------------
 constexpr int64_t kMoeMaxTokens = 64, kMoeMaxExperts = 512, kMoeMaxTopK = 32;
-size_t moe_workspace_bytes(int64_t T, int64_t k, int64_t F);
+size_t moe_workspace_bytes(int64_t T, int64_t k, int64_t F, int64_t H);
 cudaError_t launch_moe_route(const void *x, const void *w, const float *bias, int64_t T, int64_t H,
                              int E, int k, int renorm, int *ids, float *weights, cudaStream_t s);
 cudaError_t launch_moe_experts(const void *x, int64_t T, int64_t H, int64_t F, int E, int k,

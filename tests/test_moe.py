@@ -39,9 +39,9 @@ def test_route_refusals(lib):
 
 def test_experts_refusals(lib):
     f = lib.nvfp4_moe_experts
-    ws = lib.nvfp4_workspace_bytes(L.NVFP4_OP_MOE_EXPERTS, 4, 64, 2)
+    ws = lib.nvfp4_moe_workspace_bytes(4, 64, 64, 2)
     assert ws >= 4 * 2 * 64 * 2
-    assert lib.nvfp4_workspace_bytes(L.NVFP4_OP_MOE_EXPERTS, 65, 64, 2) == 0
+    assert lib.nvfp4_moe_workspace_bytes(65, 64, 64, 2) == 0
 
     def call(x=FAKE, T=4, H=64, F=64, E=8, k=2, ids=FAKE, p=FAKE, fmt=1, up=FAKE, ugs=None,
              down=FAKE, dgs=None, y=FAKE, wsp=FAKE, n=ws):
@@ -362,7 +362,7 @@ def test_experts_beside_guard_bytes(cuda):
     x = torch.randn(T, H, device="cuda", generator=gen(3)).bfloat16()
     ids, p = some_ids(T, k, E, 4)
     lib, pad = nv.load(), 256
-    n = lib.nvfp4_workspace_bytes(L.NVFP4_OP_MOE_EXPERTS, T, F, k)
+    n = lib.nvfp4_moe_workspace_bytes(T, H, F, k)
     ws = torch.full((n + 2 * pad,), 0xA5, dtype=torch.uint8, device="cuda")
     y = torch.full((T * H * 2 + 2 * pad,), 0xA5, dtype=torch.uint8, device="cuda")
     st = lib.nvfp4_moe_experts(x.data_ptr(), T, H, F, E, k, ids.data_ptr(), p.data_ptr(), 1,
