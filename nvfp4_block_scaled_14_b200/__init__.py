@@ -19,6 +19,7 @@ device memory and the current stream, nothing else.
 
 The C entry points are also available under their own names (``nvfp4_quantize`` ...).
 """
+import functools
 from dataclasses import dataclass
 
 import torch
@@ -391,40 +392,83 @@ def _scratch(device, nbytes):
     return torch.empty(nbytes, dtype=torch.uint8, device=device) if nbytes else None
 
 
-def _on_device(dev):
-    """The library launches on the current device: make the tensors' device current."""
-    return torch.cuda.device(dev)
+@functools.lru_cache(maxsize=4096)
+def _workspace_size(index, op, m, n, k):
+    """nvfp4_workspace_bytes on device `index` (a function of the sizes and the device)."""
+    with torch.cuda.device(index):
+        return load().nvfp4_workspace_bytes(op, m, n, k)
 
 
-def _check_arrays(what, device, **arrays):
-    """name=(tensor, dtype, shape): every tensor given lies contiguous on `device`, with that type
-    and shape (None: not checked); None tensors are skipped."""
-    for name, (t, dtype, shape) in arrays.items():
-        if t is None:
-            continue
-        if not isinstance(t, torch.Tensor) or not t.is_cuda or t.device != device:
-            raise ValueError(f"{what}: {name} must be a tensor on {device}")
-        if dtype is not None and t.dtype != dtype:
-            raise TypeError(f"{what}: {name} must be {dtype}")
-        if shape is not None and tuple(t.shape) != tuple(shape):
-            raise ValueError(f"{what}: {name} must have shape {tuple(shape)}")
-        if not t.is_contiguous():
-            raise ValueError(f"{what}: {name} must be contiguous")
+@functools.lru_cache(maxsize=4096)
+def _moe_workspace_size(index, T, H, F, k):
+    with torch.cuda.device(index):
+        return load().nvfp4_moe_workspace_bytes(T, H, F, k)
 
 
-def _check_mx(what, q, device, swizzled=False, linear=False):
-    """An MXFP4Tensor's arrays on `device`, large enough for its size, with the scales the call
-    reads."""
+try:  # the integers behind torch.cuda.current_device() / current_stream(), without the objects
+    from torch._C import _cuda_getCurrentRawStream as _raw_stream, _cuda_getDevice as _device_index
+except ImportError:
+    def _raw_stream(index):
+        return torch.cuda.current_stream(index).cuda_stream
+
+    def _device_index():
+        return torch.cuda.current_device()
+
+
+def _launch(what, dev, *args):
+    """The C call `what` on the device's current stream (appended to args), with that device current:
+    the library launches on the current device, which is normally that one already."""
+    f = getattr(load(), what)
+    if _device_index() == dev.index:
+        st = f(*args, _raw_stream(dev.index) or None)
+    else:
+        with torch.cuda.device(dev):
+            st = f(*args, _raw_stream(dev.index) or None)
+    if st:
+        check(st, what)
+
+
+def _bad_array(what, name, t, device, dtype, shape):
+    if not isinstance(t, torch.Tensor) or not t.is_cuda or t.device != device:
+        raise ValueError(f"{what}: {name} must be a tensor on {device}")
+    if dtype is not None and t.dtype != dtype:
+        raise TypeError(f"{what}: {name} must be {dtype}")
+    if shape is not None and tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{what}: {name} must have shape {tuple(shape)}")
+    raise ValueError(f"{what}: {name} must be contiguous")
+
+
+def _check_array(what, name, t, device, dtype, shape):
+    """t (None: nothing to check) lies contiguous on the CUDA device, with that type and shape
+    (None: any)."""
+    if t is not None and not (isinstance(t, torch.Tensor) and t.is_cuda and t.device == device and
+                              (dtype is None or t.dtype == dtype) and
+                              (shape is None or t.shape == shape) and t.is_contiguous()):
+        _bad_array(what, name, t, device, dtype, shape)
+
+
+def _mx_swizzled_bytes(rows, cols):
+    return -(-rows // 128) * 512 * -(-cols // 128)
+
+
+def _check_mx(what, q, device, swizzled=False):
+    """An MXFP4Tensor's arrays on `device`, of its size, with the scales the call reads (operand
+    layout, or linear)."""
     if not isinstance(q, MXFP4Tensor):
         raise TypeError(f"{what} expects MXFP4Tensor operands")
     if q.cols % 32 or q.rows < 0 or q.cols < 0:
         raise ValueError(f"{what}: cols must be a multiple of 32")
-    if (swizzled and q.scales_swz is None) or (linear and q.scales_lin is None):
-        raise ValueError(f"{what} needs the {'swizzled' if swizzled else 'linear'} scales")
-    _check_arrays(what, device, codes=(q.codes, torch.uint8, (q.rows, q.cols // 2)),
-                  scales_swz=(q.scales_swz, torch.uint8,
-                              (load().nvfp4_mxfp4_scales_bytes(q.rows, q.cols, 1),)),
-                  scales_lin=(q.scales_lin, torch.uint8, (q.rows, q.cols // 32)))
+    _check_array(what, "codes", q.codes, device, torch.uint8, (q.rows, q.cols // 2))
+    if swizzled:
+        if q.scales_swz is None:
+            raise ValueError(f"{what} needs the swizzled scales")
+        _check_array(what, "scales_swz", q.scales_swz, device, torch.uint8,
+                     (_mx_swizzled_bytes(q.rows, q.cols),))
+    else:
+        if q.scales_lin is None:
+            raise ValueError(f"{what} needs the linear scales")
+        _check_array(what, "scales_lin", q.scales_lin, device, torch.uint8,
+                     (q.rows, q.cols // 32))
 
 
 def _mx_out(what, out, rows, cols, dtype, device):
@@ -432,16 +476,21 @@ def _mx_out(what, out, rows, cols, dtype, device):
         raise TypeError(f"{what}: out_dtype must be float32 or bfloat16")
     if out is None:
         return torch.empty((rows, cols), dtype=dtype, device=device)
-    _check_arrays(what, device, out=(out, dtype, (rows, cols)))
+    _check_array(what, "out", out, device, dtype, (rows, cols))
     return out
 
 
 def _mx_alloc(rows, cols, device, swizzled, linear):
-    codes = torch.empty((rows, cols // 2), dtype=torch.uint8, device=device)
-    swz = (torch.empty(load().nvfp4_mxfp4_scales_bytes(rows, cols, 1), dtype=torch.uint8,
-                       device=device) if swizzled else None)
-    lin = torch.empty((rows, cols // 32), dtype=torch.uint8, device=device) if linear else None
-    return MXFP4Tensor(codes, swz, lin, rows, cols)
+    """An MXFP4Tensor whose arrays are views of one allocation."""
+    n_codes = rows * (cols // 2)
+    n_swz = _mx_swizzled_bytes(rows, cols) if swizzled else 0
+    buf = torch.empty(n_codes + n_swz + (rows * (cols // 32) if linear else 0),
+                      dtype=torch.uint8, device=device)
+    return MXFP4Tensor(
+        buf.as_strided((rows, cols // 2), (cols // 2, 1)),
+        buf.as_strided((n_swz,), (1,), n_codes) if swizzled else None,
+        buf.as_strided((rows, cols // 32), (cols // 32, 1), n_codes + n_swz) if linear else None,
+        rows, cols)
 
 
 def quantize_mxfp4(x: torch.Tensor, scale_rule: str = "floor", orient: str = "rows",
@@ -467,12 +516,10 @@ def quantize_mxfp4(x: torch.Tensor, scale_rule: str = "floor", orient: str = "ro
     qr = _mx_alloc(rows, cols, x.device, swizzled, linear) if orient != "cols" else None
     qc = _mx_alloc(cols, -(-rows // 32) * 32, x.device, swizzled, linear) \
         if orient != "rows" else None
-    with _on_device(x.device):
-        ptrs = [_ptr(t) for q in (qr, qc)
-                for t in ((q.codes, q.scales_swz, q.scales_lin) if q else (None,) * 3)]
-        st = load().nvfp4_quantize_mxfp4(_ptr(x), _OUT_TYPES[x.dtype], rows, cols,
-                                         _MX_RULES[scale_rule], *ptrs, _stream(x.device))
-    check(st, "nvfp4_quantize_mxfp4")
+    ptrs = [_ptr(t) for q in (qr, qc)
+            for t in ((q.codes, q.scales_swz, q.scales_lin) if q else (None,) * 3)]
+    _launch("nvfp4_quantize_mxfp4", x.device, x.data_ptr(), _OUT_TYPES[x.dtype], rows, cols,
+            _MX_RULES[scale_rule], *ptrs)
     return (qr, qc) if orient == "both" else qr or qc
 
 
@@ -482,12 +529,10 @@ def dequantize_mxfp4(q: MXFP4Tensor, out_dtype=torch.float32,
     if not isinstance(q, MXFP4Tensor):
         raise TypeError("dequantize_mxfp4 expects an MXFP4Tensor")
     dev = q.codes.device
-    _check_mx("dequantize_mxfp4", q, dev, linear=True)
+    _check_mx("dequantize_mxfp4", q, dev)
     out = _mx_out("dequantize_mxfp4", out, q.rows, q.cols, out_dtype, dev)
-    with _on_device(dev):
-        st = load().nvfp4_dequantize_mxfp4(_ptr(q.codes), _ptr(q.scales_lin), q.rows, q.cols,
-                                           _OUT_TYPES[out_dtype], _ptr(out), _stream(dev))
-    check(st, "nvfp4_dequantize_mxfp4")
+    _launch("nvfp4_dequantize_mxfp4", dev, q.codes.data_ptr(), q.scales_lin.data_ptr(), q.rows,
+            q.cols, _OUT_TYPES[out_dtype], out.data_ptr())
     return out
 
 
@@ -507,14 +552,11 @@ def linear_mxfp4(a: MXFP4Tensor, w: MXFP4Tensor, out_dtype=torch.bfloat16,
     M, N, K = a.rows, w.rows, a.cols
     out = _mx_out("linear_mxfp4", out, M, N, out_dtype, dev)
     flags = NVFP4_LINEAR_RESIDENT_WEIGHTS if resident_weights else NVFP4_LINEAR_DEFAULT
-    L = load()
-    with _on_device(dev):
-        ws_bytes = L.nvfp4_workspace_bytes(NVFP4_OP_LINEAR, M, N, K)
-        ws = _scratch(dev, ws_bytes)
-        st = L.nvfp4_linear_mxfp4(_ptr(a.codes), _ptr(a.scales_swz), _ptr(w.codes),
-                                  _ptr(w.scales_swz), M, N, K, _OUT_TYPES[out_dtype], _ptr(out),
-                                  _ptr(ws), ws_bytes, flags, _stream(dev))
-    check(st, "nvfp4_linear_mxfp4")
+    ws_bytes = _workspace_size(dev.index, NVFP4_OP_LINEAR, M, N, K)
+    ws = _scratch(dev, ws_bytes)
+    _launch("nvfp4_linear_mxfp4", dev, a.codes.data_ptr(), a.scales_swz.data_ptr(),
+            w.codes.data_ptr(), w.scales_swz.data_ptr(), M, N, K, _OUT_TYPES[out_dtype],
+            out.data_ptr(), _ptr(ws), ws_bytes, flags)
     return out
 
 
@@ -535,14 +577,11 @@ def linear_dynamic_mxfp4(x: torch.Tensor, w: MXFP4Tensor, out_dtype=torch.bfloat
     N = w.rows
     out = _mx_out("linear_dynamic_mxfp4", out, M, N, out_dtype, dev)
     flags = NVFP4_LINEAR_RESIDENT_WEIGHTS if resident_weights else NVFP4_LINEAR_DEFAULT
-    L = load()
-    with _on_device(dev):
-        ws_bytes = L.nvfp4_workspace_bytes(_lib.NVFP4_OP_LINEAR_DYNAMIC_MXFP4, M, N, K)
-        ws = _scratch(dev, ws_bytes)
-        st = L.nvfp4_linear_dynamic_mxfp4(_ptr(x), _OUT_TYPES[x.dtype], _ptr(w.codes),
-                                          _ptr(w.scales_swz), M, N, K, _OUT_TYPES[out_dtype],
-                                          _ptr(out), _ptr(ws), ws_bytes, flags, _stream(dev))
-    check(st, "nvfp4_linear_dynamic_mxfp4")
+    ws_bytes = _workspace_size(dev.index, _lib.NVFP4_OP_LINEAR_DYNAMIC_MXFP4, M, N, K)
+    ws = _scratch(dev, ws_bytes)
+    _launch("nvfp4_linear_dynamic_mxfp4", dev, x.data_ptr(), _OUT_TYPES[x.dtype],
+            w.codes.data_ptr(), w.scales_swz.data_ptr(), M, N, K, _OUT_TYPES[out_dtype],
+            out.data_ptr(), _ptr(ws), ws_bytes, flags)
     return out
 
 
@@ -587,15 +626,14 @@ def moe_route(x: torch.Tensor, w: torch.Tensor, top_k: int, bias: torch.Tensor =
     x, w = x.contiguous(), w.contiguous()
     T, H = x.shape
     E = w.shape[0]
-    _check_arrays("moe_route", dev, w=(w, None, (E, H)), bias=(bias, torch.float32, (E,)))
+    _check_array("moe_route", "w", w, dev, None, (E, H))
+    _check_array("moe_route", "bias", bias, dev, torch.float32, (E,))
     if not 1 <= top_k <= min(E, 32):
         raise ValueError("moe_route: top_k must be 1..min(experts, 32)")
     ids = torch.empty((T, top_k), dtype=torch.int32, device=dev)
     weights = torch.empty((T, top_k), dtype=torch.float32, device=dev)
-    with _on_device(dev):
-        st = load().nvfp4_moe_route(_ptr(x), _ptr(w), _ptr(bias), T, H, E, top_k,
-                                    int(renormalize), _ptr(ids), _ptr(weights), _stream(dev))
-    check(st, "nvfp4_moe_route")
+    _launch("nvfp4_moe_route", dev, x.data_ptr(), w.data_ptr(), _ptr(bias), T, H, E, top_k,
+            int(renormalize), ids.data_ptr(), weights.data_ptr())
     return ids, weights
 
 
@@ -628,29 +666,26 @@ def moe_experts(x: torch.Tensor, ids: torch.Tensor, weights: torch.Tensor,
     mx = gate_up.global_scale is None
     b = 32 if mx else 16
     u8 = torch.uint8
-    _check_arrays("moe_experts", dev, ids=(ids, torch.int32, (T, k)),
-                  weights=(weights, torch.float32, (T, k)),
-                  gate_up_codes=(gate_up.codes, u8, (E, 2 * F, H // 2)),
-                  gate_up_scales=(gate_up.scales, u8, (E, 2 * F, H // b)),
-                  gate_up_global_scale=(gate_up.global_scale, torch.float32, (E,)),
-                  down_codes=(down.codes, u8, (E, H, F // 2)),
-                  down_scales=(down.scales, u8, (E, H, F // b)),
-                  down_global_scale=(down.global_scale, torch.float32, (E,)))
+    for name, t, dtype, shape in (
+            ("ids", ids, torch.int32, (T, k)), ("weights", weights, torch.float32, (T, k)),
+            ("gate_up codes", gate_up.codes, u8, (E, 2 * F, H // 2)),
+            ("gate_up scales", gate_up.scales, u8, (E, 2 * F, H // b)),
+            ("gate_up global_scale", gate_up.global_scale, torch.float32, (E,)),
+            ("down codes", down.codes, u8, (E, H, F // 2)),
+            ("down scales", down.scales, u8, (E, H, F // b)),
+            ("down global_scale", down.global_scale, torch.float32, (E,))):
+        _check_array("moe_experts", name, t, dev, dtype, shape)
     if out is None:
         out = torch.empty((T, H), dtype=torch.bfloat16, device=dev)
     else:
-        _check_arrays("moe_experts", dev, out=(out, torch.bfloat16, (T, H)))
-    L = load()
-    with _on_device(dev):
-        ws_bytes = L.nvfp4_moe_workspace_bytes(T, H, F, k)
-        ws = _scratch(dev, ws_bytes)
-        st = L.nvfp4_moe_experts(_ptr(x), T, H, F, E, k, _ptr(ids), _ptr(weights),
-                                 _lib.NVFP4_EXPERTS_MXFP4 if mx else _lib.NVFP4_EXPERTS_NVFP4,
-                                 _ptr(gate_up.codes), _ptr(gate_up.scales),
-                                 _ptr(gate_up.global_scale), _ptr(down.codes), _ptr(down.scales),
-                                 _ptr(down.global_scale), _ptr(out), _ptr(ws), ws_bytes,
-                                 _stream(dev))
-    check(st, "nvfp4_moe_experts")
+        _check_array("moe_experts", "out", out, dev, torch.bfloat16, (T, H))
+    ws_bytes = _moe_workspace_size(dev.index, T, H, F, k)
+    ws = _scratch(dev, ws_bytes)
+    _launch("nvfp4_moe_experts", dev, x.data_ptr(), T, H, F, E, k, ids.data_ptr(),
+            weights.data_ptr(), _lib.NVFP4_EXPERTS_MXFP4 if mx else _lib.NVFP4_EXPERTS_NVFP4,
+            gate_up.codes.data_ptr(), gate_up.scales.data_ptr(), _ptr(gate_up.global_scale),
+            down.codes.data_ptr(), down.scales.data_ptr(), _ptr(down.global_scale),
+            out.data_ptr(), _ptr(ws), ws_bytes)
     return out
 
 

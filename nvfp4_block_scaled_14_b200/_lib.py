@@ -119,6 +119,8 @@ def lib_path() -> str:
 def load():
     """Build (if missing or stale) and load libnvfp4.so; raise if that is impossible."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is None:
             path = _build.build()

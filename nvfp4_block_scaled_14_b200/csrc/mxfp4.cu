@@ -11,6 +11,8 @@
 // side keeps the tile in shared memory; a thread takes 32 rows of two adjacent bf16 columns (of
 // one fp32 column), reading words that are contiguous across the warp, and the codes go through
 // shared memory so that they leave as whole 64-byte row pieces.
+#include <mutex>
+
 #include "mxfp4_encode.cuh"
 #include "nvfp4_internal.cuh"
 
@@ -229,9 +231,14 @@ cudaError_t launch_mx_quantize_t(const MxQuantParams &p, unsigned grid, cudaStre
 {
     const int smem = COLS ? kTile * kTile * (BF16 ? 2 : 4) + kTile * kColPitch : 0;
     if (COLS && !BF16) {
-        const cudaError_t e = cudaFuncSetAttribute(mx_quantize_kernel<BF16, ROWS, COLS>,
-                                                   cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                                   smem);
+        static std::once_flag flags[64];
+        int dev = 0;
+        cudaGetDevice(&dev);
+        cudaError_t e = cudaSuccess;
+        std::call_once(flags[dev & 63], [&]() {
+            e = cudaFuncSetAttribute(mx_quantize_kernel<BF16, ROWS, COLS>,
+                                     cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+        });
         if (e != cudaSuccess)
             return e;
     }
