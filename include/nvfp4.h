@@ -423,7 +423,7 @@ nvfp4_status nvfp4_linear_dynamic_mxfp4(const void *x, nvfp4_dtype x_dt, const u
 
 /*
  * Router of a mixture-of-experts layer: z = x . W^T + bias (x: T x H bf16, W: E x H bf16, bias:
- * E fp32 or NULL; bf16 products summed in fp32 in groups of eight and in fp64 above), and for
+ * E fp32 or NULL; products summed in fp32 in blocks of 32 and in fp64 above), and for
  * each token the top_k largest z in decreasing order, equal ones by the lower expert:
  *   ids[t, s]     the expert (int32);
  *   weights[t, s] its softmax weight (fp32): exp(z) over the sum of exp(z) of the chosen experts

@@ -45,82 +45,108 @@ struct RouteParams {
     float *weights;     // [T x k]
 };
 
-// Sum of the eight products of two 16-byte bf16 vectors: exact products, fp32 sums.
-__device__ __forceinline__ float dot8(const uint4 &a, const float (&x)[8])
-{
-    const uint32_t u[4] = {a.x, a.y, a.z, a.w};
-    float s = 0.0f;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        s = fmaf(__uint_as_float(u[i] << 16), x[2 * i], s);
-        s = fmaf(__uint_as_float(u[i] & 0xFFFF0000u), x[2 * i + 1], s);
-    }
-    return s;
-}
-
 __device__ __forceinline__ void st_cluster_f64(uint32_t addr, double v)
 {
     asm volatile("st.shared::cluster.f64 [%0], %1;" ::"r"(addr), "d"(v) : "memory");
 }
 
-// A cluster of 8 CTAs takes TG tokens: its warps share the experts out, one logit per expert and
-// token by a warp (eight-term fp32 sums added up in fp64, so that the choice between two close
-// experts does not hang on the order of a long sum), sent to the CTA that ranks the token.
-// Expert e is chosen if fewer than k experts precede it: rank by counting, every thread at once.
-template <int TG>
+// c = A B (16 x 8, K 16, bf16), and c += A B.
+__device__ __forceinline__ void mma_bf16_first(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
+                                               uint32_t a3, uint32_t b0, uint32_t b1)
+{
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, "
+        "{%4, %5, %6, %7}, {%8, %9}, {%10, %10, %10, %10};"
+        : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.0f));
+}
+
+__device__ __forceinline__ void mma_bf16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
+                                         uint32_t a3, uint32_t b0, uint32_t b1)
+{
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, "
+        "{%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// A cluster of 8 CTAs takes 8 tokens. Logits: 16 experts are the rows of bf16 MMAs, the tokens the
+// columns; a CTA takes chunks of 16 experts (with few chunks, a slice of K too), its warps every
+// eighth 32-wide block of K. Each block's 32 products are summed in fp32 by two MMAs and the blocks
+// in fp64, so that the choice between two close experts does not hang on the order of a long sum.
+// The logits go to the CTA that ranks the token: expert e is chosen if fewer than k experts precede
+// it, counted by every thread at once. Bound by the latency of one round of loads (W is 1 MB at 128
+// experts of 4096) and of the cluster barrier.
 __global__ void __cluster_dims__(kRouteCluster, 1, 1) __launch_bounds__(kRouteThreads)
     moe_route_kernel(const RouteParams p)
 {
-    extern __shared__ __align__(16) double s_z[]; // [E], this CTA's token
+    __shared__ double s_z[512];           // [slice][expert], then [expert]: this CTA's token
+    __shared__ double s_part[8][16 * 8];  // [warp][expert][token]
     __shared__ int s_sel[32];
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const uint32_t rank = cluster_ctarank();
-    const int64_t t0 = (int64_t)(blockIdx.x / kRouteCluster) * TG;
-    const int64_t nvec = p.H >> 3;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
+    const int rank = (int)cluster_ctarank();
+    const int64_t t0 = (int64_t)(blockIdx.x / kRouteCluster) * 8;
     cluster_arrive(); // matched below: every CTA of the cluster runs before remote stores
-    pdl_wait();
-    cluster_wait();
+    const int chunks = (p.E + 15) / 16;
+    const int slices = chunks == 1 ? 8 : chunks == 2 ? 4 : chunks <= 4 ? 2 : 1;
+    const int per = kRouteCluster / slices; // CTAs per slice of K
+    const int slice = rank / per;
+    const int64_t nvec = p.H >> 3;
+    const int nblk = (int)(p.H >> 5);
+    const int b0 = (int)((int64_t)nblk * slice / slices);
+    const int b1 = (int)((int64_t)nblk * (slice + 1) / slices);
     const uint32_t zaddr = smem_u32(s_z);
-    for (int e = (int)rank * 8 + warp; e < p.E; e += 8 * kRouteCluster) {
-        double acc[TG];
+    pdl_wait();
+    const int64_t tok = t0 + g < p.T ? t0 + g : p.T - 1;
+    for (int c = rank % per; c < chunks; c += per) {
+        const uint4 *wa = p.w + (int64_t)min(c * 16 + g, p.E - 1) * nvec + t;
+        const uint4 *wb = p.w + (int64_t)min(c * 16 + g + 8, p.E - 1) * nvec + t;
+        const uint4 *xr = p.x + tok * nvec + t;
+        double acc[4] = {0.0, 0.0, 0.0, 0.0};
+#pragma unroll 8
+        for (int b = b0 + warp; b < b1; b += 8) {
+            const uint4 a = __ldg(wa + 4 * b), d = __ldg(wb + 4 * b), x = __ldg(xr + 4 * b);
+            float f[4]; // lane t's k indices: its 8 values of the block, whatever their order
+            mma_bf16_first(f, a.x, d.x, a.y, d.y, x.x, x.y);
+            mma_bf16(f, a.z, d.z, a.w, d.w, x.z, x.w);
 #pragma unroll
-        for (int j = 0; j < TG; ++j)
-            acc[j] = 0.0;
-#pragma unroll 4
-        for (int64_t i = lane; i < nvec; i += 32) {
-            const uint4 a = __ldg(p.w + (int64_t)e * nvec + i);
-#pragma unroll
-            for (int j = 0; j < TG; ++j) {
-                if (t0 + j < p.T) {
-                    const uint4 v = __ldg(p.x + (t0 + j) * nvec + i);
-                    const float xf[8] = {
-                        __uint_as_float(v.x << 16), __uint_as_float(v.x & 0xFFFF0000u),
-                        __uint_as_float(v.y << 16), __uint_as_float(v.y & 0xFFFF0000u),
-                        __uint_as_float(v.z << 16), __uint_as_float(v.z & 0xFFFF0000u),
-                        __uint_as_float(v.w << 16), __uint_as_float(v.w & 0xFFFF0000u)};
-                    acc[j] += (double)dot8(a, xf);
-                }
-            }
+            for (int j = 0; j < 4; ++j)
+                acc[j] += (double)f[j];
         }
 #pragma unroll
-        for (int j = 0; j < TG; ++j) {
+        for (int j = 0; j < 4; ++j)
+            s_part[warp][(g + (j >> 1) * 8) * 8 + 2 * t + (j & 1)] = acc[j];
+        __syncthreads();
+        if (c < per)
+            cluster_wait(); // (the first chunk) the other CTAs have started
+        if (tid < 128) {
+            const int e = c * 16 + (tid >> 3), j = tid & 7;
+            double z = 0.0;
 #pragma unroll
-            for (int o = 16; o > 0; o >>= 1)
-                acc[j] += __shfl_xor_sync(0xFFFFFFFFu, acc[j], o);
-            double z = acc[j] + (p.bias ? (double)__ldg(p.bias + e) : 0.0);
-            if (!(z == z))
-                z = -INFINITY; // a NaN logit is never chosen
-            if (lane == 0)
-                st_cluster_f64(mapa_shared(zaddr + 8u * (uint32_t)e, (uint32_t)j), z);
+            for (int w = 0; w < 8; ++w)
+                z += s_part[w][tid];
+            if (e < p.E)
+                st_cluster_f64(mapa_shared(zaddr + 8u * (uint32_t)(slice * p.E + e), (uint32_t)j),
+                               z);
         }
+        __syncthreads();
     }
+    if (rank % per >= chunks)
+        cluster_wait();
     cluster_sync(); // this CTA's token has all its logits
     pdl_launch_dependents();
-    const int64_t t = t0 + rank;
-    if (rank >= TG || t >= p.T)
+    const int64_t tk = t0 + rank;
+    if (tk >= p.T)
         return;
     if (tid < 32)
         s_sel[tid] = -1;
+    for (int e = tid; e < p.E; e += kRouteThreads) {
+        double z = s_z[e];
+        for (int q = 1; q < slices; ++q)
+            z += s_z[q * p.E + e];
+        if (p.bias)
+            z += (double)__ldg(p.bias + e);
+        s_z[e] = z == z ? z : -INFINITY; // a NaN logit is never chosen
+    }
     __syncthreads();
     // parts threads share an expert's count (E <= 64: 4, <= 128: 2)
     const int parts = p.E <= 64 ? 4 : p.E <= 128 ? 2 : 1;
@@ -159,8 +185,8 @@ __global__ void __cluster_dims__(kRouteCluster, 1, 1) __launch_bounds__(kRouteTh
         for (int o = 16; o > 0; o >>= 1)
             sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
         if (lane < p.k) {
-            p.ids[t * p.k + lane] = e;
-            p.weights[t * p.k + lane] = e >= 0 ? v / sum : 0.0f;
+            p.ids[tk * p.k + lane] = e;
+            p.weights[tk * p.k + lane] = e >= 0 ? v / sum : 0.0f;
         }
     }
 }
@@ -1141,21 +1167,15 @@ cudaError_t launch_moe_route(const void *x, const void *w, const float *bias, in
     RouteParams p{reinterpret_cast<const uint4 *>(x), reinterpret_cast<const uint4 *>(w), bias, T,
                   H, E, k, renorm, ids, weights};
     cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3((unsigned)((T + 7) / 8 * kRouteCluster), 1, 1);
     cfg.blockDim = dim3(kRouteThreads, 1, 1);
-    cfg.dynamicSmemBytes = (size_t)E * 8;
     cfg.stream = s;
     cudaLaunchAttribute at[1];
     at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     at[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = at;
     cfg.numAttrs = 1;
-    const int tg = T <= 16 ? 1 : T <= 32 ? 2 : 4;
-    cfg.gridDim = dim3((unsigned)((T + tg - 1) / tg * kRouteCluster), 1, 1);
-    if (tg == 1)
-        return cudaLaunchKernelEx(&cfg, moe_route_kernel<1>, p);
-    if (tg == 2)
-        return cudaLaunchKernelEx(&cfg, moe_route_kernel<2>, p);
-    return cudaLaunchKernelEx(&cfg, moe_route_kernel<4>, p);
+    return cudaLaunchKernelEx(&cfg, moe_route_kernel, p);
 }
 
 cudaError_t launch_moe_experts(const void *x, int64_t T, int64_t H, int64_t F, int E, int k,

@@ -112,7 +112,8 @@ def check_route(x, w, k, bias=None, renorm=True):
     ref_ids, ref = route_reference(x, w, k, bias, renorm)
     assert ids.dtype == torch.int32 and p.dtype == torch.float32
     assert torch.equal(ids, ref_ids)
-    # A logit is off by the eight-term fp32 sums, 8 * 2^-24 of the sum of its products' sizes (S),
+    # A logit is off by its 32-term fp32 sums, two MMAs each off by at most two units in the last
+    # place (2^-22) of its terms' sizes, 8 * 2^-24 of the sum of the products' sizes (S) in all,
     # and by the rounding of z - max to fp32 (2^-24 of at most 2 S'); an exponential turns an
     # absolute error d into a relative one of d, twice (numerator and denominator); expf and the
     # division add 2^-22, the sum of up to 512 terms 2^-24 a term in the worst order.
