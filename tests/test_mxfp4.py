@@ -229,6 +229,11 @@ def test_dequantize_all_bytes(cuda, rows, cols, out):
     ref = torch.from_numpy(R.values(codes.numpy(), s.numpy())).float().to(out)
     assert torch.equal(got.cpu().nan_to_num(nan=123.0, posinf=9e37, neginf=-9e37),
                        ref.nan_to_num(nan=123.0, posinf=9e37, neginf=-9e37))
+    # an output that is aligned to 16 bytes only
+    n = 16 // got.element_size()
+    off = torch.empty(rows * cols + n, dtype=out, device="cuda")[n:].view(rows, cols)
+    assert torch.equal(nv.dequantize_mxfp4(q, out, out=off).view(torch.uint8),
+                       got.view(torch.uint8))
 
 
 # ---- products (GPU) --------------------------------------------------------------------------
