@@ -3,25 +3,18 @@
 //
 // Router: z = x . Wr^T + bias, the k largest of each token's z (equal ones: the lower expert
 // first), their softmax weights. Experts: y_t = sum_k w[t,k] * Wd_e (silu(Wg_e x_t) * (Wu_e x_t))
-// with e = ids[t,k]. With at most 64 tokens the cost is reading the met experts' weights once, so
-// the activations stay in 16 bits: nothing is lost to quantizing them and the weights' bytes, not
-// the products, bound the time.
+// with e = ids[t,k]. With at most 64 tokens the cost is reading the met experts' weights once.
 //
-// The products run on warp-level tensor-core MMAs (m16n8k16, f16 inputs, fp32 sums): the weights
-// are the 16-row side, a column tile is 8 tokens of one expert. An E2M1 code is exact in f16; the
-// block scales are applied to each block's fp32 partial sum, so weights lose nothing. The
-// activations are scaled by a power of two per 32 values to a largest magnitude in [1, 2) (or
-// [2, 4)) before they become f16: a bf16 value keeps its 8 bits down to 2^-14 of its block's
-// largest and is off by at most 2^-25 of that below. The gate/up result is rounded to f16 (11
-// bits) with such a block exponent, which adds 2^-12 relative to the down product's inputs, a
-// sixteenth of the final bf16 rounding's 2^-8... see moe_up_kernel for where.
-//
-// A k order that suits the loads: an MMA sums 16 products whatever their order, so lane t of a
-// quad takes 4 consecutive code bytes of a 32-code block (8 values, MXFP4; 2 + 2 bytes of the two
-// 16-code blocks, NVFP4) as its k indices, and the same 8 activations, 16 bytes, of its column.
+// The weights go to the FP4 tensor cores as they are stored. Those multiply FP4 by FP4 only, so an
+// activation is split into eight FP4 terms, each the FP4 form of what the ones before leave
+// (write_terms), and the eight products are added: the weights lose nothing and the activations
+// about 2^-18 of their block's largest value, while the terms' columns cost the otherwise idle MMA
+// 8 of its up to 256 columns a token. (Decoding the weights to f16 on the CUDA cores for mma.sync
+// took 40-54 issue slots per 16 x 32 codes, as long as HBM takes to deliver them, and ran at a
+// quarter of it: 64 tokens, 64 experts of 2048 x 1024, top 8: 135 us.)
 #include <mutex>
 
-#include "grid_exchange.cuh"
+#include "fp4_format.cuh"
 #include "mxfp4_encode.cuh"
 #include "nvfp4_internal.cuh"
 #include "sm100_ptx.cuh"
@@ -195,95 +188,77 @@ __global__ void __cluster_dims__(kRouteCluster, 1, 1) __launch_bounds__(kRouteTh
 // Experts
 // ---------------------------------------------------------------------------------------
 
-struct MoeParams {
-    const uint4 *x; // bf16 [T x H]
-    int T, k, E;
-    int64_t H, F;
-    const int *ids;
-    const float *weights;
-    const uint8_t *up_codes, *up_scales;     // [E][2F][H/2], [E][2F][H/block]
-    const uint8_t *down_codes, *down_scales; // [E][H][F/2], [E][H][F/block]
-    const float *up_gs, *down_gs;            // [E] (NVFP4)
-    uint4 *h;        // f16 [rows][F]: silu(gate) * up of each (expert, token) pair, scaled
-    uint8_t *h_exp;  // [rows][exp_pitch]: biased exponent of each 32-block's scale
-    int64_t exp_pitch;
-    __nv_bfloat16 *y; // [T x H]
-    int panel;        // values of a token kept in shared memory at a time
-    int splits;       // CTAs that share a 64-column block of y
-    float *partial;   // [64-column blocks][splits][T][64] sums of each (splits > 1)
-    int *arrived;     // [64-column blocks] CTAs whose sums are in place
-    GridBarrier *barrier;
-    int *status;
+constexpr int kTerms = 8;  // FP4 terms of an activation: the rows of one swizzle atom
+constexpr int kCols = 16;  // tokens of a column tile: 128 MMA columns
+constexpr int kUpRows = 64, kDownRows = 128; // rows of F, of H, per tile
+
+// A column tile: up to kCols of the (expert, token) rows of one expert. Packed: 9 bits of expert, 11
+// of row, 4 of columns - 1.
+struct MoeUnit {
+    int expert, row0, ncol;
 };
 
-// What the ids say, in shared memory: for each expert the set of its tokens; the (expert, token)
-// pairs in expert order as rows, with the row's token and weight (an expert that a token names
-// twice gets one row with both weights); and the column tiles, up to cols rows of one expert each.
-// ids outside [0, E) name no expert.
-struct MoeLists {
-    uint32_t *mask;   // [E][2]
-    int *base;        // [E] first row of each expert
-    float *wt;        // [rows]
-    int *n_units;
-    uint16_t *unit;   // [tiles] expert | first column of the tile << 9
-    int16_t *ids;     // [T k], -1: no expert
-    uint8_t *tok;     // [rows]
+__device__ __forceinline__ uint32_t pack_unit(int expert, int row0, int ncol)
+{
+    return (uint32_t)expert | (uint32_t)row0 << 9 | (uint32_t)(ncol - 1) << 20;
+}
+
+__device__ __forceinline__ MoeUnit unpack_unit(uint32_t u)
+{
+    return MoeUnit{(int)(u & 0x1FFu), (int)(u >> 9 & 0x7FFu), (int)(u >> 20) + 1};
+}
+
+// What the kernels of one call share in the workspace.
+struct MoeShared {
+    uint8_t *x_codes, *x_scales; // terms of x: [T * 8][H / 2], [T * 8][x_pitch]
+    float *x_factor;             // [T] (NVFP4): the power of two a token was divided by
+    int64_t x_pitch;
+    float *h;                    // [rows][F]: silu(gate) * up of each (expert, token) row
+    uint8_t *h_codes, *h_scales; // its terms
+    float *h_factor;
+    int64_t h_pitch;
+    uint32_t *units;
+    int *counts;                 // column tiles, rows
+    uint8_t *tok;                // [rows] token
+    float *wt;                   // [rows] weight
+    float *partial;              // [128-row blocks of y][splits][T][128]
 };
 
-__host__ __device__ inline size_t moe_lists_bytes(int T, int k, int E)
+// ---- lists and terms ----------------------------------------------------------------------
+
+constexpr int kPrepThreads = 512, kTermThreads = 256;
+
+// The (expert, token) pairs that the ids name, in expert order, as rows: the row's token and weight
+// (an expert that a token names twice gets one row with both weights), and the column tiles. ids
+// outside [0, E) name no expert. One CTA.
+__device__ __forceinline__ void build_lists(const MoeShared &sh, const int *ids,
+                                            const float *weights, int T, int k, int E,
+                                            uint8_t *smem)
 {
-    const size_t n = (size_t)T * k;
-    return (12 * (size_t)E + 9 * n + 4 + 15) / 16 * 16;
-}
-
-__device__ __forceinline__ MoeLists moe_lists(uint8_t *s, int T, int k, int E)
-{
-    const int n = T * k;
-    MoeLists l;
-    l.mask = reinterpret_cast<uint32_t *>(s);
-    l.base = reinterpret_cast<int *>(l.mask + 2 * E);
-    l.wt = reinterpret_cast<float *>(l.base + E);
-    l.n_units = reinterpret_cast<int *>(l.wt + n);
-    l.unit = reinterpret_cast<uint16_t *>(l.n_units + 1);
-    l.ids = reinterpret_cast<int16_t *>(l.unit + n);
-    l.tok = reinterpret_cast<uint8_t *>(l.ids + n);
-    return l;
-}
-
-__device__ __forceinline__ int mask_count(const uint32_t *m) { return __popc(m[0]) + __popc(m[1]); }
-
-// Rows of the expert's tokens before token t.
-__device__ __forceinline__ int mask_before(const uint32_t *m, int t)
-{
-    return t < 32 ? __popc(m[0] & ((1u << t) - 1u))
-                  : __popc(m[0]) + __popc(m[1] & ((1u << (t - 32)) - 1u));
-}
-
-__device__ __forceinline__ int unit_expert(uint32_t u) { return (int)(u & 0x1FFu); }
-__device__ __forceinline__ int unit_column(uint32_t u) { return (int)(u >> 9); }
-
-__device__ __forceinline__ void build_lists(const MoeLists &l, const MoeParams &p, int cols)
-{
-    const int tid = threadIdx.x, nthr = blockDim.x, n = p.T * p.k;
-    for (int i = tid; i < 2 * p.E; i += nthr)
-        l.mask[i] = 0u;
+    uint32_t *mask = reinterpret_cast<uint32_t *>(smem); // [E][2]: the expert's tokens
+    int *base = reinterpret_cast<int *>(mask + 2 * E);   // [E]: its first row
+    int16_t *s_ids = reinterpret_cast<int16_t *>(base + E);
+    const int tid = threadIdx.x, nthr = blockDim.x, n = T * k;
+    auto count = [&](int e) { return __popc(mask[2 * e]) + __popc(mask[2 * e + 1]); };
+    for (int i = tid; i < 2 * E; i += nthr)
+        mask[i] = 0u;
     __syncthreads();
     for (int i = tid; i < n; i += nthr) {
-        const int e = __ldg(p.ids + i), t = i / p.k;
-        const bool on = e >= 0 && e < p.E;
-        l.ids[i] = on ? (int16_t)e : (int16_t)-1;
+        const int e = __ldg(ids + i), t = i / k;
+        const bool on = e >= 0 && e < E;
+        s_ids[i] = on ? (int16_t)e : (int16_t)-1;
         if (on)
-            atomicOr(&l.mask[2 * e + (t >> 5)], 1u << (t & 31));
+            atomicOr(&mask[2 * e + (t >> 5)], 1u << (t & 31));
     }
     __syncthreads();
     if (tid < 32) { // exclusive prefix of rows and of tiles over the experts
-        const int per = (p.E + 31) / 32;
+        const int per = (E + 31) / 32;
         int rows = 0, tiles = 0;
         for (int q = 0; q < per; ++q) {
             const int e = tid * per + q;
-            const int c = e < p.E ? mask_count(l.mask + 2 * e) : 0;
+            const int c = e < E ? count(e) : 0;
             rows += c;
-            tiles += (c + cols - 1) / cols;
+            tiles += (c + kCols - 1) / kCols;
         }
         int r0 = rows, u0 = tiles;
 #pragma unroll
@@ -295,863 +270,845 @@ __device__ __forceinline__ void build_lists(const MoeLists &l, const MoeParams &
                 u0 += b;
             }
         }
-        if (tid == 31)
-            *l.n_units = u0;
+        if (tid == 31) {
+            sh.counts[0] = u0;
+            sh.counts[1] = r0;
+        }
         r0 -= rows;
         u0 -= tiles;
         for (int q = 0; q < per; ++q) {
             const int e = tid * per + q;
-            if (e >= p.E)
+            if (e >= E)
                 break;
-            const int c = mask_count(l.mask + 2 * e);
-            l.base[e] = r0;
-            for (int c0 = 0; c0 < c; c0 += cols)
-                l.unit[u0++] = (uint16_t)(e | c0 << 9);
+            const int c = count(e);
+            base[e] = r0;
+            for (int c0 = 0; c0 < c; c0 += kCols)
+                sh.units[u0++] = pack_unit(e, r0 + c0, min(kCols, c - c0));
             r0 += c;
         }
     }
     __syncthreads();
     for (int i = tid; i < n; i += nthr) {
-        const int e = l.ids[i], t = i / p.k;
+        const int e = s_ids[i], t = i / k;
         if (e < 0)
             continue;
         bool first = true; // of the token's slots that name e
         float w = 0.0f;
-        for (int s = t * p.k; s < (t + 1) * p.k; ++s)
-            if (l.ids[s] == e) {
+        for (int s = t * k; s < (t + 1) * k; ++s)
+            if (s_ids[s] == e) {
                 first = first && s >= i;
-                w += __ldg(p.weights + s);
+                w += __ldg(weights + s);
             }
         if (first) {
-            const int row = l.base[e] + mask_before(l.mask + 2 * e, t);
-            l.tok[row] = (uint8_t)t;
-            l.wt[row] = w;
+            const uint32_t *m = mask + 2 * e;
+            const int before = t < 32 ? __popc(m[0] & ((1u << t) - 1u))
+                                      : __popc(m[0]) + __popc(m[1] & ((1u << (t - 32)) - 1u));
+            const int row = base[e] + before;
+            sh.tok[row] = (uint8_t)t;
+            sh.wt[row] = w;
         }
     }
-    __syncthreads();
 }
 
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void *src)
+size_t lists_smem(int T, int k, int E) { return 12 * (size_t)E + 2 * (size_t)T * k; }
+
+// One row of activations (load(i): values 4i .. 4i + 3) as kTerms FP4 rows: each term is the FP4
+// form of what the terms before leave, so that the sum of the terms is the value up to the last
+// remainder. MXFP4 terms have their own E8M0 scale per 32 values ("ceil": nothing saturates; a
+// rounding is off by at most 1/5 of the block's largest remainder, 5^-8 = 2^-18.6 in all). NVFP4
+// terms have an E4M3 scale per 16 values, of the row divided by a power of two that brings its
+// largest value to 1344..2688 (off by at most 1/6 + 1/16 of the block's largest remainder a term,
+// down to the smallest scale's 2^-18 of the row's largest value). A row with a NaN or an infinity
+// gets NaN scales (MXFP4) or a NaN factor, and so NaN results. Eight lanes take 32 values.
+template <bool NV, int THREADS, typename Load>
+__device__ __forceinline__ void write_terms(int64_t cols, uint8_t *codes, uint8_t *scales,
+                                            int64_t pitch, float *factor, Load load)
 {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst),
-                 "l"(reinterpret_cast<uint64_t>(src))
-                 : "memory");
-}
-
-__device__ __forceinline__ void cp_async4(uint32_t dst, const void *src)
-{
-    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst),
-                 "l"(reinterpret_cast<uint64_t>(src))
-                 : "memory");
-}
-
-__device__ __forceinline__ void cp_async_commit()
-{
-    asm volatile("cp.async.commit_group;" ::: "memory");
-}
-
-template <int N> __device__ __forceinline__ void cp_async_wait()
-{
-    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
-}
-
-// Lane t's four code bytes of the 32-code block at `a`: bytes 4t.. (MXFP4), or bytes 2t, 2t + 1 of
-// each of its two 16-code blocks (NVFP4).
-template <bool NV> __device__ __forceinline__ uint32_t lane_codes(const uint8_t *a, int t)
-{
-    const uint32_t *w = reinterpret_cast<const uint32_t *>(a);
-    if constexpr (NV)
-        return __byte_perm(w[t >> 1], w[2 + (t >> 1)], (t & 1) ? 0x7632 : 0x5410);
-    else
-        return w[t];
-}
-
-// Code byte i of a word -> its two values as f16x2 (exact).
-template <int I> __device__ __forceinline__ uint32_t e2m1x2_to_f16x2(uint32_t w)
-{
-    uint32_t h;
-    if constexpr (I == 0)
-        asm("{\n\t.reg .b8 b0, b1, b2, b3;\n\tmov.b32 {b0, b1, b2, b3}, %1;\n\t"
-            "cvt.rn.f16x2.e2m1x2 %0, b0;\n\t}" : "=r"(h) : "r"(w));
-    else if constexpr (I == 1)
-        asm("{\n\t.reg .b8 b0, b1, b2, b3;\n\tmov.b32 {b0, b1, b2, b3}, %1;\n\t"
-            "cvt.rn.f16x2.e2m1x2 %0, b1;\n\t}" : "=r"(h) : "r"(w));
-    else if constexpr (I == 2)
-        asm("{\n\t.reg .b8 b0, b1, b2, b3;\n\tmov.b32 {b0, b1, b2, b3}, %1;\n\t"
-            "cvt.rn.f16x2.e2m1x2 %0, b2;\n\t}" : "=r"(h) : "r"(w));
-    else
-        asm("{\n\t.reg .b8 b0, b1, b2, b3;\n\tmov.b32 {b0, b1, b2, b3}, %1;\n\t"
-            "cvt.rn.f16x2.e2m1x2 %0, b3;\n\t}" : "=r"(h) : "r"(w));
-    return h;
-}
-
-// c = A B (16 x 8, K 16), and c += A B.
-__device__ __forceinline__ void mma_f16_first(float (&c)[4], const uint32_t (&a)[4], uint32_t b0,
-                                              uint32_t b1)
-{
-    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, "
-                 "{%4, %5, %6, %7}, {%8, %9}, {%10, %10, %10, %10};"
-                 : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
-                 : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.0f));
-}
-
-__device__ __forceinline__ void mma_f16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0,
-                                        uint32_t b1)
-{
-    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, "
-                 "{%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
-                 : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-                 : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-}
-
-__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi)
-{
-    uint32_t d;
-    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(hi), "f"(lo));
-    return d;
-}
-
-// Biased exponent of the power of two that a block of largest magnitude m (fp32 bits) is divided
-// by: m / 2^(e - 127) lies in [1, 2) ([2, 4) for the top binade; below 1 for a subnormal m).
-__device__ __forceinline__ uint32_t block_exponent(uint32_t m)
-{
-    const uint32_t e = m >> 23;
-    return e < 1u ? 1u : e > 253u ? 253u : e;
-}
-
-// A warp's weight tile: 16 rows x 256 codes (128 bytes at a 144-byte pitch: the fragment loads of
-// eight rows x four lanes hit 32 banks) and the rows' scale bytes of the tile (8 MXFP4, 16 NVFP4),
-// fetched as the aligned words that hold them, since a row of scales may start at any byte.
-constexpr int kTileK = 256, kTileBlocks = kTileK / 32;
-
-template <bool NV> struct Tile {
-    static constexpr int kPitch = 144;
-    static constexpr int kScaleBytes = NV ? 16 : 8; // of one row and tile
-    static constexpr int kWords = kScaleBytes / 4 + 1;
-    static constexpr int kSlot = NV ? 32 : 16;
-    static constexpr int kOffScales = 16 * kPitch;
-    static constexpr int kBytes = kOffScales + 16 * kSlot;
-};
-
-// Where a lane reads its share of a warp's rows. Local rows 0..7 are rows row..row + 7 of the
-// expert's matrix, 8..15 the same `half` rows further down.
-struct TileSource {
-    const uint8_t *codes;  // row + lane / 8, at the lane's 16-byte chunk
-    const uint8_t *scales; // the expert's
-    int64_t srow;          // byte offset of row (row + lane % 8 (+ half))'s scales
-};
-
-template <bool NV>
-__device__ __forceinline__ TileSource tile_source(const uint8_t *codes, const uint8_t *scales,
-                                                  int64_t K, int64_t row, int64_t half, int lane)
-{
-    TileSource s;
-    s.codes = codes + (row + (lane >> 3)) * (K >> 1) + (lane & 7) * 16;
-    s.scales = scales;
-    s.srow = (row + (lane & 7) + ((lane & 8) ? half : 0)) * (NV ? K >> 4 : K >> 5);
-    return s;
-}
-
-// Tile kt of the K codes of each row -> shared memory (cp.async; 16-byte pieces past the row's end
-// are left out, and so are scale words that hold none of the row's bytes).
-template <bool NV>
-__device__ __forceinline__ void load_tile(uint32_t dst, const TileSource &s, int64_t K, int64_t half,
-                                          int kt, int lane)
-{
-    using L = Tile<NV>;
-    const int64_t krow = K >> 1;
-    const int c = lane & 7;
-    if (kt * kTileBlocks + c < (int)(K >> 5)) {
-        const uint8_t *src = s.codes + (int64_t)kt * (kTileK / 2);
-        const uint32_t d = dst + (lane >> 3) * L::kPitch + c * 16;
-        cp_async16(d, src);
-        cp_async16(d + 4 * L::kPitch, src + 4 * krow);
-        cp_async16(d + 8 * L::kPitch, src + half * krow);
-        cp_async16(d + 12 * L::kPitch, src + (half + 4) * krow);
+    const int tid = threadIdx.x, lane = tid & 31, sub = lane & 7;
+    float inv_row = 1.0f;
+    if constexpr (NV) { // the row's power of two
+        __shared__ uint32_t s_max[THREADS / 32];
+        uint32_t m = 0u;
+        for (int64_t i = tid; i < cols / 4; i += THREADS) {
+            const float4 v = load(i);
+            m = max(max(m, max(__float_as_uint(v.x) & 0x7FFFFFFFu, __float_as_uint(v.y) & 0x7FFFFFFFu)),
+                    max(__float_as_uint(v.z) & 0x7FFFFFFFu, __float_as_uint(v.w) & 0x7FFFFFFFu));
+        }
+        m = __reduce_max_sync(0xFFFFFFFFu, m);
+        if (lane == 0)
+            s_max[tid >> 5] = m;
+        __syncthreads();
+        m = s_max[lane & (THREADS / 32 - 1)];
+        m = __reduce_max_sync(0xFFFFFFFFu, m);
+        // 2^k, k = floor(log2 max) - 10, kept where both it and its inverse are normal
+        const int e = min(max((int)(m >> 23) - 10, 1), 253);
+        inv_row = __uint_as_float((uint32_t)(254 - e) << 23);
+        if (tid == 0)
+            *factor = m >= 0x7F800000u ? __uint_as_float(0x7FC00000u)
+                                       : __uint_as_float((uint32_t)e << 23);
     }
-    const int64_t k0 = (int64_t)kt * L::kScaleBytes;
-    const int64_t left = (NV ? K >> 4 : K >> 5) - k0;
-    const int64_t off = s.srow + k0, a = off & ~(int64_t)3;
-    const int64_t end = off + (left < L::kScaleBytes ? left : L::kScaleBytes);
-    const uint32_t d = dst + L::kOffScales + (lane & 15) * L::kSlot;
-#pragma unroll
-    for (int w = 0; w < L::kWords; w += 2) { // lanes 16.. take the odd words
-        const int q = w + (lane >> 4);
-        if (a + 4 * q < end)
-            cp_async4(d + 4 * q, s.scales + a + 4 * q);
-    }
-}
-
-// Scale bytes of local row r as whole words; sh8: 8 x the byte in its word at which they start.
-template <bool NV>
-__device__ __forceinline__ void tile_scales(const uint8_t *tile, int r, uint32_t sh8,
-                                            uint32_t (&s)[NV ? 4 : 2])
-{
-    const uint4 *a =
-        reinterpret_cast<const uint4 *>(tile + Tile<NV>::kOffScales + r * Tile<NV>::kSlot);
-    const uint4 w = a[0];
-    s[0] = __funnelshift_r(w.x, w.y, sh8);
-    s[1] = __funnelshift_r(w.y, w.z, sh8);
-    if constexpr (NV) {
-        s[2] = __funnelshift_r(w.z, w.w, sh8);
-        s[3] = __funnelshift_r(w.w, a[1].x, sh8);
-    }
-}
-
-// Whether a word has a byte 0 or 255 (MXFP4 scales that are not a shifted exponent field).
-__device__ __forceinline__ bool odd_scale(uint32_t w)
-{
-    return ((((w - 0x01010101u) & ~w) | ((~w - 0x01010101u) & w)) & 0x80808080u) != 0u;
-}
-
-// acc += half a tile (four 32-blocks, nb of them live) x activations. frag(n, b) gives the
-// activations of column tile n as MMA B fragments; colscale(n, b, j) the scale of this lane's j-th
-// accumulator column (COLS). NL live column tiles. SPECIAL: the general form, for short tiles and
-// for MXFP4 scale bytes 0 and 255; the other has no branch, so that the loads and MMAs of
-// neighbouring blocks interleave.
-template <int NT, int NL, bool NV, bool COLS, bool SPECIAL, typename Frag, typename ColScale>
-__device__ __forceinline__ void half_blocks(float (&acc)[NT][4], const uint8_t *codes, int nb,
-                                            int lane, const uint32_t *s0, const uint32_t *s1,
-                                            Frag frag, ColScale colscale)
-{
-    const int g = lane >> 2, t = lane & 3;
-    const uint8_t *ra = codes + g * Tile<NV>::kPitch, *rb = ra + 8 * Tile<NV>::kPitch;
-#pragma unroll
-    for (int b = 0; b < 4; ++b) {
-        if (SPECIAL && b >= nb)
-            break;
-        const uint32_t w0 = lane_codes<NV>(ra + b * 16, t), w1 = lane_codes<NV>(rb + b * 16, t);
-        // k16 step, fragment: rows g and g + 8, k indices 2t.. and 2t + 8..
-        const uint32_t a[2][4] = {{e2m1x2_to_f16x2<0>(w0), e2m1x2_to_f16x2<0>(w1),
-                                   e2m1x2_to_f16x2<1>(w0), e2m1x2_to_f16x2<1>(w1)},
-                                  {e2m1x2_to_f16x2<2>(w0), e2m1x2_to_f16x2<2>(w1),
-                                   e2m1x2_to_f16x2<3>(w0), e2m1x2_to_f16x2<3>(w1)}};
-        float f0[2], f1[2]; // block scales of rows g, g + 8 (NVFP4: of each 16-block)
+    const int64_t groups = (pitch * (NV ? 16 : 32) + 31) / 32; // 32-value groups, padding included
+    for (int64_t b = tid >> 3; b < groups; b += THREADS / 8) { // (whole warps in step)
+        const bool on = b * 32 < cols;
+        float4 v = on ? load(b * 8 + sub) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
         if constexpr (NV) {
-            const float2 p0 = e4m3x2_to_f32x2(s0[b >> 1] >> (16 * (b & 1)));
-            const float2 p1 = e4m3x2_to_f32x2(s1[b >> 1] >> (16 * (b & 1)));
-            f0[0] = p0.x;
-            f0[1] = p0.y;
-            f1[0] = p1.x;
-            f1[1] = p1.y;
-        } else if constexpr (SPECIAL) {
-            f0[0] = mx_scale_f32((s0[0] >> (8 * b)) & 0xFFu);
-            f1[0] = mx_scale_f32((s1[0] >> (8 * b)) & 0xFFu);
-        } else { // the byte into bits 23..30
-            f0[0] = __uint_as_float(__byte_perm(s0[0], 0u, 0x0444u | b << 12) >> 1);
-            f1[0] = __uint_as_float(__byte_perm(s1[0], 0u, 0x0444u | b << 12) >> 1);
+            v.x *= inv_row;
+            v.y *= inv_row;
+            v.z *= inv_row;
+            v.w *= inv_row;
         }
 #pragma unroll
-        for (int n = 0; n < NL; ++n) {
-            const uint4 u = frag(n, b);
-            float q0 = 1.0f, q1 = 1.0f;
-            if constexpr (COLS) {
-                q0 = colscale(n, b, 0);
-                q1 = colscale(n, b, 1);
-            }
-            float c[4];
-            mma_f16_first(c, a[0], u.x, u.y);
+        for (int j = 0; j < kTerms; ++j) {
+            uint32_t m =
+                max(max(__float_as_uint(v.x) & 0x7FFFFFFFu, __float_as_uint(v.y) & 0x7FFFFFFFu),
+                    max(__float_as_uint(v.z) & 0x7FFFFFFFu, __float_as_uint(v.w) & 0x7FFFFFFFu));
+            m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 1));
+            m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 2));
+            uint32_t sb;
+            float s, inv;
             if constexpr (NV) {
-                float d[4];
-                mma_f16_first(d, a[1], u.z, u.w);
-                acc[n][0] = fmaf(COLS ? c[0] * q0 : c[0], f0[0], acc[n][0]);
-                acc[n][1] = fmaf(COLS ? c[1] * q1 : c[1], f0[0], acc[n][1]);
-                acc[n][2] = fmaf(COLS ? c[2] * q0 : c[2], f1[0], acc[n][2]);
-                acc[n][3] = fmaf(COLS ? c[3] * q1 : c[3], f1[0], acc[n][3]);
-                acc[n][0] = fmaf(COLS ? d[0] * q0 : d[0], f0[1], acc[n][0]);
-                acc[n][1] = fmaf(COLS ? d[1] * q1 : d[1], f0[1], acc[n][1]);
-                acc[n][2] = fmaf(COLS ? d[2] * q0 : d[2], f1[1], acc[n][2]);
-                acc[n][3] = fmaf(COLS ? d[3] * q1 : d[3], f1[1], acc[n][3]);
+                sb = m >= 0x7F800000u ? 0u : cvt_e4m3(__uint_as_float(m) * (1.0f / 6.0f));
+                s = e4m3_to_f32(sb);
+                inv = sb != 0u ? __frcp_rn(s) : 0.0f;
             } else {
-                mma_f16(c, a[1], u.z, u.w);
-                acc[n][0] = fmaf(COLS ? c[0] * q0 : c[0], f0[0], acc[n][0]);
-                acc[n][1] = fmaf(COLS ? c[1] * q1 : c[1], f0[0], acc[n][1]);
-                acc[n][2] = fmaf(COLS ? c[2] * q0 : c[2], f1[0], acc[n][2]);
-                acc[n][3] = fmaf(COLS ? c[3] * q1 : c[3], f1[0], acc[n][3]);
+                m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 4));
+                sb = mx_scale_byte(m, true);
+                s = sb == kMxNan ? 0.0f : mx_scale_f32(sb);
+                inv = mx_inverse(sb);
+            }
+            const float y[8] = {v.x * inv, v.y * inv, v.z * inv, v.w * inv, 0.0f, 0.0f, 0.0f, 0.0f};
+            const uint32_t w = inv != 0.0f ? cvt_e2m1x8(y) & 0xFFFFu : 0u;
+            const float2 lo = e2m1x2_to_f32x2(w & 0xFFu), hi = e2m1x2_to_f32x2(w >> 8);
+            v.x = fmaf(-lo.x, s, v.x);
+            v.y = fmaf(-lo.y, s, v.y);
+            v.z = fmaf(-hi.x, s, v.z);
+            v.w = fmaf(-hi.y, s, v.w);
+            if (!NV && sb == kMxNan)
+                v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+            if (on)
+                *reinterpret_cast<uint16_t *>(codes + j * (cols >> 1) + b * 16 + sub * 2) =
+                    (uint16_t)w;
+            if (NV) {
+                if ((sub & 3) == 0 && 2 * b + (sub >> 2) < pitch)
+                    scales[j * pitch + 2 * b + (sub >> 2)] = on ? (uint8_t)sb : (uint8_t)0;
+            } else if (sub == 0 && b < pitch) {
+                scales[j * pitch + b] = on ? (uint8_t)sb : (uint8_t)0;
             }
         }
     }
 }
 
-// The scales of a tile's rows g and g + 8, and whether they (or a short tile) need the general form.
-template <bool NV> struct TileScales {
-    uint32_t s0[NV ? 4 : 2], s1[NV ? 4 : 2];
-    bool special;
-
-    __device__ __forceinline__ void load(const uint8_t *tile, int nb, int lane, uint32_t sh0,
-                                         uint32_t sh1)
-    {
-        tile_scales<NV>(tile, lane >> 2, sh0, s0);
-        tile_scales<NV>(tile, (lane >> 2) + 8, sh1, s1);
-        special = nb < kTileBlocks;
-        if constexpr (!NV)
-            special = special || __any_sync(0xFFFFFFFFu, odd_scale(s0[0]) || odd_scale(s0[1]) ||
-                                                             odd_scale(s1[0]) || odd_scale(s1[1]));
-    }
-};
-
-// Half HALF of a tile, nt live column tiles.
-template <int HALF, int NT, bool NV, bool COLS, typename Frag, typename ColScale>
-__device__ __forceinline__ void half_product(float (&acc)[NT][4], const uint8_t *tile, int nb,
-                                             int nt, int lane, const TileScales<NV> &sc, Frag frag,
-                                             ColScale colscale)
+__device__ __forceinline__ float4 bf16x4(uint2 v)
 {
-    constexpr int kW = NV ? 2 * HALF : HALF; // first scale word
-    const uint8_t *codes = tile + HALF * 64;
-    if (sc.special)
-        half_blocks<NT, NT, NV, COLS, true>(acc, codes, nb - 4 * HALF, lane, sc.s0 + kW, sc.s1 + kW,
-                                            frag, colscale);
-    else if (nt == 1)
-        half_blocks<NT, 1, NV, COLS, false>(acc, codes, 4, lane, sc.s0 + kW, sc.s1 + kW, frag,
-                                            colscale);
-    else
-        half_blocks<NT, NT, NV, COLS, false>(acc, codes, 4, lane, sc.s0 + kW, sc.s1 + kW, frag,
-                                             colscale);
+    return make_float4(__uint_as_float(v.x << 16), __uint_as_float(v.x & 0xFFFF0000u),
+                       __uint_as_float(v.y << 16), __uint_as_float(v.y & 0xFFFF0000u));
 }
 
-// Place of value v (0..31) of a 32-block in the activations' layout: each lane's 8 values are
-// consecutive (MXFP4: v itself; NVFP4: lane t takes 4t.. of both 16-blocks).
-template <bool NV> __device__ __forceinline__ int lane_order(int v)
+// The tokens' terms (one CTA a token) and, in the last CTA, the lists.
+template <bool NV>
+__global__ void __launch_bounds__(kPrepThreads)
+    moe_prepare_kernel(const MoeShared sh, const uint2 *x, const int *ids, const float *weights,
+                       int T, int k, int E, int64_t H)
 {
-    if constexpr (NV)
-        return (((v >> 2) & 3) * 2 + (v >> 4)) * 4 + (v & 3);
-    else
-        return v;
-}
-
-constexpr int kMaxSmem = 232448 - 64; // per CTA, beside the static part
-constexpr int kWarps = 16, kGroups = kWarps / 4, kStages = 3;
-constexpr int kRowBlock = 64;  // columns of y a CTA sums at a time: 16 a warp of a group
-constexpr int kHPitch = 36;    // floats between columns of the h exchange: conflict-free
-constexpr uint32_t kBarrierLimit = 1u << 21;
-
-// Shared memory: rings; sums of the K-split; h exchange; token exponents; x panel (gate/up) or y
-// sums (down); lists.
-template <int NT, bool NV, int KS> struct Layout {
-    static constexpr int kRed = (kGroups / KS) * KS * (KS - 1) * 4 * NT * 32 * 16;
-    static constexpr int kOffRed = kWarps * kStages * Tile<NV>::kBytes;
-    static constexpr int kOffH = kOffRed + kRed;
-    static constexpr int kOffExp = kOffH + kGroups * 8 * NT * kHPitch * 4;
-    static constexpr int kOffX = kOffExp + 128;
-    // bytes between columns of the x panel: 64 past a multiple of 128, so that the 16-byte
-    // fragment loads of two columns x four lanes hit 32 banks
-    __host__ __device__ static int x_pitch(int panel)
-    {
-        return panel * 2 + (panel * 2 % 128 == 0 ? 64 : 0);
-    }
-    __host__ __device__ static int x_bytes(int T, int panel)
-    {
-        const int x = (T < 8 * NT ? T : 8 * NT) * x_pitch(panel), y = kWarps * 16 * T * 4;
-        return x > y ? x : y;
-    }
-};
-
-// The whole layer's experts in one cooperative launch, one CTA of 16 warps per SM.
-//
-// Gate/up: an item is 32 columns of F (64 weight rows) of one column tile. A team of KS groups of
-// four warps takes an item; a warp has 8 of its columns, 8 gate rows and the same 8 up rows as its 16
-// MMA rows, so that a lane's accumulators hold both sides of its products; the team's groups split
-// the k-tiles, and take turns in adding the others' sums and finishing an item (h and its block
-// exponents, to the workspace). A CTA's items are a run, so its tokens change seldom; they are kept in
-// shared memory as f16, each divided by its power of two (whole rows, or panels of them where they
-// do not fit).
-//
-// Grid barrier (every h is in place), behind which the rings already fill with the next tiles.
-//
-// Down: a CTA sums 64 columns of y, its groups' and `splits` CTAs' shares being runs of the flat list
-// of (column tile, k-tile) pairs of all met experts. A warp weights its sums of a column tile into
-// its own [T x 16] array; the arrays are added group by group, the CTAs' sums split by split by the
-// CTA that comes last, so the order of every sum is fixed.
-//
-// Bound by the decode (35-40 issue slots per 16 x 32 codes and column tile, about the time HBM takes
-// for them), so both have to run at once: the rings are private to the warps and run on across items.
-template <int NT, bool NV, int KS>
-__global__ void __launch_bounds__(kWarps * 32, 1) moe_experts_kernel(const MoeParams p)
-{
-    using L = Tile<NV>;
-    using U = Layout<NT, NV, KS>;
-    constexpr int NC = 8 * NT, kTeams = kGroups / KS;
-    extern __shared__ __align__(16) uint8_t smem[];
-    __shared__ int s_flag;
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
-    const int grp = warp >> 2, w4 = warp & 3, team = grp / KS, kg = grp % KS;
-    const MoeLists l = moe_lists(smem + U::kOffX + U::x_bytes(p.T, p.panel), p.T, p.k, p.E);
-    const int nrb = (int)((p.H + kRowBlock - 1) / kRowBlock);
+    extern __shared__ __align__(16) uint8_t list_smem[];
+    pdl_launch_dependents();
     pdl_wait();
-    if (blockIdx.x == 0)
-        for (int i = tid; i < nrb; i += kWarps * 32)
-            p.arrived[i] = 0;
-    build_lists(l, p, NC);
-
-    const int nf = (int)(p.F >> 5); // items per column tile
-    const int n_units = *l.n_units;
-    const int64_t items = (int64_t)n_units * nf;
-    const int i0 = (int)(items * blockIdx.x / gridDim.x);
-    const int i1 = (int)(items * (blockIdx.x + 1) / gridDim.x);
-    const int upblk = (int)(p.H >> 5), upkt = (upblk + kTileBlocks - 1) / kTileBlocks;
-    const int dnblk = (int)(p.F >> 5), dnkt = (dnblk + kTileBlocks - 1) / kTileBlocks;
-    const int64_t uprow = NV ? p.H >> 4 : p.H >> 5, dnrow = NV ? p.F >> 4 : p.F >> 5;
-
-    // ---- the tiles this warp loads, in the order in which it uses them -------------------------
-    uint8_t *ring = smem + warp * kStages * L::kBytes;
-    const uint32_t ring_addr = smem_u32(ring);
-    int phase = 0;                      // 0 gate/up, 1 down, 2 none left
-    int lu, li, lkt, left = 0, lslot = 0, job = 0;
-    TileSource src;
-    // the warp's run of (column tile, k-tile) pairs in down job j: [a, b)
-    auto down_run = [&](int j, int &a, int &b) {
-        const int64_t row = (int64_t)(j / p.splits) * kRowBlock + w4 * 16;
-        const int64_t total = row < p.H ? (int64_t)n_units * dnkt : 0;
-        const int run = (j % p.splits) * kGroups + grp, runs = p.splits * kGroups;
-        a = (int)(total * run / runs);
-        b = (int)(total * (run + 1) / runs);
-    };
-    auto down_source = [&]() {
-        const int64_t e = unit_expert(l.unit[lu]);
-        src = tile_source<NV>(p.down_codes + e * p.H * (p.F >> 1), p.down_scales + e * p.H * dnrow,
-                              p.F, (int64_t)(job / p.splits) * kRowBlock + w4 * 16, 8, lane);
-    };
-    auto down_seek = [&]() { // to the first down job from `job` on with tiles for this warp
-        phase = 2;
-        for (; job < nrb * p.splits; job += gridDim.x) {
-            int a, b;
-            down_run(job, a, b);
-            if (a < b) {
-                left = b - a;
-                lu = a / dnkt;
-                lkt = a % dnkt;
-                phase = 1;
-                down_source();
-                return;
-            }
-        }
-    };
-    auto up_seek = [&]() { // to this team's next item, of the same column tile or a later one
-        while (li >= min(i1, (lu + 1) * nf)) {
-            ++lu;
-            li = lu * nf + team;
-            if (lu * nf >= i1) {
-                job = blockIdx.x;
-                down_seek();
-                return;
-            }
-        }
-        const int64_t e = unit_expert(l.unit[lu]);
-        src = tile_source<NV>(p.up_codes + e * 2 * p.F * (p.H >> 1),
-                              p.up_scales + e * 2 * p.F * uprow, p.H,
-                              (int64_t)(li - lu * nf) * 32 + w4 * 8, p.F, lane);
-    };
-    auto issue = [&]() {
-        const uint32_t dst = ring_addr + lslot * L::kBytes;
-        if (phase == 0) {
-            load_tile<NV>(dst, src, p.H, p.F, lkt, lane);
-            lkt += KS;
-            if (lkt >= upkt) {
-                lkt = kg;
-                li += kTeams;
-                up_seek();
-            }
-        } else if (phase == 1) {
-            load_tile<NV>(dst, src, p.F, 8, lkt, lane);
-            if (--left == 0) {
-                job += gridDim.x;
-                down_seek();
-            } else if (++lkt == dnkt) {
-                lkt = 0;
-                ++lu;
-                down_source();
-            }
-        }
-        cp_async_commit();
-        lslot = lslot + 1 == kStages ? 0 : lslot + 1;
-    };
-    if (i0 < i1 && kg < upkt) {
-        lu = i0 / nf;
-        li = i0 + team;
-        lkt = kg;
-        up_seek();
-    } else {
-        job = blockIdx.x;
-        down_seek();
-    }
-#pragma unroll
-    for (int i = 0; i < kStages - 1; ++i)
-        issue();
-    int slot = 0;
-    auto next_tile = [&]() -> const uint8_t * { // the oldest tile, once it has arrived
-        issue();
-        cp_async_wait<kStages - 1>();
-        __syncwarp();
-        return ring + slot * L::kBytes;
-    };
-    auto tile_done = [&]() {
-        __syncwarp(); // the tile is read before its slot is filled again
-        slot = slot + 1 == kStages ? 0 : slot + 1;
-    };
-
-    // ---- gate/up --------------------------------------------------------------------------------
-    {
-        const int pitch = U::x_pitch(p.panel);
-        uint8_t *sx = smem + U::kOffX;
-        uint32_t *s_ex = reinterpret_cast<uint32_t *>(smem + U::kOffExp);
-        float *hx = reinterpret_cast<float *>(smem + U::kOffH) + grp * NC * kHPitch;
-        // [team][turn][other group][w4][n][lane]
-        float4 *red = reinterpret_cast<float4 *>(smem + U::kOffRed) +
-                      team * KS * (KS - 1) * 4 * NT * 32;
-        const uint8_t *xcol[NT]; // this lane's column of each column tile (past the last: that one)
-#pragma unroll
-        for (int n = 0; n < NT; ++n)
-            xcol[n] = sx + min(n * 8 + g, min(NC, p.T) - 1) * pitch + t * 16;
-        int turn = 0; // the team's group that finishes the item
-        for (int u = i0 / nf; u * nf < i1; ++u) {
-            const int e = unit_expert(l.unit[u]), c0 = unit_column(l.unit[u]);
-            const int row0 = l.base[e] + c0;
-            const int ncol = min(NC, mask_count(l.mask + 2 * e) - c0);
-            const int nt = (ncol + 7) >> 3;
-            const int a = max(i0, u * nf), b = min(i1, (u + 1) * nf);
-            const float gs = NV ? __ldg(p.up_gs + e) : 1.0f;
-            for (int r = a; r < b; r += kTeams) {
-                const int it = r + team;
-                const bool on = it < b;
-                const int64_t f0 = (int64_t)(it - u * nf) * 32;
-                const uint32_t sh0 = (uint32_t)(((f0 + w4 * 8 + g) * uprow) & 3) * 8u;
-                const uint32_t sh1 = (uint32_t)(((p.F + f0 + w4 * 8 + g) * uprow) & 3) * 8u;
-                float acc[NT][4] = {};
-                int kt = kg;
-                for (int k0 = 0; k0 < (int)p.H; k0 += p.panel) {
-                    const int k1 = min((int)p.H, k0 + p.panel);
-                    if (r == a || p.panel < (int)p.H) {
-                        __syncthreads(); // the last panel has been used
-                        for (int c = warp; c < ncol; c += kWarps) {
-                            const uint4 *x = p.x + (int64_t)l.tok[row0 + c] * (p.H >> 3);
-                            uint32_t m = 0u;
-#pragma unroll 4
-                            for (int i = lane; i < (int)(p.H >> 3); i += 32) {
-                                const uint4 v = __ldg(x + i);
-                                m = max_u16x2(
-                                    m, max_u16x2(max_u16x2(v.x & kAbs16x2, v.y & kAbs16x2),
-                                                 max_u16x2(v.z & kAbs16x2, v.w & kAbs16x2)));
-                            }
-                            m = __reduce_max_sync(0xFFFFFFFFu, max(m & 0xFFFFu, m >> 16));
-                            const uint32_t ex = block_exponent(m << 16);
-                            const float inv = __uint_as_float((254u - ex) << 23);
-                            if (lane == 0)
-                                s_ex[c] = ex;
-#pragma unroll 4
-                            for (int i = (k0 >> 3) + lane; i < k1 >> 3; i += 32) {
-                                const uint4 v = __ldg(x + i);
-                                const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-                                uint32_t h[4];
-#pragma unroll
-                                for (int q = 0; q < 4; ++q)
-                                    h[q] = pack_f16x2(__uint_as_float(w[q] << 16) * inv,
-                                                      __uint_as_float(w[q] & 0xFFFF0000u) * inv);
-                                // eight values: two groups of four at their lanes' places
-                                uint8_t *d = sx + c * pitch + ((i - (k0 >> 3)) >> 2) * 64;
-                                const int v0 = (i & 3) * 8;
-                                *reinterpret_cast<uint2 *>(d + lane_order<NV>(v0) * 2) =
-                                    make_uint2(h[0], h[1]);
-                                *reinterpret_cast<uint2 *>(d + lane_order<NV>(v0 + 4) * 2) =
-                                    make_uint2(h[2], h[3]);
-                            }
-                        }
-                        __syncthreads();
-                    }
-                    for (; on && kt * kTileK < k1; kt += KS) {
-                        const uint8_t *tile = next_tile();
-                        const int nb = min(kTileBlocks, upblk - kt * kTileBlocks);
-                        TileScales<NV> sc;
-                        sc.load(tile, nb, lane, sh0, sh1);
-                        const int xt = (kt * kTileK - k0) * 2;
-                        const auto one = [](int, int, int) { return 1.0f; };
-                        half_product<0, NT, NV, false>(
-                            acc, tile, nb, nt, lane, sc,
-                            [&](int n, int b_) {
-                                return *reinterpret_cast<const uint4 *>(xcol[n] + xt + b_ * 64);
-                            },
-                            one);
-                        half_product<1, NT, NV, false>(
-                            acc, tile, nb, nt, lane, sc,
-                            [&](int n, int b_) {
-                                return *reinterpret_cast<const uint4 *>(xcol[n] + xt + 256 +
-                                                                        b_ * 64);
-                            },
-                            one);
-                        tile_done();
-                    }
-                }
-                if (!on)
-                    continue;
-                // The others hand their sums to the group whose turn it is. A turn's buffer comes
-                // around after KS items: every other group has by then had its own turn, for which
-                // it waited for this one's next arrival, made after the buffer was read.
-                float4 *rt = red + turn * (KS - 1) * 4 * NT * 32;
-                if (kg != turn) {
-                    float4 *dst = rt + ((kg < turn ? kg : kg - 1) * 4 + w4) * NT * 32 + lane;
-#pragma unroll
-                    for (int n = 0; n < NT; ++n)
-                        dst[n * 32] = make_float4(acc[n][0], acc[n][1], acc[n][2], acc[n][3]);
-                    named_bar_arrive(1 + team * KS + turn, KS * 128);
-                } else {
-                    named_bar_sync(1 + team * KS + turn, KS * 128);
-#pragma unroll
-                    for (int n = 0; n < NT; ++n) {
-                        float4 s = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-#pragma unroll
-                        for (int q = 0; q < KS; ++q) { // in group order
-                            float4 v = make_float4(acc[n][0], acc[n][1], acc[n][2], acc[n][3]);
-                            if (q != kg)
-                                v = rt[((q < kg ? q : q - 1) * 4 + w4) * NT * 32 + n * 32 + lane];
-                            s.x += v.x;
-                            s.y += v.y;
-                            s.z += v.z;
-                            s.w += v.w;
-                        }
-                        const float gate[2] = {s.x, s.y}, upv[2] = {s.z, s.w};
-#pragma unroll
-                        for (int j = 0; j < 2; ++j) {
-                            const int c = n * 8 + 2 * t + j;
-                            if (c < ncol) {
-                                const float q = __uint_as_float(s_ex[c] << 23);
-                                const float ga = gate[j] * q * gs, up = upv[j] * q * gs;
-                                hx[c * kHPitch + w4 * 8 + g] = ga / (1.0f + __expf(-ga)) * up;
-                            }
-                        }
-                    }
-                    named_bar_sync(9 + grp, 128);
-                    for (int c = w4; c < ncol; c += 4) {
-                        const float v = hx[c * kHPitch + lane];
-                        const uint32_t m =
-                            __reduce_max_sync(0xFFFFFFFFu, __float_as_uint(v) & 0x7FFFFFFFu);
-                        const uint32_t ex = block_exponent(m);
-                        const int64_t row = row0 + c;
-                        reinterpret_cast<__half *>(p.h)[row * p.F + f0 + lane_order<NV>(lane)] =
-                            __float2half_rn(v * __uint_as_float((254u - ex) << 23));
-                        if (lane == 0)
-                            p.h_exp[row * p.exp_pitch + (f0 >> 5)] = (uint8_t)ex;
-                    }
-                }
-                turn = turn + 1 == KS ? 0 : turn + 1;
-            }
-        }
-    }
-
-    // ---- every h in place -----------------------------------------------------------------------
-    __syncthreads();
-    if (tid == 0) {
-        s_flag = grid_barrier_sync(p.barrier, (int)gridDim.x, (int)blockIdx.x, kBarrierLimit) ? 1 : 0;
-        if (!s_flag)
-            atomicExch(p.status, (int)NVFP4_ERR_TIMEOUT);
-    }
-    __syncthreads();
-    if (!s_flag) {
-        cp_async_wait<0>();
+    const int t = blockIdx.x;
+    if (t == T) {
+        build_lists(sh, ids, weights, T, k, E, list_smem);
         return;
     }
-
-    // ---- down -----------------------------------------------------------------------------------
-    float *ysum = reinterpret_cast<float *>(smem + U::kOffX); // [group][w4][T][16]
-    float *mysum = ysum + warp * 16 * p.T;
-    for (int jb = blockIdx.x; jb < nrb * p.splits; jb += gridDim.x) {
-        for (int i = lane; i < 16 * p.T; i += 32)
-            mysum[i] = 0.0f;
-        __syncwarp();
-        const int64_t r0 = (int64_t)(jb / p.splits) * kRowBlock + w4 * 16;
-        const uint32_t sh0 = (uint32_t)(((r0 + g) * dnrow) & 3) * 8u;
-        const uint32_t sh1 = (uint32_t)(((r0 + g + 8) * dnrow) & 3) * 8u;
-        int a, b;
-        down_run(jb, a, b);
-        float acc[NT][4] = {};
-        for (int u = a / dnkt, kt = a % dnkt, rest = b - a; rest > 0; ++u, kt = 0) {
-            const int e = unit_expert(l.unit[u]), c0 = unit_column(l.unit[u]);
-            const int row = l.base[e] + c0;
-            const int ncol = min(NC, mask_count(l.mask + 2 * e) - c0);
-            const int nt = (ncol + 7) >> 3;
-            const int kend = min(dnkt, kt + rest);
-            rest -= kend - kt;
-            const uint4 *hp[NT];
-            const uint8_t *ep[NT][2];
-#pragma unroll
-            for (int n = 0; n < NT; ++n) { // dead columns read a live one's
-                hp[n] = p.h + (int64_t)(row + min(n * 8 + g, ncol - 1)) * (p.F >> 3) + t;
-#pragma unroll
-                for (int j = 0; j < 2; ++j)
-                    ep[n][j] =
-                        p.h_exp + (int64_t)(row + min(n * 8 + 2 * t + j, ncol - 1)) * p.exp_pitch;
-            }
-            // half a tile's activations and their exponents
-            struct Half {
-                uint4 h[NT][4];
-                uint32_t e[NT][2];
-            };
-            auto fetch = [&](Half &f, int blk) {
-#pragma unroll
-                for (int n = 0; n < NT; ++n) {
-                    if (n > 0 && n >= nt)
-                        break;
-#pragma unroll
-                    for (int q = 0; q < 4; ++q)
-                        f.h[n][q] = hp[n][min(blk + q, dnblk - 1) * 4];
-#pragma unroll
-                    for (int j = 0; j < 2; ++j)
-                        f.e[n][j] = *reinterpret_cast<const uint32_t *>(ep[n][j] + blk);
-                }
-            };
-            auto scale_of = [](const Half &f, int n, int q, int j) {
-                return __uint_as_float(__byte_perm(f.e[n][j], 0u, 0x0444u | q << 12) >> 1);
-            };
-            Half f0, f1;
-            fetch(f0, kt * kTileBlocks);
-            for (; kt < kend; ++kt) {
-                const uint8_t *tile = next_tile();
-                const int nb = min(kTileBlocks, dnblk - kt * kTileBlocks);
-                TileScales<NV> sc;
-                sc.load(tile, nb, lane, sh0, sh1);
-                fetch(f1, kt * kTileBlocks + 4); // exponents past the row: its padding
-                half_product<0, NT, NV, true>(
-                    acc, tile, nb, nt, lane, sc, [&](int n, int q) { return f0.h[n][q]; },
-                    [&](int n, int q, int j) { return scale_of(f0, n, q, j); });
-                if (kt + 1 < kend)
-                    fetch(f0, (kt + 1) * kTileBlocks);
-                half_product<1, NT, NV, true>(
-                    acc, tile, nb, nt, lane, sc, [&](int n, int q) { return f1.h[n][q]; },
-                    [&](int n, int q, int j) { return scale_of(f1, n, q, j); });
-                tile_done();
-            }
-            // the column tile's sums of this run
-            const float gs = NV ? __ldg(p.down_gs + e) : 1.0f;
-#pragma unroll
-            for (int n = 0; n < NT; ++n)
-#pragma unroll
-                for (int j = 0; j < 2; ++j) {
-                    const int c = n * 8 + 2 * t + j;
-                    if (c < ncol) {
-                        const float w = l.wt[row + c];
-                        float *y = mysum + l.tok[row + c] * 16 + g;
-                        y[0] = fmaf(acc[n][j] * gs, w, y[0]);
-                        y[8] = fmaf(acc[n][2 + j] * gs, w, y[8]);
-                    }
-                    acc[n][j] = acc[n][2 + j] = 0.0f;
-                }
-            __syncwarp(); // the next tile's columns may be other lanes' tokens
-        }
-        __syncthreads();
-        // the groups' sums: y, or this split's share of it
-        const int rb = jb / p.splits;
-        float *part = p.partial + ((int64_t)rb * p.splits + jb % p.splits) * p.T * kRowBlock;
-        for (int i = tid; i < kRowBlock * p.T; i += kWarps * 32) {
-            const int r = i % kRowBlock, tk = i / kRowBlock;
-            float s = 0.0f;
-#pragma unroll
-            for (int q = 0; q < kGroups; ++q)
-                s += ysum[((q * 4 + (r >> 4)) * p.T + tk) * 16 + (r & 15)];
-            if (p.splits > 1)
-                part[i] = s;
-            else if ((int64_t)rb * kRowBlock + r < p.H)
-                p.y[tk * p.H + (int64_t)rb * kRowBlock + r] = __float2bfloat16_rn(s);
-        }
-        if (p.splits > 1) {
-            __threadfence();
-            __syncthreads();
-            if (tid == 0)
-                s_flag = atomicAdd(p.arrived + rb, 1);
-            __syncthreads();
-            if (s_flag == p.splits - 1) { // the last of the block's CTAs adds them up
-                __threadfence();
-                const float *all = p.partial + (int64_t)rb * p.splits * p.T * kRowBlock;
-                for (int i = tid; i < kRowBlock * p.T; i += kWarps * 32) {
-                    const int r = i % kRowBlock, tk = i / kRowBlock;
-                    float s = 0.0f;
-                    for (int q = 0; q < p.splits; ++q)
-                        s += __ldcg(all + (int64_t)q * p.T * kRowBlock + i);
-                    if ((int64_t)rb * kRowBlock + r < p.H)
-                        p.y[tk * p.H + (int64_t)rb * kRowBlock + r] = __float2bfloat16_rn(s);
-                }
-            }
-        }
-        __syncthreads(); // s_flag and the sums have been read
-    }
-    cp_async_wait<0>();
+    const uint2 *row = x + t * (H >> 2);
+    write_terms<NV, kPrepThreads>(H, sh.x_codes + (int64_t)t * kTerms * (H >> 1),
+                    sh.x_scales + (int64_t)t * kTerms * sh.x_pitch, sh.x_pitch, sh.x_factor + t,
+                    [&](int64_t i) { return bf16x4(__ldg(row + i)); });
 }
 
-template <int NT, bool NV, int KS> cudaError_t launch_experts(MoeParams p, cudaStream_t s)
+// The terms of h, one CTA a row.
+template <bool NV>
+__global__ void __launch_bounds__(kTermThreads) moe_terms_kernel(const MoeShared sh, int64_t F)
 {
-    using U = Layout<NT, NV, KS>;
-    const int lists = (int)moe_lists_bytes(p.T, p.k, p.E);
-    // the x panel: all of H where it fits beside the rings
-    const int room = kMaxSmem - U::kOffX - lists;
-    if (U::x_bytes(p.T, (int)p.H) <= room)
-        p.panel = (int)p.H;
+    pdl_launch_dependents();
+    pdl_wait();
+    const int r = blockIdx.x;
+    if (r >= sh.counts[1])
+        return;
+    const float4 *row = reinterpret_cast<const float4 *>(sh.h + (int64_t)r * F);
+    write_terms<NV, kTermThreads>(F, sh.h_codes + (int64_t)r * kTerms * (F >> 1),
+                    sh.h_scales + (int64_t)r * kTerms * sh.h_pitch, sh.h_pitch, sh.h_factor + r,
+                    [&](int64_t i) { return __ldcg(row + i); });
+}
+
+// ---- products -----------------------------------------------------------------------------
+
+constexpr int kThreads = 352;
+constexpr uint32_t kWaitLimit = 1u << 20;
+constexpr int kSfAhead = 4;  // k-tiles whose scales are on their way to shared memory
+constexpr int kSfRing = kSfAhead + 1;
+constexpr int kMaxStages = 8;
+constexpr int kMaxSmem = 232448 - 1024;
+
+struct MoeGemm {
+    MoeShared sh;
+    int T, n_slots;          // tokens, T x top_k
+    int64_t H, F;
+    const uint8_t *a_scales; // the experts', linear
+    int64_t a_rows;          // rows of the stacked weights
+    const float *gs;         // [E] (NVFP4)
+    int stages, b_rows;      // operand ring: stages, term rows of a stage
+    int dense;               // gate/up: a stage holds all tokens' term rows, in token order
+    int splits, blocks;      // down: CTAs per 128-row block of y, blocks
+    __nv_bfloat16 *y;
+    int *status;
+};
+
+// A run of k-tiles of one tile, whose sums stay in one accumulator.
+struct MoeGroup {
+    MoeUnit unit;
+    int64_t ra0, ra1; // rows of the stacked weights of the tile's two 64-row halves
+    int k0, k1;       // k-tiles (none: an empty job)
+    int first;        // gate/up: first column of h; down: the block of y
+    int split;
+    bool last;        // down: the job's last run
+};
+
+// The groups of a CTA, in order; every role of the CTA walks them by itself. Gate/up: a run of the
+// flat list of (column tile, 64 columns of F). Down: jobs (128-row block of y, split), whose run of
+// the flat list of (column tile, k-tile) pairs is cut at the column tiles.
+template <bool DOWN> struct MoeWalk {
+    const MoeGemm &p;
+    const uint32_t *units; // in shared memory
+    int n_units, nkt, per;
+    int64_t i, i1;       // gate/up
+    int job, u, kt;      // down
+    int64_t rest;
+
+    __device__ __forceinline__ MoeWalk(const MoeGemm &q, const uint32_t *list, int n)
+        : p(q), units(list), n_units(n)
+    {
+        const int64_t K = DOWN ? p.F : p.H;
+        nkt = (int)((K + 255) >> 8);
+        if constexpr (DOWN) {
+            job = (int)blockIdx.x - (int)gridDim.x;
+            rest = -1;
+        } else {
+            per = (int)((p.F + kUpRows - 1) / kUpRows);
+            const int64_t n = (int64_t)n_units * per;
+            i = n * blockIdx.x / gridDim.x;
+            i1 = n * (blockIdx.x + 1) / gridDim.x;
+        }
+    }
+
+    __device__ __forceinline__ bool next(MoeGroup &g)
+    {
+        if constexpr (!DOWN) {
+            if (i >= i1)
+                return false;
+            g.unit = unpack_unit(units[(int)(i / per)]);
+            g.first = (int)(i % per) * kUpRows;
+            g.ra0 = (int64_t)g.unit.expert * 2 * p.F + g.first;
+            g.ra1 = g.ra0 + p.F;
+            g.k0 = 0;
+            g.k1 = nkt;
+            ++i;
+        } else {
+            if (rest <= 0) {
+                job += gridDim.x;
+                if (job >= p.blocks * p.splits)
+                    return false;
+                const int64_t total = (int64_t)n_units * nkt;
+                g.split = job % p.splits;
+                const int64_t a = total * g.split / p.splits;
+                rest = total * (g.split + 1) / p.splits - a;
+                u = (int)(a / nkt);
+                kt = (int)(a % nkt);
+            }
+            g.first = job / p.splits;
+            g.split = job % p.splits;
+            if (rest == 0) {
+                g.unit = MoeUnit{0, 0, 0};
+                g.k0 = g.k1 = 0;
+                g.last = true;
+                return true;
+            }
+            g.unit = unpack_unit(units[u]);
+            g.ra0 = (int64_t)g.unit.expert * p.H + (int64_t)g.first * kDownRows;
+            g.ra1 = g.ra0 + 64;
+            g.k0 = kt;
+            g.k1 = (int)(rest < nkt - kt ? kt + rest : nkt);
+            rest -= g.k1 - g.k0;
+            ++u;
+            kt = 0;
+            g.last = rest == 0;
+        }
+        return true;
+    }
+};
+
+template <int BYTES> __device__ __forceinline__ void cp_async(uint32_t dst, const uint8_t *src)
+{
+    if constexpr (BYTES == 16)
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst),
+                     "l"(reinterpret_cast<uint64_t>(src))
+                     : "memory");
     else
-        p.panel = (room / (p.T < 8 * NT ? p.T : 8 * NT) - 64) / 2 / kTileK * kTileK;
-    const size_t smem = U::kOffX + U::x_bytes(p.T, p.panel) + lists;
-    auto kernel = moe_experts_kernel<NT, NV, KS>;
+        asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(dst),
+                     "l"(reinterpret_cast<uint64_t>(src)), "n"(BYTES)
+                     : "memory");
+}
+
+// One row's scale bytes of a k-tile where they are not a whole aligned piece: `have` of SB bytes,
+// then zeros.
+template <int SB>
+__device__ __noinline__ void fetch_scales_general(uint32_t dst, const uint8_t *src, int have)
+{
+    if (have == SB && (reinterpret_cast<uintptr_t>(src) & 3) == 0) {
+        for (int i = 0; i < SB; i += 4)
+            cp_async<4>(dst + i, src + i);
+        return;
+    }
+    for (int i = 0; i < SB; i += 4) {
+        uint32_t w = 0u;
+        for (int j = 0; j < 4; ++j)
+            if (i + j < have)
+                w |= (uint32_t)__ldg(src + i + j) << (8 * j);
+        asm volatile("st.shared.u32 [%0], %1;" ::"r"(dst + i), "r"(w) : "memory");
+    }
+}
+
+// 128 rows' scale bytes (SB a row at `sm`) -> the TMEM columns of F::kAtoms atoms, this warp's lane
+// quarter: lane r's word i of an atom is row r + 32 i's.
+template <class F>
+__device__ __forceinline__ void feed_rows(const uint8_t *sm, uint32_t tcol, int lane)
+{
+    constexpr int SB = 4 * F::kAtoms;
+    uint32_t r[4 * F::kAtoms];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        if constexpr (F::kMx) {
+            const uint2 v = *reinterpret_cast<const uint2 *>(sm + (lane + 32 * i) * SB);
+            r[i] = v.x;
+            r[4 + i] = v.y;
+        } else {
+            const uint4 v = *reinterpret_cast<const uint4 *>(sm + (lane + 32 * i) * SB);
+            r[i] = v.x;
+            r[4 + i] = v.y;
+            r[8 + i] = v.z;
+            r[12 + i] = v.w;
+        }
+    }
+    if constexpr (F::kMx)
+        tmem_st_32x32b_x8(tcol, r);
+    else
+        tmem_st_32x32b_x16(tcol, r);
+}
+
+// Gate/up (DOWN false) and down products on the FP4 tensor cores: 128 weight rows are the M side of
+// block-scaled MMAs, eight term rows of each token of a column tile the N side (8..128 columns), so
+// the weights go from HBM to the tensor cores as they are stored and the sum of a token's eight
+// columns is the product with its full-precision value. One persistent CTA per SM:
+//   warp 0      TMA producer of the weights: per 256-wide k-tile the tile's two 64-row halves;
+//   warp 10     TMA producer of the term rows: one box (down; up to 16 tokens in all), or a box of
+//               eight rows per token of the column tile;
+//   warps 6..9  scale feeders: the rows' linear scale bytes to shared memory by cp.async, kSfAhead
+//               k-tiles ahead, then to the stage's TMEM columns in the MMA's layout;
+//   warp 1      MMA issuer; accumulators alternate between two TMEM buffers, so that a tile's
+//               epilogue overlaps the next tile's MMAs;
+//   warps 2..5  epilogue. Gate/up: a tile is 64 gate rows and the same 64 up rows; they meet in
+//               shared memory and silu(gate) * up goes to the workspace in fp32. Down: the weighted
+//               sums of every column tile are added to [T][128] sums in shared memory, which go to y
+//               or, split by split, to the workspace (moe_sum_kernel).
+// A stage's bytes and scales complete one barrier, and the MMAs that have read them another.
+// Bound by HBM: a k-tile's 16 KB take 370 ns of an SM's share, its four MMAs of N = 64 about 70 ns;
+// a role must therefore take fewer than 700 cycles a k-tile, which is why each is a warp of its own
+// with few instructions a step. Waits are bounded; after one that gave up the roles run on without
+// waiting and the status word says so.
+template <class F, bool DOWN>
+__global__ void __launch_bounds__(kThreads, 1)
+    moe_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
+                    const MoeGemm p)
+{
+    constexpr int SB = 4 * F::kAtoms;          // scale bytes of a row and k-tile
+    constexpr int kSfRows = 2 * 128 * SB;      // weights' and terms' rows of one k-tile
+    constexpr uint32_t kAccCols = 128, kSfCol = 2 * kAccCols, kSlotCols = 32;
+    extern __shared__ __align__(1024) uint8_t smem[];
+    __shared__ __align__(8) uint64_t full_bar[kMaxStages], empty_bar[kMaxStages];
+    __shared__ __align__(8) uint64_t acc_full[2], acc_empty[2], drain_bar;
+    __shared__ uint32_t tmem_slot;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    if ((smem_u32(smem) & 1023u) != 0) { // the same for every CTA
+        if (tid == 0)
+            atomicExch(p.status, (int)NVFP4_ERR_CUDA);
+        return;
+    }
+    const int stage_bytes = 16384 + p.b_rows * 128;
+    uint8_t *sf_ring = smem + p.stages * stage_bytes;
+    float *s_out = reinterpret_cast<float *>(sf_ring + kSfRing * kSfRows);
+    if (tid == 0) {
+        for (int s = 0; s < p.stages; ++s) {
+            mbar_init(&full_bar[s], 2 + 4); // the producers, the feeders' warps
+            mbar_init(&empty_bar[s], 1);
+        }
+        for (int s = 0; s < 2; ++s) {
+            mbar_init(&acc_full[s], 1);
+            mbar_init(&acc_empty[s], 4);
+        }
+        mbar_init(&drain_bar, 1);
+        fence_barrier_init();
+    }
+    if (warp == 1) {
+        tmem_alloc(&tmem_slot, 512);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = tmem_slot;
+    pdl_launch_dependents();
+    pdl_wait(); // the lists, the terms
+    // the lists to shared memory: [rows] weights, [column tiles], [rows] tokens
+    const int n_units = __ldg(p.sh.counts), n_rows = __ldg(p.sh.counts + 1);
+    float *s_wt = s_out + (DOWN ? p.T : kCols) * 128;
+    uint32_t *s_units = reinterpret_cast<uint32_t *>(s_wt + p.n_slots);
+    uint8_t *s_tok = reinterpret_cast<uint8_t *>(s_units + p.n_slots);
+    for (int i = tid; i < n_rows; i += kThreads) {
+        s_wt[i] = __ldg(p.sh.wt + i);
+        s_tok[i] = __ldg(p.sh.tok + i);
+    }
+    for (int i = tid; i < n_units; i += kThreads)
+        s_units[i] = __ldg(p.sh.units + i);
+    __syncthreads();
+
+    bool dead = false; // a wait gave up: run on without waiting
+    auto wait = [&](uint64_t *bar, uint32_t parity) {
+        if (!dead && !mbar_wait(bar, parity, kWaitLimit)) {
+            dead = true;
+            atomicExch(p.status, (int)NVFP4_ERR_TIMEOUT);
+        }
+    };
+    int stage = 0;
+    uint32_t phase = 0;
+    auto next_stage = [&]() {
+        if (++stage == p.stages) {
+            stage = 0;
+            phase ^= 1;
+        }
+    };
+    MoeWalk<DOWN> walk(p, s_units, n_units);
+    MoeGroup gr;
+    if (warp == 0) {
+        // ------------------------------- the weights' TMA producer ------------------
+        if (lane == 0) {
+            int issued = 0;
+            while (walk.next(gr)) {
+                const int y0 = (int)gr.ra0, y1 = (int)gr.ra1;
+                for (int kt = gr.k0; kt < gr.k1; ++kt) {
+                    uint8_t *a = smem + stage * stage_bytes;
+                    uint64_t *bar = &full_bar[stage];
+                    wait(&empty_bar[stage], phase ^ 1);
+                    mbar_arrive_expect_tx(bar, 16384u);
+                    tma_load_2d(a, &tmA, bar, kt * 128, y0);
+                    tma_load_2d(a + 8192, &tmA, bar, kt * 128, y1);
+                    ++issued;
+                    next_stage();
+                }
+            }
+            // every copy issued has landed before the CTA may exit
+            const int last = issued < p.stages ? issued : p.stages;
+            for (int i = 0; i < last; ++i) {
+                if (--stage < 0) {
+                    stage = p.stages - 1;
+                    phase ^= 1;
+                }
+                wait(&full_bar[stage], phase);
+            }
+        }
+        __syncwarp();
+    } else if (warp == 10) {
+        // ------------------------------- the term rows' TMA producer ----------------
+        const bool one_box = DOWN || p.dense; // else a box of eight rows per token
+        while (walk.next(gr)) {
+            const int ncol = one_box ? 1 : gr.unit.ncol;
+            const uint32_t bytes = one_box ? (uint32_t)p.b_rows * 128u : (uint32_t)ncol * 1024u;
+            int row = 0;
+            if (DOWN)
+                row = gr.unit.row0 * kTerms;
+            else if (!one_box && lane < ncol)
+                row = (int)s_tok[gr.unit.row0 + lane] * kTerms;
+            for (int kt = gr.k0; kt < gr.k1; ++kt) {
+                uint64_t *bar = &full_bar[stage];
+                wait(&empty_bar[stage], phase ^ 1);
+                if (lane == 0)
+                    mbar_arrive_expect_tx(bar, bytes);
+                if (lane < ncol)
+                    tma_load_2d(smem + stage * stage_bytes + 16384 + lane * 1024, &tmB, bar, kt * 128,
+                                row);
+                __syncwarp();
+                next_stage();
+            }
+        }
+    } else if (warp >= 6) {
+        // ------------------------------- scale feeders ------------------------------
+        const int q = warp & 3, r = tid - 192; // lane quarter of TMEM; this thread's row
+        const int srow = (int)((DOWN ? p.F : p.H) / F::kBlock);
+        const int64_t pitch = DOWN ? p.sh.h_pitch : p.sh.x_pitch;
+        const uint8_t *bs = DOWN ? p.sh.h_scales : p.sh.x_scales;
+        const bool even = srow % SB == 0; // every piece of a row is whole and aligned
+        const uint32_t ring = smem_u32(sf_ring) + r * SB;
+        MoeWalk<DOWN> ahead(p, s_units, n_units); // kSfAhead k-tiles before the stores
+        int akt = 0, akend = 0, aslot = 0;
+        bool more = true, a_on = false, b_on = false;
+        const uint8_t *asrc = p.a_scales, *bsrc = bs;
+        auto zero = [&](uint32_t dst) {
+#pragma unroll
+            for (int i = 0; i < SB; i += 4)
+                asm volatile("st.shared.u32 [%0], %1;" ::"r"(dst + i), "r"(0u) : "memory");
+        };
+        auto load = [&]() {
+            while (more && akt >= akend) {
+                MoeGroup ga;
+                more = ahead.next(ga);
+                if (!more)
+                    break;
+                akt = ga.k0;
+                akend = ga.k1;
+                const int64_t row = r < 64 ? ga.ra0 + r : ga.ra1 + (r - 64);
+                a_on = row < p.a_rows;
+                asrc = p.a_scales + (a_on ? row * srow + (int64_t)akt * SB : 0);
+                const bool dense = !DOWN && p.dense;
+                const int c = r / kTerms; // this row's token of the stage
+                b_on = dense ? c < p.T : c < ga.unit.ncol;
+                if (b_on) {
+                    const int t = dense ? c
+                                  : DOWN ? ga.unit.row0 + c
+                                         : (int)s_tok[ga.unit.row0 + c];
+                    bsrc = bs + ((int64_t)t * kTerms + r % kTerms) * pitch + (int64_t)akt * SB;
+                }
+            }
+            if (more) {
+                const uint32_t dst = ring + aslot * kSfRows;
+                if (!a_on)
+                    zero(dst);
+                else if (even)
+                    cp_async<SB>(dst, asrc);
+                else
+                    fetch_scales_general<SB>(dst, asrc, min(SB, srow - akt * SB));
+                if (b_on)
+                    cp_async<SB>(dst + 128 * SB, bsrc);
+                else
+                    zero(dst + 128 * SB);
+                asrc += a_on ? SB : 0;
+                bsrc += SB;
+                ++akt;
+                aslot = aslot + 1 == kSfRing ? 0 : aslot + 1;
+            }
+            asm volatile("cp.async.commit_group;" ::: "memory");
+        };
+#pragma unroll 1
+        for (int i = 0; i < kSfAhead; ++i)
+            load();
+        int rslot = 0;
+        const uint32_t tbase = tmem + ((uint32_t)(q * 32) << 16) + kSfCol;
+        while (walk.next(gr)) {
+            for (int kt = gr.k0; kt < gr.k1; ++kt) {
+                asm volatile("cp.async.wait_group %0;" ::"n"(kSfAhead - 1) : "memory");
+                named_bar_sync(2, 128); // the rows are here, and the last k-tile's have been read
+                load();
+                wait(&empty_bar[stage], phase ^ 1);
+                __syncwarp();
+                tc_fence_after();
+                const uint8_t *src = sf_ring + rslot * kSfRows;
+                feed_rows<F>(src, tbase + stage * kSlotCols, lane);
+                feed_rows<F>(src + 128 * SB, tbase + stage * kSlotCols + 16, lane);
+                tmem_st_wait();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0)
+                    mbar_arrive(&full_bar[stage]);
+                rslot = rslot + 1 == kSfRing ? 0 : rslot + 1;
+                next_stage();
+            }
+        }
+        asm volatile("cp.async.wait_group 0;" ::: "memory");
+    } else if (warp == 1) {
+        // ------------------------------- MMA issuer ---------------------------------
+        int buf = 0;
+        uint32_t aphase = 0;
+        const uint64_t desc0 = smem_desc(smem_u32(smem), 16, 1024, kLayoutSwizzle128B);
+        while (walk.next(gr)) {
+            if (gr.k0 == gr.k1)
+                continue;
+            const int ncol = !DOWN && p.dense ? p.T : gr.unit.ncol;
+            const uint32_t n = ncol <= 1 ? 8 : ncol <= 2 ? 16 : ncol <= 4 ? 32 : ncol <= 8 ? 64 : 128;
+            const uint32_t idesc = F::kIdesc | (1u << 7) | (1u << 10) | ((n >> 3) << 17) | (8u << 24);
+            const uint32_t acc = tmem + buf * kAccCols;
+            wait(&acc_empty[buf], aphase ^ 1);
+            uint32_t add = 0u;
+            for (int kt = gr.k0; kt < gr.k1; ++kt) {
+                wait(&full_bar[stage], phase);
+                __syncwarp();
+                tc_fence_after();
+                if (lane == 0) {
+                    const uint32_t tsf = tmem + kSfCol + stage * kSlotCols;
+                    const uint64_t adesc = desc0 + (uint64_t)((stage * stage_bytes) >> 4);
+                    const uint64_t bdesc = adesc + (16384u >> 4);
+#pragma unroll
+                    for (int kb = 0; kb < 4; ++kb)
+                        tc_mma_fp4<F>(acc, adesc + (uint64_t)(2 * kb), bdesc + (uint64_t)(2 * kb),
+                                      idesc | sf_id_bits<F>(kb), tsf + sf_atom<F>(kb) * 4,
+                                      tsf + 16 + sf_atom<F>(kb) * 4, kb > 0 ? 1u : add);
+                    tc_commit(&empty_bar[stage]);
+                }
+                add = 1u;
+                __syncwarp();
+                next_stage();
+            }
+            if (lane == 0)
+                tc_commit(&acc_full[buf]);
+            __syncwarp();
+            buf ^= 1;
+            if (buf == 0)
+                aphase ^= 1;
+        }
+        if (lane == 0) { // every MMA issued completes before TMEM is freed
+            tc_commit(&drain_bar);
+            wait(&drain_bar, 0);
+        }
+        __syncwarp();
+    } else {
+        // ------------------------------- epilogue (warps 2..5) ----------------------
+        const int q = warp & 3, r = q * 32 + lane; // this thread's accumulator row
+        const int et = tid - 64;
+        int buf = 0;
+        uint32_t aphase = 0;
+        if constexpr (DOWN) {
+            for (int i = et; i < p.T * 128; i += 128)
+                s_out[i] = 0.0f; // [T][128]
+            named_bar_sync(1, 128);
+        }
+        while (walk.next(gr)) {
+            const int ncol = gr.unit.ncol;
+            if (gr.k0 < gr.k1) {
+                wait(&acc_full[buf], aphase);
+                __syncwarp();
+                tc_fence_after();
+                const uint32_t trow = tmem + ((uint32_t)(q * 32) << 16) + buf * kAccCols;
+                const float gs = F::kMx ? 1.0f : __ldg(p.gs + gr.unit.expert);
+                for (int c0 = 0; c0 < ncol; c0 += 4) { // four tokens' columns at a time
+                    uint32_t v[4][8];
+                    int tok[4];
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) {
+                        const int cc = min(c0 + c, ncol - 1);
+                        tok[c] = (int)s_tok[gr.unit.row0 + cc];
+                        tmem_ld_32x32b_x8(trow + (!DOWN && p.dense ? tok[c] : cc) * kTerms, v[c]);
+                    }
+                    tmem_ld_wait();
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) {
+                        if (c0 + c >= ncol)
+                            break;
+                        float s = 0.0f; // the smallest terms first
+#pragma unroll
+                        for (int j = kTerms - 1; j >= 0; --j)
+                            s += __uint_as_float(v[c][j]);
+                        const int row = gr.unit.row0 + c0 + c;
+                        if constexpr (!F::kMx)
+                            s *= gs * __ldg(DOWN ? p.sh.h_factor + row : p.sh.x_factor + tok[c]);
+                        if constexpr (DOWN)
+                            s_out[tok[c] * 128 + r] = fmaf(s, s_wt[row], s_out[tok[c] * 128 + r]);
+                        else
+                            s_out[(c0 + c) * 128 + r] = s; // gate rows 0..63, up rows 64..127
+                    }
+                }
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0)
+                    mbar_arrive(&acc_empty[buf]);
+                buf ^= 1;
+                if (buf == 0)
+                    aphase ^= 1;
+            }
+            if constexpr (!DOWN) {
+                named_bar_sync(1, 128);
+                const int f = et & 63;
+                if (gr.first + f < p.F)
+                    for (int c = et >> 6; c < ncol; c += 2) {
+                        const float ga = s_out[c * 128 + f], up = s_out[c * 128 + 64 + f];
+                        p.sh.h[(int64_t)(gr.unit.row0 + c) * p.F + gr.first + f] =
+                            ga / (1.0f + __expf(-ga)) * up;
+                    }
+                named_bar_sync(1, 128);
+            } else if (gr.last) {
+                // this job's sums: y, or a split's share of it
+                const int64_t col = (int64_t)gr.first * kDownRows + r;
+                float *part = p.sh.partial +
+                              ((int64_t)gr.first * p.splits + gr.split) * p.T * kDownRows + r;
+                for (int t = 0; t < p.T; ++t) {
+                    const float s = s_out[t * 128 + r];
+                    s_out[t * 128 + r] = 0.0f;
+                    if (p.splits > 1)
+                        part[t * kDownRows] = s;
+                    else if (col < p.H)
+                        p.y[t * p.H + col] = __float2bfloat16_rn(s);
+                }
+            }
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 1) {
+        tc_fence_after();
+        tmem_dealloc(tmem, 512);
+    }
+}
+
+// y from the splits' sums, in split order; four columns a thread.
+__global__ void __launch_bounds__(256)
+    moe_sum_kernel(const float *partial, int splits, int T, int64_t H, __nv_bfloat16 *y)
+{
+    pdl_launch_dependents();
+    pdl_wait();
+    const int64_t n = (int64_t)T * (H >> 2);
+    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n; i += (int64_t)gridDim.x * 256) {
+        const int64_t t = i / (H >> 2), c = (i % (H >> 2)) * 4;
+        const float *src = partial + ((c / kDownRows) * splits * T + t) * kDownRows + c % kDownRows;
+        float4 s = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll 4
+        for (int k = 0; k < splits; ++k) {
+            const float4 v = __ldcg(reinterpret_cast<const float4 *>(src + (int64_t)k * T * kDownRows));
+            s.x += v.x;
+            s.y += v.y;
+            s.z += v.z;
+            s.w += v.w;
+        }
+        const __nv_bfloat162 lo = __floats2bfloat162_rn(s.x, s.y), hi = __floats2bfloat162_rn(s.z, s.w);
+        *reinterpret_cast<uint2 *>(y + t * H + c) =
+            make_uint2(*reinterpret_cast<const uint32_t *>(&lo), *reinterpret_cast<const uint32_t *>(&hi));
+    }
+}
+
+template <typename K, typename... Args>
+cudaError_t launch_after(K kernel, int grid, int threads, size_t smem, cudaStream_t s, Args... args)
+{
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3((unsigned)grid, 1, 1);
+    cfg.blockDim = dim3((unsigned)threads, 1, 1);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
+template <class F, bool DOWN>
+cudaError_t launch_gemm(MoeGemm g, const CUtensorMap &tmA, const CUtensorMap &tmB, cudaStream_t s)
+{
     static std::once_flag flags[64];
     int dev = 0;
     cudaGetDevice(&dev);
     cudaError_t e = cudaSuccess;
     std::call_once(flags[dev & 63], [&]() {
-        e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxSmem);
+        e = cudaFuncSetAttribute(moe_gemm_kernel<F, DOWN>,
+                                 cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxSmem);
     });
     if (e != cudaSuccess)
         return e;
-    cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3((unsigned)num_sms(), 1, 1);
-    cfg.blockDim = dim3(kWarps * 32, 1, 1);
-    cfg.dynamicSmemBytes = smem;
-    cfg.stream = s;
-    cudaLaunchAttribute at[2];
-    at[0].id = cudaLaunchAttributeCooperative; // the CTAs wait for one another: all resident
-    at[0].val.cooperative = 1;
-    at[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    at[1].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = at;
-    cfg.numAttrs = 2;
-    return cudaLaunchKernelEx(&cfg, kernel, p);
+    const int fixed = kSfRing * 2 * 128 * 4 * F::kAtoms + (DOWN ? g.T : kCols) * 128 * 4 +
+                      9 * g.n_slots;
+    const int stage = 16384 + g.b_rows * 128;
+    const int fit = (kMaxSmem - fixed) / stage;
+    g.stages = fit < kMaxStages ? fit : kMaxStages;
+    return launch_after(moe_gemm_kernel<F, DOWN>, num_sms(), kThreads,
+                        (size_t)g.stages * stage + fixed, s, tmA, tmB, g);
 }
 
-// Whether a token panel of 16 whole rows fits.
-template <bool NV> bool wide_fits(const MoeParams &p)
-{
-    using U = Layout<2, NV, 2>;
-    return U::kOffX + U::x_bytes(p.T, (int)p.H) + (int)moe_lists_bytes(p.T, p.k, p.E) <=
-           kMaxSmem;
-}
-
-template <bool NV> cudaError_t launch_experts_fmt(const MoeParams &p, cudaStream_t s)
-{
-    if (p.T <= 4)
-        return launch_experts<1, NV, 4>(p, s);
-    // column tiles of 16 where an expert may well meet more than 8 tokens
-    if (p.T > 8 && p.T * p.k > 4 * p.E && wide_fits<NV>(p))
-        return launch_experts<2, NV, 2>(p, s);
-    return launch_experts<1, NV, 2>(p, s);
-}
-
-// CTAs per 64-column block of y.
+// CTAs per 128-row block of y.
 int moe_splits(int64_t H)
 {
-    const int64_t nrb = (H + kRowBlock - 1) / kRowBlock;
-    const int64_t s = num_sms() / nrb;
+    const int64_t s = num_sms() / ((H + kDownRows - 1) / kDownRows);
     return (int)(s < 1 ? 1 : s);
 }
 
-// Workspace: h, its exponents, the splits' sums of y, the arrival counters.
+// The workspace: offsets of MoeShared's arrays for T tokens of k experts.
 struct MoeWs {
-    size_t exps, partial, arrived, total;
+    size_t x_codes, x_scales, x_factor, h, h_codes, h_scales, h_factor, units, counts, tok, wt,
+        partial, total;
 };
 
 MoeWs moe_ws(int64_t T, int64_t k, int64_t F, int64_t H)
 {
-    auto align = [](size_t v) { return (v + 255) & ~(size_t)255; };
-    const size_t rows = (size_t)T * (size_t)k, nrb = (size_t)((H + kRowBlock - 1) / kRowBlock);
+    size_t at = 0;
+    auto take = [&](size_t bytes) {
+        const size_t o = at;
+        at += (bytes + 255) & ~(size_t)255;
+        return o;
+    };
+    const size_t n = (size_t)T * (size_t)k, blocks = (size_t)((H + kDownRows - 1) / kDownRows);
     const int splits = moe_splits(H);
     MoeWs w;
-    w.exps = align(rows * (size_t)F * 2);
-    w.partial = w.exps + align(rows * (size_t)((F / 32 + 7) / 8 * 8));
-    w.arrived = w.partial + (splits > 1 ? align(nrb * splits * (size_t)T * kRowBlock * 4) : 0);
-    w.total = w.arrived + align(nrb * 4);
+    const size_t x_pitch = (size_t)(H / 16 + 15) / 16 * 16, h_pitch = (size_t)(F / 16 + 15) / 16 * 16;
+    w.x_codes = take((size_t)T * kTerms * (size_t)H / 2);
+    w.x_scales = take((size_t)T * kTerms * x_pitch);
+    w.x_factor = take((size_t)T * 4);
+    w.h = take(n * (size_t)F * 4);
+    w.h_codes = take(n * kTerms * (size_t)F / 2);
+    w.h_scales = take(n * kTerms * h_pitch);
+    w.h_factor = take(n * 4);
+    w.units = take(n * 4);
+    w.counts = take(8);
+    w.tok = take(n);
+    w.wt = take(n * 4);
+    w.partial = take(splits > 1 ? blocks * splits * (size_t)T * kDownRows * 4 : 0);
+    w.total = at;
     return w;
+}
+
+template <class F>
+cudaError_t launch_experts(MoeGemm g, const uint2 *x, const int *ids,
+                           const float *weights, int k, int E, const uint8_t *up_codes,
+                           const uint8_t *up_scales, const float *up_gs, const uint8_t *down_codes,
+                           const uint8_t *down_scales, const float *down_gs, cudaStream_t s)
+{
+    constexpr bool NV = !F::kMx;
+    // scale bytes of a term row: whole 16-byte pieces, so that every k-tile's lie inside
+    g.sh.x_pitch = (g.H / F::kBlock + 15) / 16 * 16;
+    g.sh.h_pitch = (g.F / F::kBlock + 15) / 16 * 16;
+    g.b_rows = (g.T < kCols ? g.T : kCols) * kTerms;
+    g.dense = g.T <= kCols;
+    CUtensorMap up, down, xt, ht;
+    const int64_t n = (int64_t)g.T * k;
+    if (!make_fp4_codes_map(&up, up_codes, (int64_t)E * 2 * g.F, g.H, 64) ||
+        !make_fp4_codes_map(&down, down_codes, (int64_t)E * g.H, g.F, 64) ||
+        !make_fp4_codes_map(&xt, g.sh.x_codes, (int64_t)g.T * kTerms, g.H,
+                            g.dense ? g.b_rows : kTerms) ||
+        !make_fp4_codes_map(&ht, g.sh.h_codes, n * kTerms, g.F, g.b_rows))
+        return cudaErrorInvalidValue;
+    cudaError_t e = launch_after(moe_prepare_kernel<NV>, g.T + 1, kPrepThreads,
+                                 lists_smem(g.T, k, E), s, g.sh, x, ids, weights, g.T, k, E,
+                                 g.H);
+    if (e != cudaSuccess)
+        return e;
+    MoeGemm u = g, d = g;
+    u.a_scales = up_scales;
+    u.a_rows = (int64_t)E * 2 * g.F;
+    u.gs = up_gs;
+    d.a_scales = down_scales;
+    d.a_rows = (int64_t)E * g.H;
+    d.gs = down_gs;
+    if ((e = launch_gemm<F, false>(u, up, xt, s)) != cudaSuccess)
+        return e;
+    if ((e = launch_after(moe_terms_kernel<NV>, (int)n, kTermThreads, (size_t)0, s, g.sh, g.F)) !=
+        cudaSuccess)
+        return e;
+    if ((e = launch_gemm<F, true>(d, down, ht, s)) != cudaSuccess || g.splits == 1)
+        return e;
+    const int64_t need = ((int64_t)g.T * (g.H / 4) + 255) / 256, cap = (int64_t)num_sms() * 4;
+    return launch_after(moe_sum_kernel, (int)(need < cap ? need : cap), 256, (size_t)0, s,
+                        g.sh.partial, g.splits, g.T, g.H, g.y);
 }
 
 } // namespace
@@ -1185,35 +1142,30 @@ cudaError_t launch_moe_experts(const void *x, int64_t T, int64_t H, int64_t F, i
                                const uint8_t *down_scales, const float *down_gs, void *y, void *ws,
                                cudaStream_t s)
 {
-    MoeParams p{};
-    p.x = reinterpret_cast<const uint4 *>(x);
-    p.T = (int)T;
-    p.k = k;
-    p.E = E;
-    p.H = H;
-    p.F = F;
-    p.ids = ids;
-    p.weights = weights;
-    p.up_codes = up_codes;
-    p.up_scales = up_scales;
-    p.up_gs = up_gs;
-    p.down_codes = down_codes;
-    p.down_scales = down_scales;
-    p.down_gs = down_gs;
     const MoeWs w = moe_ws(T, k, F, H);
     uint8_t *b = reinterpret_cast<uint8_t *>(ws);
-    p.h = reinterpret_cast<uint4 *>(b);
-    p.h_exp = b + w.exps;
-    p.exp_pitch = (F / 32 + 7) / 8 * 8;
-    p.y = reinterpret_cast<__nv_bfloat16 *>(y);
-    p.splits = moe_splits(H);
-    p.partial = reinterpret_cast<float *>(b + w.partial);
-    p.arrived = reinterpret_cast<int *>(b + w.arrived);
-    p.status = device_status_ptr();
-    p.barrier = grid_barrier_for(s);
-    if (!p.status || !p.barrier)
+    auto f32 = [&](size_t o) { return reinterpret_cast<float *>(b + o); };
+    auto i32 = [&](size_t o) { return reinterpret_cast<int *>(b + o); };
+    MoeGemm g{};
+    g.sh = MoeShared{b + w.x_codes, b + w.x_scales, f32(w.x_factor), 0,
+                     f32(w.h), b + w.h_codes, b + w.h_scales, f32(w.h_factor), 0,
+                     reinterpret_cast<uint32_t *>(b + w.units), i32(w.counts), b + w.tok, f32(w.wt),
+                     f32(w.partial)};
+    g.T = (int)T;
+    g.n_slots = (int)T * k;
+    g.H = H;
+    g.F = F;
+    g.splits = moe_splits(H);
+    g.blocks = (int)((H + kDownRows - 1) / kDownRows);
+    g.y = reinterpret_cast<__nv_bfloat16 *>(y);
+    g.status = device_status_ptr();
+    if (!g.status)
         return cudaErrorInvalidValue;
-    return mx ? launch_experts_fmt<false>(p, s) : launch_experts_fmt<true>(p, s);
+    const uint2 *xv = reinterpret_cast<const uint2 *>(x);
+    return mx ? launch_experts<FmtMxfp4>(g, xv, ids, weights, k, E, up_codes, up_scales, up_gs,
+                                         down_codes, down_scales, down_gs, s)
+              : launch_experts<FmtNvfp4>(g, xv, ids, weights, k, E, up_codes, up_scales, up_gs,
+                                         down_codes, down_scales, down_gs, s);
 }
 
 } // namespace nvfp4

@@ -204,39 +204,54 @@ def make_experts(E, rows, cols, fmt, seed, std=0.05):
     return nv.stack_experts(q), torch.stack(vals)
 
 
+def blocks_max(v):
+    """Largest magnitude of each value's 32-block."""
+    return v.abs().view(-1, 32).max(-1).values.repeat_interleave(32)
+
+
+def terms_error(v):
+    """Bound on what eight FP4 terms leave of v. A term's rounding leaves at most 1/5 of its block's
+    largest remainder (MXFP4, scales rounded up to a power of two: codes between 4 and 6 are 1 off at
+    most, of a largest value of 5 or more there) or 0.18 (NVFP4: 1 of 6 / (1 + 1/16), or saturation
+    at 6 of 6.4): 5^-8 < 2^-18 of the block's largest value. NVFP4 scales end at 2^-10 (half the
+    smallest), a remainder of 6 * 2^-10, with the row's largest value at 1344 or more: 2^-17 of it."""
+    return 2.0 ** -18 * blocks_max(v) + 2.0 ** -17 * v.abs().max()
+
+
 def experts_reference(x, ids, p, up, down):
     """y and a bound on |y_kernel - y| before y's own rounding, in float64.
 
-    a = Wg x: f16 inputs off by at most 2^-25 of their block's largest value (below 2^-14 of it;
-    else exact), fp32 sums of K/16 groups: |da| <= (K/16 * 2^-22 + 2^-25 * 32) * |Wg| |x| with 32
-    bounding a block's largest value by its sum of magnitudes. silu has slope at most 1.1 and
-    |silu(a)| <= |a|; expf, the division and the products add 2^-20 relative. h is rounded to 11
-    bits: 2^-11 relative (half a step 2^-12, doubled for the block's small values, which also take
-    2^-25 of the block's largest). The down sums add (F/16 * 2^-22) |Wd| |h|, the weighted sum
-    over slots, warps and tiles 2^-18 relative of its terms' sizes."""
+    a = Wg x: inputs off by terms_error, and fp32 sums over the terms, whose sizes add up to at most
+    |x| + blocks_max(x) / 2 a value (a term exceeds what is left by at most its rounding: twice
+    1/5 + 1/25 + ...): K/16 additions, each off by at most 2^-22 of the sum of the sizes. silu has
+    slope at most 1.1 and |silu(a)| <= |a|; expf, the division and the products add 2^-20 relative.
+    h is kept in fp32 and enters the down product the same way; the weighted sum over rows and
+    splits adds 2^-18 relative of its terms' sizes."""
     T, H = x.shape
     F = down.shape[2]
     y = torch.zeros(T, H, dtype=torch.float64, device=x.device)
     err = torch.zeros_like(y)
     x = x.double()
+
+    def product_error(w, v, dv):
+        w = w.abs()
+        sizes = w @ (v.abs() + dv + 0.5 * blocks_max(v.abs() + dv))
+        return w @ (dv + terms_error(v.abs() + dv)) + v.numel() / 16 * 2.0 ** -22 * sizes
     for t in range(T):
         for s in range(ids.shape[1]):
             e = int(ids[t, s])
             if not 0 <= e < up.shape[0]:
                 continue
-            a, a_abs = up[e] @ x[t], up[e].abs() @ x[t].abs()
-            da = (H / 16 * 2.0 ** -22 + 2.0 ** -20) * a_abs
+            a, da = up[e] @ x[t], product_error(up[e], x[t], torch.zeros_like(x[t]))
             gate, upv = a[:F], a[F:]
             act = gate / (1 + torch.exp(-gate))
             h = act * upv
             dh = (1.1 * da[:F] + 2.0 ** -20 * act.abs()) * (upv.abs() + da[F:]) \
                 + act.abs() * da[F:]
-            top = (h.abs() + dh).view(-1, 32).max(-1).values.repeat_interleave(32)
-            dh = dh + 2.0 ** -11 * (h.abs() + dh) + 2.0 ** -25 * top
             w = float(p[t, s])
             y[t] += w * (down[e] @ h)
             size = down[e].abs() @ (h.abs() + dh)
-            err[t] += abs(w) * (down[e].abs() @ dh + (F / 16 * 2.0 ** -22 + 2.0 ** -18) * size)
+            err[t] += abs(w) * (product_error(down[e], h, dh) + 2.0 ** -18 * size)
     return y, err
 
 
