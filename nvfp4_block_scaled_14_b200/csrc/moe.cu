@@ -441,9 +441,9 @@ __global__ void __launch_bounds__(kTermThreads) moe_terms_kernel(const MoeShared
 
 // ---- products -----------------------------------------------------------------------------
 
-constexpr int kThreads = 352;
+constexpr int kThreads = 480;
 constexpr uint32_t kWaitLimit = 1u << 20;
-constexpr int kSfAhead = 4;  // k-tiles whose scales are on their way to shared memory
+constexpr int kSfAhead = 2;  // a feeder group's k-tiles whose scales are on their way
 constexpr int kSfRing = kSfAhead + 1;
 constexpr int kMaxStages = 8;
 constexpr int kMaxSmem = 232448 - 1024;
@@ -608,10 +608,11 @@ __device__ __forceinline__ void feed_rows(const uint8_t *sm, uint32_t tcol, int 
 // the weights go from HBM to the tensor cores as they are stored and the sum of a token's eight
 // columns is the product with its full-precision value. One persistent CTA per SM:
 //   warp 0      TMA producer of the weights: per 256-wide k-tile the tile's two 64-row halves;
-//   warp 10     TMA producer of the term rows: one box (down; up to 16 tokens in all), or a box of
+//   warp 14     TMA producer of the term rows: one box (down; up to 16 tokens in all), or a box of
 //               eight rows per token of the column tile;
-//   warps 6..9  scale feeders: the rows' linear scale bytes to shared memory by cp.async, kSfAhead
-//               k-tiles ahead, then to the stage's TMEM columns in the MMA's layout;
+//   warps 6..13 scale feeders, two groups in turn: the rows' linear scale bytes to shared memory by
+//               cp.async ahead of time, then to the stage's TMEM columns in the MMA's layout (one
+//               group takes 750 cycles for that);
 //   warp 1      MMA issuer; accumulators alternate between two TMEM buffers, so that a tile's
 //               epilogue overlaps the next tile's MMAs;
 //   warps 2..5  epilogue. Gate/up: a tile is 64 gate rows and the same 64 up rows; they meet in
@@ -635,7 +636,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     __shared__ __align__(8) uint64_t full_bar[kMaxStages], empty_bar[kMaxStages];
     __shared__ __align__(8) uint64_t acc_full[2], acc_empty[2], drain_bar;
     __shared__ uint32_t tmem_slot;
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int tid = threadIdx.x, lane = tid & 31;
+    // the same in every lane, and known to be: the roles' loops then run on uniform registers
+    const int warp = __shfl_sync(0xFFFFFFFFu, tid >> 5, 0);
     if ((smem_u32(smem) & 1023u) != 0) { // the same for every CTA
         if (tid == 0)
             atomicExch(p.status, (int)NVFP4_ERR_CUDA);
@@ -643,10 +646,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     const int stage_bytes = 16384 + p.b_rows * 128;
     uint8_t *sf_ring = smem + p.stages * stage_bytes;
-    float *s_out = reinterpret_cast<float *>(sf_ring + kSfRing * kSfRows);
+    float *s_out = reinterpret_cast<float *>(sf_ring + 2 * kSfRing * kSfRows);
     if (tid == 0) {
         for (int s = 0; s < p.stages; ++s) {
-            mbar_init(&full_bar[s], 2 + 4); // the producers, the feeders' warps
+            mbar_init(&full_bar[s], 2 + 4); // the producers, a feeder group's warps
             mbar_init(&empty_bar[s], 1);
         }
         for (int s = 0; s < 2; ++s) {
@@ -724,7 +727,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
         }
         __syncwarp();
-    } else if (warp == 10) {
+    } else if (warp == 14) {
         // ------------------------------- the term rows' TMA producer ----------------
         const bool one_box = DOWN || p.dense; // else a box of eight rows per token
         while (walk.next(gr)) {
@@ -749,14 +752,17 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
     } else if (warp >= 6) {
         // ------------------------------- scale feeders ------------------------------
-        const int q = warp & 3, r = tid - 192; // lane quarter of TMEM; this thread's row
+        const int group = (warp - 6) >> 2; // takes every other k-tile
+        const int q = warp & 3;            // lane quarter of TMEM
+        const int r = tid - 192 - 128 * group; // this thread's row
         const int srow = (int)((DOWN ? p.F : p.H) / F::kBlock);
         const int64_t pitch = DOWN ? p.sh.h_pitch : p.sh.x_pitch;
         const uint8_t *bs = DOWN ? p.sh.h_scales : p.sh.x_scales;
         const bool even = srow % SB == 0; // every piece of a row is whole and aligned
-        const uint32_t ring = smem_u32(sf_ring) + r * SB;
-        MoeWalk<DOWN> ahead(p, s_units, n_units); // kSfAhead k-tiles before the stores
-        int akt = 0, akend = 0, aslot = 0;
+        uint8_t *my_ring = sf_ring + group * kSfRing * kSfRows;
+        const uint32_t ring = smem_u32(my_ring) + r * SB;
+        MoeWalk<DOWN> ahead(p, s_units, n_units); // kSfAhead of its k-tiles before the stores
+        int akt = group, akend = 0, aslot = 0;    // (k-tiles count on into the next run)
         bool more = true, a_on = false, b_on = false;
         const uint8_t *asrc = p.a_scales, *bsrc = bs;
         auto zero = [&](uint32_t dst) {
@@ -770,8 +776,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                 more = ahead.next(ga);
                 if (!more)
                     break;
-                akt = ga.k0;
+                akt += ga.k0 - akend;
                 akend = ga.k1;
+                if (akt >= akend)
+                    continue;
                 const int64_t row = r < 64 ? ga.ra0 + r : ga.ra1 + (r - 64);
                 a_on = row < p.a_rows;
                 asrc = p.a_scales + (a_on ? row * srow + (int64_t)akt * SB : 0);
@@ -797,9 +805,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                     cp_async<SB>(dst + 128 * SB, bsrc);
                 else
                     zero(dst + 128 * SB);
-                asrc += a_on ? SB : 0;
-                bsrc += SB;
-                ++akt;
+                asrc += a_on ? 2 * SB : 0;
+                bsrc += 2 * SB;
+                akt += 2;
                 aslot = aslot + 1 == kSfRing ? 0 : aslot + 1;
             }
             asm volatile("cp.async.commit_group;" ::: "memory");
@@ -807,17 +815,21 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll 1
         for (int i = 0; i < kSfAhead; ++i)
             load();
-        int rslot = 0;
+        int rslot = 0, turn = group;
         const uint32_t tbase = tmem + ((uint32_t)(q * 32) << 16) + kSfCol;
         while (walk.next(gr)) {
             for (int kt = gr.k0; kt < gr.k1; ++kt) {
+                if (turn++ & 1) {
+                    next_stage();
+                    continue;
+                }
                 asm volatile("cp.async.wait_group %0;" ::"n"(kSfAhead - 1) : "memory");
-                named_bar_sync(2, 128); // the rows are here, and the last k-tile's have been read
+                named_bar_sync(2 + group, 128); // the rows are here, and the last k-tile's have been read
                 load();
                 wait(&empty_bar[stage], phase ^ 1);
                 __syncwarp();
                 tc_fence_after();
-                const uint8_t *src = sf_ring + rslot * kSfRows;
+                const uint8_t *src = my_ring + rslot * kSfRows;
                 feed_rows<F>(src, tbase + stage * kSlotCols, lane);
                 feed_rows<F>(src + 128 * SB, tbase + stage * kSlotCols + 16, lane);
                 tmem_st_wait();
@@ -848,7 +860,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 wait(&full_bar[stage], phase);
                 __syncwarp();
                 tc_fence_after();
-                if (lane == 0) {
+                if (elect_one()) {
                     const uint32_t tsf = tmem + kSfCol + stage * kSlotCols;
                     const uint64_t adesc = desc0 + (uint64_t)((stage * stage_bytes) >> 4);
                     const uint64_t bdesc = adesc + (16384u >> 4);
@@ -863,17 +875,17 @@ __global__ void __launch_bounds__(kThreads, 1)
                 __syncwarp();
                 next_stage();
             }
-            if (lane == 0)
+            if (elect_one())
                 tc_commit(&acc_full[buf]);
             __syncwarp();
             buf ^= 1;
             if (buf == 0)
                 aphase ^= 1;
         }
-        if (lane == 0) { // every MMA issued completes before TMEM is freed
+        // every MMA issued completes before TMEM is freed (one lane issued them all)
+        if (elect_one())
             tc_commit(&drain_bar);
-            wait(&drain_bar, 0);
-        }
+        wait(&drain_bar, 0);
         __syncwarp();
     } else {
         // ------------------------------- epilogue (warps 2..5) ----------------------
@@ -1017,7 +1029,7 @@ cudaError_t launch_gemm(MoeGemm g, const CUtensorMap &tmA, const CUtensorMap &tm
     });
     if (e != cudaSuccess)
         return e;
-    const int fixed = kSfRing * 2 * 128 * 4 * F::kAtoms + (DOWN ? g.T : kCols) * 128 * 4 +
+    const int fixed = 2 * kSfRing * 2 * 128 * 4 * F::kAtoms + (DOWN ? g.T : kCols) * 128 * 4 +
                       9 * g.n_slots;
     const int stage = 16384 + g.b_rows * 128;
     const int fit = (kMaxSmem - fixed) / stage;

@@ -171,6 +171,15 @@ __device__ __forceinline__ void bulk_load_1d(void *dst, const void *src, uint32_
                  : "memory");
 }
 
+// True in one lane of the (converged) warp, always the same one.
+__device__ __forceinline__ bool elect_one()
+{
+    uint32_t r;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xFFFFFFFF;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+                 : "=r"(r));
+    return r != 0u;
+}
+
 // ---------------------------------------------------------------------------------------
 // tcgen05
 // ---------------------------------------------------------------------------------------
