@@ -7,14 +7,16 @@
 //
 // The weights go to the FP4 tensor cores as they are stored. Those multiply FP4 by FP4 only, so an
 // activation is split into eight FP4 terms, each the FP4 form of what the ones before leave
-// (write_terms), and the eight products are added: the weights lose nothing and the activations
-// about 2^-18 of their block's largest value, while the terms' columns cost the otherwise idle MMA
+// (put_terms), and the eight products are added: the weights lose nothing and the activations at
+// most 2^-22 (MXFP4) of their block's largest value, or 2^-19 (NVFP4) of their row's, while the terms' columns cost the otherwise idle MMA
 // 8 of its up to 256 columns a token. (Decoding the weights to f16 on the CUDA cores for mma.sync
 // took 40-54 issue slots per 16 x 32 codes, as long as HBM takes to deliver them, and ran at a
 // quarter of it: 64 tokens, 64 experts of 2048 x 1024, top 8: 135 us.)
 #include <mutex>
+#include <type_traits>
 
 #include "fp4_format.cuh"
+#include "grid_exchange.cuh"
 #include "mxfp4_encode.cuh"
 #include "nvfp4_internal.cuh"
 #include "sm100_ptx.cuh"
@@ -190,6 +192,7 @@ __global__ void __cluster_dims__(kRouteCluster, 1, 1) __launch_bounds__(kRouteTh
 
 constexpr int kTerms = 8;  // FP4 terms of an activation: the rows of one swizzle atom
 constexpr int kCols = 16;  // tokens of a column tile: 128 MMA columns
+constexpr int kThreads = 480;
 constexpr int kUpRows = 64, kDownRows = 128; // rows of F, of H, per tile
 
 // A column tile: up to kCols of the (expert, token) rows of one expert. Packed: 9 bits of expert, 11
@@ -208,44 +211,46 @@ __device__ __forceinline__ MoeUnit unpack_unit(uint32_t u)
     return MoeUnit{(int)(u & 0x1FFu), (int)(u >> 9 & 0x7FFu), (int)(u >> 20) + 1};
 }
 
-// What the kernels of one call share in the workspace.
+// What the CTAs of one call share in the workspace. Rows: the (expert, token) pairs, in expert order.
 struct MoeShared {
-    uint8_t *x_codes, *x_scales; // terms of x: [T * 8][H / 2], [T * 8][x_pitch]
-    float *x_factor;             // [T] (NVFP4): the power of two a token was divided by
-    int64_t x_pitch;
-    float *h;                    // [rows][F]: silu(gate) * up of each (expert, token) row
-    uint8_t *h_codes, *h_scales; // its terms
-    float *h_factor;
-    int64_t h_pitch;
-    uint32_t *units;
-    int *counts;                 // column tiles, rows
-    uint8_t *tok;                // [rows] token
-    float *wt;                   // [rows] weight
+    uint8_t *x_codes, *x_scales; // terms of the rows' x: [rows * 8][H / 2], [rows * 8][x_pitch]
+    uint8_t *h_codes, *h_scales; // terms of the rows' h = silu(gate) * up
+    int64_t x_pitch, h_pitch;
+    uint32_t *x_max, *h_max;     // [rows] (NVFP4): bits of the row's largest magnitude
+    float *h;                    // [rows][F] (NVFP4)
     float *partial;              // [128-row blocks of y][splits][T][128]
 };
 
 // ---- lists and terms ----------------------------------------------------------------------
 
-constexpr int kPrepThreads = 512, kTermThreads = 256;
-
 // The (expert, token) pairs that the ids name, in expert order, as rows: the row's token and weight
 // (an expert that a token names twice gets one row with both weights), and the column tiles. ids
-// outside [0, E) name no expert. One CTA.
-__device__ __forceinline__ void build_lists(const MoeShared &sh, const int *ids,
-                                            const float *weights, int T, int k, int E,
-                                            uint8_t *smem)
+// outside [0, E) name no expert. In the CTA's shared memory.
+struct MoeLists {
+    float *wt;       // [rows]
+    uint32_t *units; // [column tiles]
+    int *counts;     // column tiles, rows
+    uint8_t *tok;    // [rows]
+};
+
+// Built by the whole CTA. tmp: 12 E + 6 T k bytes.
+__device__ __forceinline__ void build_lists(const MoeLists &l, const int *ids, const float *weights,
+                                            int T, int k, int E, uint8_t *tmp)
 {
-    uint32_t *mask = reinterpret_cast<uint32_t *>(smem); // [E][2]: the expert's tokens
-    int *base = reinterpret_cast<int *>(mask + 2 * E);   // [E]: its first row
-    int16_t *s_ids = reinterpret_cast<int16_t *>(base + E);
-    const int tid = threadIdx.x, nthr = blockDim.x, n = T * k;
+    uint32_t *mask = reinterpret_cast<uint32_t *>(tmp); // [E][2]: the expert's tokens
+    int *base = reinterpret_cast<int *>(mask + 2 * E);  // [E]: its first row
+    float *s_w = reinterpret_cast<float *>(base + E);
+    int16_t *s_ids = reinterpret_cast<int16_t *>(s_w + T * k);
+    const int n = T * k, tid = threadIdx.x;
     auto count = [&](int e) { return __popc(mask[2 * e]) + __popc(mask[2 * e + 1]); };
-    for (int i = tid; i < 2 * E; i += nthr)
+    int id = tid < n ? __ldg(ids + tid) : -1; // on its way while the masks are cleared
+    for (int i = tid; i < 2 * E; i += kThreads)
         mask[i] = 0u;
     __syncthreads();
-    for (int i = tid; i < n; i += nthr) {
-        const int e = __ldg(ids + i), t = i / k;
+    for (int i = tid; i < n; i += kThreads) {
+        const int e = i == tid ? id : __ldg(ids + i), t = i / k;
         const bool on = e >= 0 && e < E;
+        s_w[i] = __ldg(weights + i);
         s_ids[i] = on ? (int16_t)e : (int16_t)-1;
         if (on)
             atomicOr(&mask[2 * e + (t >> 5)], 1u << (t & 31));
@@ -271,8 +276,8 @@ __device__ __forceinline__ void build_lists(const MoeShared &sh, const int *ids,
             }
         }
         if (tid == 31) {
-            sh.counts[0] = u0;
-            sh.counts[1] = r0;
+            l.counts[0] = u0;
+            l.counts[1] = r0;
         }
         r0 -= rows;
         u0 -= tiles;
@@ -283,12 +288,12 @@ __device__ __forceinline__ void build_lists(const MoeShared &sh, const int *ids,
             const int c = count(e);
             base[e] = r0;
             for (int c0 = 0; c0 < c; c0 += kCols)
-                sh.units[u0++] = pack_unit(e, r0 + c0, min(kCols, c - c0));
+                l.units[u0++] = pack_unit(e, r0 + c0, min(kCols, c - c0));
             r0 += c;
         }
     }
     __syncthreads();
-    for (int i = tid; i < n; i += nthr) {
+    for (int i = tid; i < n; i += kThreads) {
         const int e = s_ids[i], t = i / k;
         if (e < 0)
             continue;
@@ -297,151 +302,137 @@ __device__ __forceinline__ void build_lists(const MoeShared &sh, const int *ids,
         for (int s = t * k; s < (t + 1) * k; ++s)
             if (s_ids[s] == e) {
                 first = first && s >= i;
-                w += __ldg(weights + s);
+                w += s_w[s];
             }
         if (first) {
             const uint32_t *m = mask + 2 * e;
             const int before = t < 32 ? __popc(m[0] & ((1u << t) - 1u))
                                       : __popc(m[0]) + __popc(m[1] & ((1u << (t - 32)) - 1u));
             const int row = base[e] + before;
-            sh.tok[row] = (uint8_t)t;
-            sh.wt[row] = w;
+            l.tok[row] = (uint8_t)t;
+            l.wt[row] = w;
         }
     }
 }
 
-size_t lists_smem(int T, int k, int E) { return 12 * (size_t)E + 2 * (size_t)T * k; }
-
-// One row of activations (load(i): values 4i .. 4i + 3) as kTerms FP4 rows: each term is the FP4
-// form of what the terms before leave, so that the sum of the terms is the value up to the last
-// remainder. MXFP4 terms have their own E8M0 scale per 32 values ("ceil": nothing saturates; a
-// rounding is off by at most 1/5 of the block's largest remainder, 5^-8 = 2^-18.6 in all). NVFP4
-// terms have an E4M3 scale per 16 values, of the row divided by a power of two that brings its
-// largest value to 1344..2688 (off by at most 1/6 + 1/16 of the block's largest remainder a term,
-// down to the smallest scale's 2^-18 of the row's largest value). A row with a NaN or an infinity
-// gets NaN scales (MXFP4) or a NaN factor, and so NaN results. Eight lanes take 32 values.
-template <bool NV, int THREADS, typename Load>
-__device__ __forceinline__ void write_terms(int64_t cols, uint8_t *codes, uint8_t *scales,
-                                            int64_t pitch, float *factor, Load load)
+// Activations as kTerms FP4 terms. A block's first term has the power of two as its scale with which
+// its largest value lies in 3..6 steps: a rounding leaves at most one step (between 4 and 6), a 1/5 of
+// that value. The second term's step is a quarter of that, each further one's an eighth of the one
+// before: what is left is at most 4 of these steps, and half a step after the rounding. So the scales
+// follow from the first one, a term costs a lane no exchange, every subtraction is exact, and the
+// eight terms leave at most 2^-21 of the first step, 2^-22 of the block's largest value. Steps end at
+// the format's smallest scale: MXFP4 (E8M0, blocks of 32) 2^-127. NVFP4 (E4M3, blocks of 16) has
+// 2^8 .. 2^-9 only, of the row divided by a power of two that brings its largest value to 512..1024:
+// 2^-10 is left, 2^-19 of that value. (The first version gave each term the best scale for what the
+// terms before left; a block's maximum for every term took the 512 x 1024 values of 64 tokens 10 us.)
+// A NaN or an infinity: the block's first scale is NaN (MXFP4), or the row's factor is (NVFP4), and
+// so the row's results are.
+//
+// v: values c0 .. c0 + 7 of a row of `cols`, lane i's c0 being lane 0's + 8 i in aligned groups of four
+// lanes; zeros behind the row's end. codes, scales: the row's first term. Called by whole warps.
+template <bool NV>
+__device__ __forceinline__ void put_terms(const float (&v)[8], int64_t c0, int64_t cols,
+                                          uint8_t *codes, uint8_t *scales, int64_t pitch, bool live)
 {
-    const int tid = threadIdx.x, lane = tid & 31, sub = lane & 7;
-    float inv_row = 1.0f;
-    if constexpr (NV) { // the row's power of two
-        __shared__ uint32_t s_max[THREADS / 32];
-        uint32_t m = 0u;
-        for (int64_t i = tid; i < cols / 4; i += THREADS) {
-            const float4 v = load(i);
-            m = max(max(m, max(__float_as_uint(v.x) & 0x7FFFFFFFu, __float_as_uint(v.y) & 0x7FFFFFFFu)),
-                    max(__float_as_uint(v.z) & 0x7FFFFFFFu, __float_as_uint(v.w) & 0x7FFFFFFFu));
-        }
-        m = __reduce_max_sync(0xFFFFFFFFu, m);
-        if (lane == 0)
-            s_max[tid >> 5] = m;
-        __syncthreads();
-        m = s_max[lane & (THREADS / 32 - 1)];
-        m = __reduce_max_sync(0xFFFFFFFFu, m);
-        // 2^k, k = floor(log2 max) - 10, kept where both it and its inverse are normal
-        const int e = min(max((int)(m >> 23) - 10, 1), 253);
-        inv_row = __uint_as_float((uint32_t)(254 - e) << 23);
-        if (tid == 0)
-            *factor = m >= 0x7F800000u ? __uint_as_float(0x7FC00000u)
-                                       : __uint_as_float((uint32_t)e << 23);
-    }
-    const int64_t groups = (pitch * (NV ? 16 : 32) + 31) / 32; // 32-value groups, padding included
-    for (int64_t b = tid >> 3; b < groups; b += THREADS / 8) { // (whole warps in step)
-        const bool on = b * 32 < cols;
-        float4 v = on ? load(b * 8 + sub) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-        if constexpr (NV) {
-            v.x *= inv_row;
-            v.y *= inv_row;
-            v.z *= inv_row;
-            v.w *= inv_row;
-        }
+    constexpr int kBlock = NV ? 16 : 32;
+    constexpr uint32_t kLow = NV ? 127 - 9 : 0;
+    uint32_t m = 0u;
 #pragma unroll
-        for (int j = 0; j < kTerms; ++j) {
-            uint32_t m =
-                max(max(__float_as_uint(v.x) & 0x7FFFFFFFu, __float_as_uint(v.y) & 0x7FFFFFFFu),
-                    max(__float_as_uint(v.z) & 0x7FFFFFFFu, __float_as_uint(v.w) & 0x7FFFFFFFu));
-            m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 1));
-            m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 2));
-            uint32_t sb;
-            float s, inv;
-            if constexpr (NV) {
-                sb = m >= 0x7F800000u ? 0u : cvt_e4m3(__uint_as_float(m) * (1.0f / 6.0f));
-                s = e4m3_to_f32(sb);
-                inv = sb != 0u ? __frcp_rn(s) : 0.0f;
-            } else {
-                m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 4));
-                sb = mx_scale_byte(m, true);
-                s = sb == kMxNan ? 0.0f : mx_scale_f32(sb);
-                inv = mx_inverse(sb);
-            }
-            const float y[8] = {v.x * inv, v.y * inv, v.z * inv, v.w * inv, 0.0f, 0.0f, 0.0f, 0.0f};
-            const uint32_t w = inv != 0.0f ? cvt_e2m1x8(y) & 0xFFFFu : 0u;
-            const float2 lo = e2m1x2_to_f32x2(w & 0xFFu), hi = e2m1x2_to_f32x2(w >> 8);
-            v.x = fmaf(-lo.x, s, v.x);
-            v.y = fmaf(-lo.y, s, v.y);
-            v.z = fmaf(-hi.x, s, v.z);
-            v.w = fmaf(-hi.y, s, v.w);
-            if (!NV && sb == kMxNan)
-                v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-            if (on)
-                *reinterpret_cast<uint16_t *>(codes + j * (cols >> 1) + b * 16 + sub * 2) =
-                    (uint16_t)w;
-            if (NV) {
-                if ((sub & 3) == 0 && 2 * b + (sub >> 2) < pitch)
-                    scales[j * pitch + 2 * b + (sub >> 2)] = on ? (uint8_t)sb : (uint8_t)0;
-            } else if (sub == 0 && b < pitch) {
-                scales[j * pitch + b] = on ? (uint8_t)sb : (uint8_t)0;
-            }
+    for (int i = 0; i < 8; ++i)
+        m = max(m, __float_as_uint(v[i]) & 0x7FFFFFFFu);
+    m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 1));
+    if constexpr (!NV)
+        m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 2));
+    uint32_t b = mx_scale_byte(m, true); // of the power of two, also where E4M3 holds it
+    const bool bad = b == kMxNan;
+    if constexpr (NV)
+        b = min(max(b, kLow), 127u + 8u);
+    const float inv = mx_inverse(b);
+    float2 r[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        r[i] = bad ? make_float2(0.0f, 0.0f)
+                   : __fmul2_rn(make_float2(v[2 * i], v[2 * i + 1]), make_float2(inv, inv));
+    const bool on = live && c0 < cols;
+    const bool put_scale = live && c0 % kBlock == 0 && c0 / kBlock < pitch;
+    codes += c0 >> 1;
+    scales += c0 / kBlock;
+#pragma unroll
+    for (int j = 0; j < kTerms; ++j) {
+        if (j > 0) {
+            const uint32_t d = min(j == 1 ? 2u : 3u, b - kLow);
+            b -= d;
+            const float up = __uint_as_float((127u + d) << 23);
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                r[i] = __fmul2_rn(r[i], make_float2(up, up));
+        }
+        const float y[8] = {r[0].x, r[0].y, r[1].x, r[1].y, r[2].x, r[2].y, r[3].x, r[3].y};
+        const uint32_t w = cvt_e2m1x8(y);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const float2 q = e2m1x2_to_f32x2(w >> (8 * i) & 0xFFu);
+            r[i] = __fadd2_rn(r[i], make_float2(-q.x, -q.y));
+        }
+        if (on)
+            *reinterpret_cast<uint32_t *>(codes + j * (cols >> 1)) = w;
+        if (put_scale) {
+            const uint32_t e4 = b >= 127u - 6u ? (b - 120u) << 3 : 1u << (b - kLow);
+            scales[j * pitch] = on ? (uint8_t)(NV ? e4 : b) : (uint8_t)0;
         }
     }
 }
 
-__device__ __forceinline__ float4 bf16x4(uint2 v)
+// The power of two that a row with the largest magnitude m (bits) is divided by: kept where both it
+// and its inverse are normal.
+__device__ __forceinline__ uint32_t row_exponent(uint32_t m)
 {
-    return make_float4(__uint_as_float(v.x << 16), __uint_as_float(v.x & 0xFFFF0000u),
-                       __uint_as_float(v.y << 16), __uint_as_float(v.y & 0xFFFF0000u));
+    return (uint32_t)min(max((int)(m >> 23) - 9, 1), 253);
 }
 
-// The tokens' terms (one CTA a token) and, in the last CTA, the lists.
-template <bool NV>
-__global__ void __launch_bounds__(kPrepThreads)
-    moe_prepare_kernel(const MoeShared sh, const uint2 *x, const int *ids, const float *weights,
-                       int T, int k, int E, int64_t H)
+__device__ __forceinline__ float row_inverse(uint32_t m)
 {
-    extern __shared__ __align__(16) uint8_t list_smem[];
-    pdl_launch_dependents();
-    pdl_wait();
-    const int t = blockIdx.x;
-    if (t == T) {
-        build_lists(sh, ids, weights, T, k, E, list_smem);
-        return;
+    return __uint_as_float((254u - row_exponent(m)) << 23);
+}
+
+__device__ __forceinline__ float row_factor(uint32_t m)
+{
+    return __uint_as_float(m >= 0x7F800000u ? 0x7FC00000u : row_exponent(m) << 23);
+}
+
+// A CTA's share of the rows' 256-value chunks, one warp each.
+struct MoeChunks {
+    int64_t per, first, last;
+
+    __device__ __forceinline__ MoeChunks(int64_t rows, int64_t cols)
+    {
+        per = (cols + 255) >> 8;
+        first = rows * per * blockIdx.x / gridDim.x;
+        last = rows * per * (blockIdx.x + 1) / gridDim.x;
     }
-    const uint2 *row = x + t * (H >> 2);
-    write_terms<NV, kPrepThreads>(H, sh.x_codes + (int64_t)t * kTerms * (H >> 1),
-                    sh.x_scales + (int64_t)t * kTerms * sh.x_pitch, sh.x_pitch, sh.x_factor + t,
-                    [&](int64_t i) { return bf16x4(__ldg(row + i)); });
-}
+};
 
-// The terms of h, one CTA a row.
-template <bool NV>
-__global__ void __launch_bounds__(kTermThreads) moe_terms_kernel(const MoeShared sh, int64_t F)
+// Terms of the CTA's chunks, by all warps but warp 0; load(row, c0, v): eight values.
+template <bool NV, typename Load>
+__device__ __forceinline__ void write_terms(const MoeChunks &ch, int64_t cols, uint8_t *codes,
+                                            uint8_t *scales, int64_t pitch, int warp, Load load)
 {
-    pdl_launch_dependents();
-    pdl_wait();
-    const int r = blockIdx.x;
-    if (r >= sh.counts[1])
+    const int lane = threadIdx.x & 31;
+    if (warp == 0)
         return;
-    const float4 *row = reinterpret_cast<const float4 *>(sh.h + (int64_t)r * F);
-    write_terms<NV, kTermThreads>(F, sh.h_codes + (int64_t)r * kTerms * (F >> 1),
-                    sh.h_scales + (int64_t)r * kTerms * sh.h_pitch, sh.h_pitch, sh.h_factor + r,
-                    [&](int64_t i) { return __ldcg(row + i); });
+    for (int64_t i = ch.first + warp - 1; i < ch.last; i += kThreads / 32 - 1) {
+        const int64_t row = i / ch.per, c0 = (i % ch.per) * 256 + lane * 8;
+        float v[8] = {};
+        if (c0 < cols)
+            load(row, c0, v);
+        put_terms<NV>(v, c0, cols, codes + row * kTerms * (cols >> 1), scales + row * kTerms * pitch,
+                      pitch, true);
+    }
 }
 
 // ---- products -----------------------------------------------------------------------------
 
-constexpr int kThreads = 480;
+constexpr uint32_t kBarrierLimit = 1u << 21;
 constexpr uint32_t kWaitLimit = 1u << 20;
 constexpr int kSfAhead = 2;  // a feeder group's k-tiles whose scales are on their way
 constexpr int kSfRing = kSfAhead + 1;
@@ -450,15 +441,18 @@ constexpr int kMaxSmem = 232448 - 1024;
 
 struct MoeGemm {
     MoeShared sh;
-    int T, n_slots;          // tokens, T x top_k
+    const uint4 *x; // bf16 [T x H]
+    const int *ids;
+    const float *weights;
+    int T, k, E;
     int64_t H, F;
-    const uint8_t *a_scales; // the experts', linear
-    int64_t a_rows;          // rows of the stacked weights
-    const float *gs;         // [E] (NVFP4)
-    int stages, b_rows;      // operand ring: stages, term rows of a stage
-    int dense;               // gate/up: a stage holds all tokens' term rows, in token order
+    const uint8_t *up_scales, *down_scales; // linear
+    const float *up_gs, *down_gs;           // [E] (NVFP4)
+    int stages, stage_bytes; // operand ring
+    int box;                 // term rows of a TMA box
     int splits, blocks;      // down: CTAs per 128-row block of y, blocks
     __nv_bfloat16 *y;
+    GridBarrier *barrier;
     int *status;
 };
 
@@ -472,59 +466,67 @@ struct MoeGroup {
     bool last;        // down: the job's last run
 };
 
+// Where a CTA's share begins, computed once (in shared memory). k-tiles and 64-column tiles of the
+// longest allowed axes times the 2048 rows pass 32 bits only where the weights pass the memory.
+struct MoeStart {
+    int up_kt, up_tiles, down_kt; // k-tiles of H, 64-column tiles of F, k-tiles of F
+    int runs, u, tile;            // gate/up: runs of this CTA, the first one's column tile and tile
+    uint32_t q, r;                // down: (column tile, k-tile) pairs of a split, splits with one more
+
+    __device__ __forceinline__ uint32_t cut(uint32_t split) const
+    {
+        return split * q + min(split, r);
+    }
+};
+
 // The groups of a CTA, in order; every role of the CTA walks them by itself. Gate/up: a run of the
 // flat list of (column tile, 64 columns of F). Down: jobs (128-row block of y, split), whose run of
 // the flat list of (column tile, k-tile) pairs is cut at the column tiles.
 template <bool DOWN> struct MoeWalk {
     const MoeGemm &p;
     const uint32_t *units; // in shared memory
-    int n_units, nkt, per;
-    int64_t i, i1;       // gate/up
-    int job, u, kt;      // down
-    int64_t rest;
+    const MoeStart &st;
+    int rest, u, tile; // runs (gate/up) or k-tiles (down) left, column tile, tile of it
+    int job;           // down
 
-    __device__ __forceinline__ MoeWalk(const MoeGemm &q, const uint32_t *list, int n)
-        : p(q), units(list), n_units(n)
+    __device__ __forceinline__ MoeWalk(const MoeGemm &q, const uint32_t *list, const MoeStart &s)
+        : p(q), units(list), st(s)
     {
-        const int64_t K = DOWN ? p.F : p.H;
-        nkt = (int)((K + 255) >> 8);
-        if constexpr (DOWN) {
-            job = (int)blockIdx.x - (int)gridDim.x;
-            rest = -1;
-        } else {
-            per = (int)((p.F + kUpRows - 1) / kUpRows);
-            const int64_t n = (int64_t)n_units * per;
-            i = n * blockIdx.x / gridDim.x;
-            i1 = n * (blockIdx.x + 1) / gridDim.x;
-        }
+        rest = DOWN ? -1 : s.runs;
+        u = s.u;
+        tile = s.tile;
+        job = (int)blockIdx.x - (int)gridDim.x;
     }
 
     __device__ __forceinline__ bool next(MoeGroup &g)
     {
         if constexpr (!DOWN) {
-            if (i >= i1)
+            if (rest == 0)
                 return false;
-            g.unit = unpack_unit(units[(int)(i / per)]);
-            g.first = (int)(i % per) * kUpRows;
+            --rest;
+            g.unit = unpack_unit(units[u]);
+            g.first = tile * kUpRows;
             g.ra0 = (int64_t)g.unit.expert * 2 * p.F + g.first;
             g.ra1 = g.ra0 + p.F;
             g.k0 = 0;
-            g.k1 = nkt;
-            ++i;
+            g.k1 = st.up_kt;
+            if (++tile == st.up_tiles) {
+                tile = 0;
+                ++u;
+            }
         } else {
             if (rest <= 0) {
                 job += gridDim.x;
                 if (job >= p.blocks * p.splits)
                     return false;
-                const int64_t total = (int64_t)n_units * nkt;
-                g.split = job % p.splits;
-                const int64_t a = total * g.split / p.splits;
-                rest = total * (g.split + 1) / p.splits - a;
-                u = (int)(a / nkt);
-                kt = (int)(a % nkt);
+                const uint32_t split = (uint32_t)job % (uint32_t)p.splits;
+                const uint32_t a = st.cut(split);
+                rest = (int)(st.cut(split + 1) - a);
+                u = (int)(a / (uint32_t)st.down_kt);
+                tile = (int)(a % (uint32_t)st.down_kt);
             }
-            g.first = job / p.splits;
-            g.split = job % p.splits;
+            g.first = (int)((uint32_t)job / (uint32_t)p.splits);
+            g.split = job - g.first * p.splits;
             if (rest == 0) {
                 g.unit = MoeUnit{0, 0, 0};
                 g.k0 = g.k1 = 0;
@@ -534,11 +536,11 @@ template <bool DOWN> struct MoeWalk {
             g.unit = unpack_unit(units[u]);
             g.ra0 = (int64_t)g.unit.expert * p.H + (int64_t)g.first * kDownRows;
             g.ra1 = g.ra0 + 64;
-            g.k0 = kt;
-            g.k1 = (int)(rest < nkt - kt ? kt + rest : nkt);
+            g.k0 = tile;
+            g.k1 = min(tile + rest, st.down_kt);
             rest -= g.k1 - g.k0;
             ++u;
-            kt = 0;
+            tile = 0;
             g.last = rest == 0;
         }
         return true;
@@ -603,32 +605,123 @@ __device__ __forceinline__ void feed_rows(const uint8_t *sm, uint32_t tcol, int 
         tmem_st_32x32b_x16(tcol, r);
 }
 
-// Gate/up (DOWN false) and down products on the FP4 tensor cores: 128 weight rows are the M side of
-// block-scaled MMAs, eight term rows of each token of a column tile the N side (8..128 columns), so
-// the weights go from HBM to the tensor cores as they are stored and the sum of a token's eight
-// columns is the product with its full-precision value. One persistent CTA per SM:
-//   warp 0      TMA producer of the weights: per 256-wide k-tile the tile's two 64-row halves;
-//   warp 14     TMA producer of the term rows: one box (down; up to 16 tokens in all), or a box of
-//               eight rows per token of the column tile;
-//   warps 6..13 scale feeders, two groups in turn: the rows' linear scale bytes to shared memory by
-//               cp.async ahead of time, then to the stage's TMEM columns in the MMA's layout (one
-//               group takes 750 cycles for that);
-//   warp 1      MMA issuer; accumulators alternate between two TMEM buffers, so that a tile's
-//               epilogue overlaps the next tile's MMAs;
-//   warps 2..5  epilogue. Gate/up: a tile is 64 gate rows and the same 64 up rows; they meet in
-//               shared memory and silu(gate) * up goes to the workspace in fp32. Down: the weighted
-//               sums of every column tile are added to [T][128] sums in shared memory, which go to y
-//               or, split by split, to the workspace (moe_sum_kernel).
-// A stage's bytes and scales complete one barrier, and the MMAs that have read them another.
-// Bound by HBM: a k-tile's 16 KB take 370 ns of an SM's share, its four MMAs of N = 64 about 70 ns;
-// a role must therefore take fewer than 700 cycles a k-tile, which is why each is a warp of its own
-// with few instructions a step. Waits are bounded; after one that gave up the roles run on without
-// waiting and the status word says so.
-template <class F, bool DOWN>
-__global__ void __launch_bounds__(kThreads, 1)
-    moe_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
-                    const MoeGemm p)
+// A scale feeder thread's row: its scale bytes of every other k-tile, from `first` on (k-tiles count on
+// from one run into the next), into a ring of kSfRing rows of 128 of weights and 128 of terms.
+template <class F, bool DOWN> struct ScaleRow {
+    static constexpr int SB = 4 * F::kAtoms; // bytes of a row and k-tile
+    const MoeGemm &p;
+    MoeWalk<DOWN> walk;
+    uint32_t ring; // this row's slot 0
+    int r, srow, slot;
+    int kt, kend = 0;
+    bool more = true, a_on = false, b_on = false;
+    const uint8_t *asrc, *bsrc;
+
+    __device__ __forceinline__ ScaleRow(const MoeGemm &q, const uint32_t *units, const MoeStart &st,
+                                        int row, uint32_t ring_row, int first, int first_slot)
+        : p(q), walk(q, units, st), ring(ring_row), r(row), slot(first_slot), kt(first)
+    {
+        srow = (int)((DOWN ? p.F : p.H) / F::kBlock);
+    }
+
+    __device__ __forceinline__ static void zero(uint32_t dst)
+    {
+#pragma unroll
+        for (int i = 0; i < SB; i += 4)
+            asm volatile("st.shared.u32 [%0], %1;" ::"r"(dst + i), "r"(0u) : "memory");
+    }
+
+    // The next k-tile's bytes (of the weights, of the terms), as one cp.async group.
+    __device__ __forceinline__ void load(bool weights, bool terms)
+    {
+        while (more && kt >= kend) {
+            MoeGroup g;
+            more = walk.next(g);
+            if (!more)
+                break;
+            kt += g.k0 - kend;
+            kend = g.k1;
+            if (kt >= kend)
+                continue;
+            const int64_t row = r < 64 ? g.ra0 + r : g.ra1 + (r - 64);
+            a_on = row < (int64_t)p.E * (DOWN ? p.H : 2 * p.F);
+            asrc = (DOWN ? p.down_scales : p.up_scales) + (a_on ? row * srow + (int64_t)kt * SB : 0);
+            b_on = r / kTerms < g.unit.ncol; // a token of the column tile
+            bsrc = (DOWN ? p.sh.h_scales : p.sh.x_scales) +
+                   ((int64_t)g.unit.row0 * kTerms + r) * (DOWN ? p.sh.h_pitch : p.sh.x_pitch) +
+                   (int64_t)kt * SB;
+        }
+        if (more) {
+            const uint32_t dst = ring + slot * (2 * 128 * SB);
+            if (weights) {
+                if (!a_on)
+                    zero(dst);
+                else if (srow % SB == 0) // every piece of a row is whole and aligned
+                    cp_async<SB>(dst, asrc);
+                else
+                    fetch_scales_general<SB>(dst, asrc, min(SB, srow - kt * SB));
+            }
+            if (terms) {
+                if (b_on)
+                    cp_async<SB>(dst + 128 * SB, bsrc);
+                else
+                    zero(dst + 128 * SB);
+            }
+            asrc += a_on ? 2 * SB : 0;
+            bsrc += 2 * SB;
+            kt += 2;
+            slot = slot + 1 == kSfRing ? 0 : slot + 1;
+        }
+        asm volatile("cp.async.commit_group;" ::: "memory");
+    }
+};
+
+// Four columns of y.
+__device__ __forceinline__ void put_y(__nv_bfloat16 *y, const float4 &v)
 {
+    const __nv_bfloat162 lo = __floats2bfloat162_rn(v.x, v.y);
+    const __nv_bfloat162 hi = __floats2bfloat162_rn(v.z, v.w);
+    *reinterpret_cast<uint2 *>(y) = make_uint2(*reinterpret_cast<const uint32_t *>(&lo),
+                                               *reinterpret_cast<const uint32_t *>(&hi));
+}
+
+// The experts in one cooperative launch, one CTA per SM, five phases between grid barriers (a launch
+// of its own for each cost 3 to 4 us more):
+//   lists of the (expert, token) rows (every CTA its own) and the rows' terms of x;
+//   gate/up products and, for MXFP4, the terms of h, whose blocks lie in one tile;
+//   terms of h, for NVFP4, whose rows are divided by a power of two of their largest value first;
+//   down products;
+//   the splits' sums of y (where a block of y is shared by several CTAs).
+// Products, on the FP4 tensor cores: 128 weight rows are the M side of block-scaled MMAs, eight term
+// rows of each token of a column tile the N side (8..128 columns), so the weights go from HBM to the
+// tensor cores as they are stored and the sum of a token's eight columns is the product with its
+// full-precision value. Roles:
+//   warp 0       TMA producer of the weights: per 256-wide k-tile the tile's two 64-row halves (the
+//                next phase's first stages before the barriers);
+//   warp 14      TMA producer of the term rows: a box per four tokens of the column tile;
+//   warps 6..13  scale feeders, two groups in turn: the rows' linear scale bytes to shared memory by
+//                cp.async ahead of time, then to the stage's TMEM columns in the MMA's layout (one
+//                group takes 750 cycles for that);
+//   warp 1       MMA issuer; accumulators alternate between two TMEM buffers, so that a tile's
+//                epilogue overlaps the next tile's MMAs;
+//   warps 2..5   epilogue. Gate/up: a tile is 64 gate rows and the same 64 up rows; they meet in
+//                shared memory and silu(gate) * up, in fp32, is split into terms or (NVFP4)
+//                goes to the workspace. Down: the weighted
+//                sums of every column tile are added to [T][128] sums in shared memory, which go to y
+//                or, split by split, to the workspace.
+// A stage's bytes and scales complete one barrier, and the MMAs that have read them another.
+// Bound by HBM: a k-tile's 16 KB take 370 ns of an SM's share, its four MMAs of N = 64 about 70 ns; a
+// role must therefore take fewer than 700 cycles a k-tile, which is why each is a warp of its own with
+// few instructions a step. Waits are bounded; after one that gave up the roles run on without waiting
+// and the status word says so.
+template <class F>
+__global__ void __launch_bounds__(kThreads, 1)
+    moe_experts_kernel(const __grid_constant__ CUtensorMap tmUp,
+                       const __grid_constant__ CUtensorMap tmDown,
+                       const __grid_constant__ CUtensorMap tmX,
+                       const __grid_constant__ CUtensorMap tmH, const MoeGemm p)
+{
+    constexpr bool NV = !F::kMx;
     constexpr int SB = 4 * F::kAtoms;          // scale bytes of a row and k-tile
     constexpr int kSfRows = 2 * 128 * SB;      // weights' and terms' rows of one k-tile
     constexpr uint32_t kAccCols = 128, kSfCol = 2 * kAccCols, kSlotCols = 32;
@@ -636,17 +729,26 @@ __global__ void __launch_bounds__(kThreads, 1)
     __shared__ __align__(8) uint64_t full_bar[kMaxStages], empty_bar[kMaxStages];
     __shared__ __align__(8) uint64_t acc_full[2], acc_empty[2], drain_bar;
     __shared__ uint32_t tmem_slot;
+    __shared__ int s_counts[2];
+    __shared__ uint32_t s_max[kMoeMaxTokens];
+    __shared__ MoeStart s_start;
     const int tid = threadIdx.x, lane = tid & 31;
     // the same in every lane, and known to be: the roles' loops then run on uniform registers
     const int warp = __shfl_sync(0xFFFFFFFFu, tid >> 5, 0);
-    if ((smem_u32(smem) & 1023u) != 0) { // the same for every CTA
+    const bool misaligned = (smem_u32(smem) & 1023u) != 0; // the same for every CTA
+    if (misaligned) {
         if (tid == 0)
             atomicExch(p.status, (int)NVFP4_ERR_CUDA);
         return;
     }
-    const int stage_bytes = 16384 + p.b_rows * 128;
+    const int stage_bytes = p.stage_bytes;
     uint8_t *sf_ring = smem + p.stages * stage_bytes;
     float *s_out = reinterpret_cast<float *>(sf_ring + 2 * kSfRing * kSfRows);
+    MoeLists l;
+    l.wt = s_out + (p.T > kCols ? p.T : kCols) * 128;
+    l.units = reinterpret_cast<uint32_t *>(l.wt + p.T * p.k);
+    l.tok = reinterpret_cast<uint8_t *>(l.units + p.T * p.k);
+    l.counts = s_counts;
     if (tid == 0) {
         for (int s = 0; s < p.stages; ++s) {
             mbar_init(&full_bar[s], 2 + 4); // the producers, a feeder group's warps
@@ -659,6 +761,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         mbar_init(&drain_bar, 1);
         fence_barrier_init();
     }
+    if (tid == 32 * 14) {
+        tma_prefetch_desc(&tmUp);
+        tma_prefetch_desc(&tmX);
+        tma_prefetch_desc(&tmDown);
+        tma_prefetch_desc(&tmH);
+    }
     if (warp == 1) {
         tmem_alloc(&tmem_slot, 512);
         tmem_relinquish();
@@ -667,388 +775,445 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = tmem_slot;
-    pdl_launch_dependents();
-    pdl_wait(); // the lists, the terms
-    // the lists to shared memory: [rows] weights, [column tiles], [rows] tokens
-    const int n_units = __ldg(p.sh.counts), n_rows = __ldg(p.sh.counts + 1);
-    float *s_wt = s_out + (DOWN ? p.T : kCols) * 128;
-    uint32_t *s_units = reinterpret_cast<uint32_t *>(s_wt + p.n_slots);
-    uint8_t *s_tok = reinterpret_cast<uint8_t *>(s_units + p.n_slots);
-    for (int i = tid; i < n_rows; i += kThreads) {
-        s_wt[i] = __ldg(p.sh.wt + i);
-        s_tok[i] = __ldg(p.sh.tok + i);
-    }
-    for (int i = tid; i < n_units; i += kThreads)
-        s_units[i] = __ldg(p.sh.units + i);
-    __syncthreads();
+    pdl_wait(); // the ids, the activations
 
     bool dead = false; // a wait gave up: run on without waiting
-    auto wait = [&](uint64_t *bar, uint32_t parity) {
-        if (!dead && !mbar_wait(bar, parity, kWaitLimit)) {
-            dead = true;
-            atomicExch(p.status, (int)NVFP4_ERR_TIMEOUT);
-        }
+    auto give_up = [&]() {
+        dead = true;
+        atomicExch(p.status, (int)NVFP4_ERR_TIMEOUT);
     };
-    int stage = 0;
-    uint32_t phase = 0;
+    auto wait = [&](uint64_t *bar, uint32_t parity) {
+        if (!dead && !mbar_wait(bar, parity, kWaitLimit))
+            give_up();
+    };
+    // Every CTA's writes so far are visible to every CTA, to its TMA loads too. Warp 0 has weights on
+    // their way meanwhile, which its fences would wait for; it has written nothing and reads nothing
+    // that others write.
+    auto grid_sync = [&]() {
+        if (warp != 0)
+            asm volatile("fence.proxy.async;" ::: "memory");
+        __syncthreads();
+        if (tid == 32 && !grid_barrier_sync(p.barrier, (int)gridDim.x, (int)blockIdx.x, kBarrierLimit))
+            give_up();
+        __syncthreads();
+        if (warp != 0)
+            asm volatile("fence.proxy.async;" ::: "memory");
+    };
+
+    build_lists(l, p.ids, p.weights, p.T, p.k, p.E, smem);
+    if (tid == 32) { // (the counts are there since the lists' last barrier)
+        MoeStart st;
+        st.up_kt = (int)((p.H + 255) >> 8);
+        st.down_kt = (int)((p.F + 255) >> 8);
+        st.up_tiles = (int)((p.F + kUpRows - 1) / kUpRows);
+        const uint32_t n = (uint32_t)s_counts[0] * (uint32_t)st.up_tiles, g = gridDim.x;
+        const uint32_t q = n / g, r = n % g, b = blockIdx.x; // the first r CTAs have one more
+        const uint32_t i = b * q + min(b, r);
+        st.runs = (int)(q + (b < r ? 1u : 0u));
+        st.u = (int)(i / (uint32_t)st.up_tiles);
+        st.tile = (int)(i % (uint32_t)st.up_tiles);
+        const uint32_t m = (uint32_t)s_counts[0] * (uint32_t)st.down_kt;
+        st.q = m / (uint32_t)p.splits;
+        st.r = m % (uint32_t)p.splits;
+        s_start = st;
+    }
+    fence_proxy_async_smem(); // the lists' temporaries lay where TMA writes next
+    __syncthreads();
+    const int n_rows = s_counts[1];
+
+    // ---- the roles' state, kept across the phases -----------------------------------------------
+    int stage = 0, buf = 0;
+    uint32_t phase = 0, aphase = 0;
     auto next_stage = [&]() {
         if (++stage == p.stages) {
             stage = 0;
             phase ^= 1;
         }
     };
-    MoeWalk<DOWN> walk(p, s_units, n_units);
-    MoeGroup gr;
-    if (warp == 0) {
-        // ------------------------------- the weights' TMA producer ------------------
-        if (lane == 0) {
-            int issued = 0;
-            while (walk.next(gr)) {
-                const int y0 = (int)gr.ra0, y1 = (int)gr.ra1;
-                for (int kt = gr.k0; kt < gr.k1; ++kt) {
-                    uint8_t *a = smem + stage * stage_bytes;
-                    uint64_t *bar = &full_bar[stage];
-                    wait(&empty_bar[stage], phase ^ 1);
-                    mbar_arrive_expect_tx(bar, 16384u);
-                    tma_load_2d(a, &tmA, bar, kt * 128, y0);
-                    tma_load_2d(a + 8192, &tmA, bar, kt * 128, y1);
-                    ++issued;
-                    next_stage();
-                }
-            }
-            // every copy issued has landed before the CTA may exit
-            const int last = issued < p.stages ? issued : p.stages;
-            for (int i = 0; i < last; ++i) {
-                if (--stage < 0) {
-                    stage = p.stages - 1;
-                    phase ^= 1;
-                }
-                wait(&full_bar[stage], phase);
-            }
-        }
-        __syncwarp();
-    } else if (warp == 14) {
-        // ------------------------------- the term rows' TMA producer ----------------
-        const bool one_box = DOWN || p.dense; // else a box of eight rows per token
-        while (walk.next(gr)) {
-            const int ncol = one_box ? 1 : gr.unit.ncol;
-            const uint32_t bytes = one_box ? (uint32_t)p.b_rows * 128u : (uint32_t)ncol * 1024u;
-            int row = 0;
-            if (DOWN)
-                row = gr.unit.row0 * kTerms;
-            else if (!one_box && lane < ncol)
-                row = (int)s_tok[gr.unit.row0 + lane] * kTerms;
-            for (int kt = gr.k0; kt < gr.k1; ++kt) {
+    const int group = (warp - 6) >> 2; // a feeder's: takes every other k-tile
+    int rslot = 0, turn = group;
+    uint8_t *my_ring = sf_ring + (group & 1) * kSfRing * kSfRows;
+    const int feed_row = (tid - 192) & 127; // a feeder thread's row
+    const uint32_t ring_row = smem_u32(my_ring) + feed_row * SB;
+
+    // The weights' tiles of a phase's k-tiles `skip` .. `count` - 1 (warp 0's lane 0).
+    auto load_weights = [&](auto down, int skip, int count) -> int {
+        constexpr bool DOWN = decltype(down)::value;
+        MoeWalk<DOWN> walk(p, l.units, s_start);
+        MoeGroup gr;
+        int n = 0;
+        const CUtensorMap *tm = DOWN ? &tmDown : &tmUp;
+        while (n < count && walk.next(gr)) {
+            const int y0 = (int)gr.ra0, y1 = (int)gr.ra1;
+            for (int kt = gr.k0; kt < gr.k1 && n < count; ++kt, ++n) {
+                if (n < skip)
+                    continue;
+                uint8_t *a = smem + stage * stage_bytes;
                 uint64_t *bar = &full_bar[stage];
                 wait(&empty_bar[stage], phase ^ 1);
-                if (lane == 0)
-                    mbar_arrive_expect_tx(bar, bytes);
-                if (lane < ncol)
-                    tma_load_2d(smem + stage * stage_bytes + 16384 + lane * 1024, &tmB, bar, kt * 128,
-                                row);
-                __syncwarp();
+                if (dead)
+                    return n;
+                mbar_arrive_expect_tx(bar, 16384u);
+                tma_load_2d(a, tm, bar, kt * 128, y0);
+                tma_load_2d(a + 8192, tm, bar, kt * 128, y1);
                 next_stage();
             }
         }
-    } else if (warp >= 6) {
-        // ------------------------------- scale feeders ------------------------------
-        const int group = (warp - 6) >> 2; // takes every other k-tile
-        const int q = warp & 3;            // lane quarter of TMEM
-        const int r = tid - 192 - 128 * group; // this thread's row
-        const int srow = (int)((DOWN ? p.F : p.H) / F::kBlock);
-        const int64_t pitch = DOWN ? p.sh.h_pitch : p.sh.x_pitch;
-        const uint8_t *bs = DOWN ? p.sh.h_scales : p.sh.x_scales;
-        const bool even = srow % SB == 0; // every piece of a row is whole and aligned
-        uint8_t *my_ring = sf_ring + group * kSfRing * kSfRows;
-        const uint32_t ring = smem_u32(my_ring) + r * SB;
-        MoeWalk<DOWN> ahead(p, s_units, n_units); // kSfAhead of its k-tiles before the stores
-        int akt = group, akend = 0, aslot = 0;    // (k-tiles count on into the next run)
-        bool more = true, a_on = false, b_on = false;
-        const uint8_t *asrc = p.a_scales, *bsrc = bs;
-        auto zero = [&](uint32_t dst) {
-#pragma unroll
-            for (int i = 0; i < SB; i += 4)
-                asm volatile("st.shared.u32 [%0], %1;" ::"r"(dst + i), "r"(0u) : "memory");
-        };
-        auto load = [&]() {
-            while (more && akt >= akend) {
-                MoeGroup ga;
-                more = ahead.next(ga);
-                if (!more)
-                    break;
-                akt += ga.k0 - akend;
-                akend = ga.k1;
-                if (akt >= akend)
-                    continue;
-                const int64_t row = r < 64 ? ga.ra0 + r : ga.ra1 + (r - 64);
-                a_on = row < p.a_rows;
-                asrc = p.a_scales + (a_on ? row * srow + (int64_t)akt * SB : 0);
-                const bool dense = !DOWN && p.dense;
-                const int c = r / kTerms; // this row's token of the stage
-                b_on = dense ? c < p.T : c < ga.unit.ncol;
-                if (b_on) {
-                    const int t = dense ? c
-                                  : DOWN ? ga.unit.row0 + c
-                                         : (int)s_tok[ga.unit.row0 + c];
-                    bsrc = bs + ((int64_t)t * kTerms + r % kTerms) * pitch + (int64_t)akt * SB;
-                }
-            }
-            if (more) {
-                const uint32_t dst = ring + aslot * kSfRows;
-                if (!a_on)
-                    zero(dst);
-                else if (even)
-                    cp_async<SB>(dst, asrc);
-                else
-                    fetch_scales_general<SB>(dst, asrc, min(SB, srow - akt * SB));
-                if (b_on)
-                    cp_async<SB>(dst + 128 * SB, bsrc);
-                else
-                    zero(dst + 128 * SB);
-                asrc += a_on ? 2 * SB : 0;
-                bsrc += 2 * SB;
-                akt += 2;
-                aslot = aslot + 1 == kSfRing ? 0 : aslot + 1;
-            }
-            asm volatile("cp.async.commit_group;" ::: "memory");
-        };
-#pragma unroll 1
-        for (int i = 0; i < kSfAhead; ++i)
-            load();
-        int rslot = 0, turn = group;
-        const uint32_t tbase = tmem + ((uint32_t)(q * 32) << 16) + kSfCol;
-        while (walk.next(gr)) {
-            for (int kt = gr.k0; kt < gr.k1; ++kt) {
-                if (turn++ & 1) {
-                    next_stage();
-                    continue;
-                }
-                asm volatile("cp.async.wait_group %0;" ::"n"(kSfAhead - 1) : "memory");
-                named_bar_sync(2 + group, 128); // the rows are here, and the last k-tile's have been read
-                load();
-                wait(&empty_bar[stage], phase ^ 1);
-                __syncwarp();
-                tc_fence_after();
-                const uint8_t *src = my_ring + rslot * kSfRows;
-                feed_rows<F>(src, tbase + stage * kSlotCols, lane);
-                feed_rows<F>(src + 128 * SB, tbase + stage * kSlotCols + 16, lane);
-                tmem_st_wait();
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0)
-                    mbar_arrive(&full_bar[stage]);
-                rslot = rslot + 1 == kSfRing ? 0 : rslot + 1;
-                next_stage();
-            }
-        }
-        asm volatile("cp.async.wait_group 0;" ::: "memory");
-    } else if (warp == 1) {
-        // ------------------------------- MMA issuer ---------------------------------
-        int buf = 0;
-        uint32_t aphase = 0;
-        const uint64_t desc0 = smem_desc(smem_u32(smem), 16, 1024, kLayoutSwizzle128B);
-        while (walk.next(gr)) {
-            if (gr.k0 == gr.k1)
-                continue;
-            const int ncol = !DOWN && p.dense ? p.T : gr.unit.ncol;
-            const uint32_t n = ncol <= 1 ? 8 : ncol <= 2 ? 16 : ncol <= 4 ? 32 : ncol <= 8 ? 64 : 128;
-            const uint32_t idesc = F::kIdesc | (1u << 7) | (1u << 10) | ((n >> 3) << 17) | (8u << 24);
-            const uint32_t acc = tmem + buf * kAccCols;
-            wait(&acc_empty[buf], aphase ^ 1);
-            uint32_t add = 0u;
-            for (int kt = gr.k0; kt < gr.k1; ++kt) {
-                wait(&full_bar[stage], phase);
-                __syncwarp();
-                tc_fence_after();
-                if (elect_one()) {
-                    const uint32_t tsf = tmem + kSfCol + stage * kSlotCols;
-                    const uint64_t adesc = desc0 + (uint64_t)((stage * stage_bytes) >> 4);
-                    const uint64_t bdesc = adesc + (16384u >> 4);
-#pragma unroll
-                    for (int kb = 0; kb < 4; ++kb)
-                        tc_mma_fp4<F>(acc, adesc + (uint64_t)(2 * kb), bdesc + (uint64_t)(2 * kb),
-                                      idesc | sf_id_bits<F>(kb), tsf + sf_atom<F>(kb) * 4,
-                                      tsf + 16 + sf_atom<F>(kb) * 4, kb > 0 ? 1u : add);
-                    tc_commit(&empty_bar[stage]);
-                }
-                add = 1u;
-                __syncwarp();
-                next_stage();
-            }
-            if (elect_one())
-                tc_commit(&acc_full[buf]);
+        return n;
+    };
+
+    // What a phase can request before the barrier ahead of it: the first stages' weights and their
+    // scales.
+    int ahead = 0;
+    auto start = [&](auto down) {
+        constexpr bool DOWN = decltype(down)::value;
+        if (warp == 0) {
+            if (lane == 0)
+                ahead = load_weights(down, 0, p.stages);
             __syncwarp();
-            buf ^= 1;
-            if (buf == 0)
-                aphase ^= 1;
+        } else if (warp >= 6 && warp < 14) {
+            named_bar_sync(3 + group, 128); // the ring's last rows have been read
+            ScaleRow<F, DOWN> row(p, l.units, s_start, feed_row, ring_row, turn & 1, rslot);
+#pragma unroll 1
+            for (int i = 0; i < kSfAhead; ++i)
+                row.load(true, false);
         }
-        // every MMA issued completes before TMEM is freed (one lane issued them all)
-        if (elect_one())
-            tc_commit(&drain_bar);
-        wait(&drain_bar, 0);
-        __syncwarp();
-    } else {
-        // ------------------------------- epilogue (warps 2..5) ----------------------
-        const int q = warp & 3, r = q * 32 + lane; // this thread's accumulator row
-        const int et = tid - 64;
-        int buf = 0;
-        uint32_t aphase = 0;
-        if constexpr (DOWN) {
-            for (int i = et; i < p.T * 128; i += 128)
-                s_out[i] = 0.0f; // [T][128]
-            named_bar_sync(1, 128);
-        }
-        while (walk.next(gr)) {
-            const int ncol = gr.unit.ncol;
-            if (gr.k0 < gr.k1) {
-                wait(&acc_full[buf], aphase);
-                __syncwarp();
-                tc_fence_after();
-                const uint32_t trow = tmem + ((uint32_t)(q * 32) << 16) + buf * kAccCols;
-                const float gs = F::kMx ? 1.0f : __ldg(p.gs + gr.unit.expert);
-                for (int c0 = 0; c0 < ncol; c0 += 4) { // four tokens' columns at a time
-                    uint32_t v[4][8];
-                    int tok[4];
-#pragma unroll
-                    for (int c = 0; c < 4; ++c) {
-                        const int cc = min(c0 + c, ncol - 1);
-                        tok[c] = (int)s_tok[gr.unit.row0 + cc];
-                        tmem_ld_32x32b_x8(trow + (!DOWN && p.dense ? tok[c] : cc) * kTerms, v[c]);
-                    }
-                    tmem_ld_wait();
-#pragma unroll
-                    for (int c = 0; c < 4; ++c) {
-                        if (c0 + c >= ncol)
-                            break;
-                        float s = 0.0f; // the smallest terms first
-#pragma unroll
-                        for (int j = kTerms - 1; j >= 0; --j)
-                            s += __uint_as_float(v[c][j]);
-                        const int row = gr.unit.row0 + c0 + c;
-                        if constexpr (!F::kMx)
-                            s *= gs * __ldg(DOWN ? p.sh.h_factor + row : p.sh.x_factor + tok[c]);
-                        if constexpr (DOWN)
-                            s_out[tok[c] * 128 + r] = fmaf(s, s_wt[row], s_out[tok[c] * 128 + r]);
-                        else
-                            s_out[(c0 + c) * 128 + r] = s; // gate rows 0..63, up rows 64..127
-                    }
+    };
+
+    // One phase of products, after its start().
+    auto products = [&](auto down) {
+        constexpr bool DOWN = decltype(down)::value;
+        MoeWalk<DOWN> walk(p, l.units, s_start);
+        MoeGroup gr;
+        if (warp == 0) {
+            if (lane == 0)
+                load_weights(down, ahead, 0x7FFFFFFF);
+            __syncwarp();
+        } else if (warp == 14) {
+            // ------------------------------- the term rows' TMA producer --------------------
+            const CUtensorMap *tm = DOWN ? &tmH : &tmX;
+            while (walk.next(gr)) {
+                const int row = gr.unit.row0 * kTerms + lane * p.box;
+                const int n = (gr.unit.ncol * kTerms + p.box - 1) / p.box;
+                const uint32_t bytes = (uint32_t)(n * p.box * 128);
+                for (int kt = gr.k0; kt < gr.k1 && !dead; ++kt) {
+                    uint64_t *bar = &full_bar[stage];
+                    wait(&empty_bar[stage], phase ^ 1);
+                    dead = __any_sync(0xFFFFFFFFu, dead);
+                    if (dead)
+                        break;
+                    if (lane == 0)
+                        mbar_arrive_expect_tx(bar, bytes);
+                    __syncwarp();
+                    if (lane < n)
+                        tma_load_2d(smem + stage * stage_bytes + 16384 + lane * p.box * 128, tm, bar,
+                                    kt * 128, row);
+                    __syncwarp();
+                    next_stage();
                 }
-                tc_fence_before();
+            }
+        } else if (warp >= 6) {
+            // ------------------------------- scale feeders ----------------------------------
+            const int q = warp & 3;                // lane quarter of TMEM
+            ScaleRow<F, DOWN> row(p, l.units, s_start, feed_row, ring_row, turn & 1, rslot);
+#pragma unroll 1
+            for (int i = 0; i < kSfAhead; ++i)
+                row.load(false, true); // (the weights' are on their way since before the barrier)
+            const uint32_t tbase = tmem + ((uint32_t)(q * 32) << 16) + kSfCol;
+            while (walk.next(gr)) {
+                for (int kt = gr.k0; kt < gr.k1; ++kt) {
+                    if (turn++ & 1) {
+                        next_stage();
+                        continue;
+                    }
+                    asm volatile("cp.async.wait_group %0;" ::"n"(kSfAhead - 1) : "memory");
+                    named_bar_sync(3 + group, 128); // the rows are here, the last ones read
+                    row.load(true, true);
+                    wait(&empty_bar[stage], phase ^ 1);
+                    __syncwarp();
+                    tc_fence_after();
+                    const uint8_t *src = my_ring + rslot * kSfRows;
+                    feed_rows<F>(src, tbase + stage * kSlotCols, lane);
+                    feed_rows<F>(src + 128 * SB, tbase + stage * kSlotCols + 16, lane);
+                    tmem_st_wait();
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0)
+                        mbar_arrive(&full_bar[stage]);
+                    rslot = rslot + 1 == kSfRing ? 0 : rslot + 1;
+                    next_stage();
+                }
+            }
+            asm volatile("cp.async.wait_group 0;" ::: "memory");
+        } else if (warp == 1) {
+            // ------------------------------- MMA issuer -------------------------------------
+            const uint64_t desc0 = smem_desc(smem_u32(smem), 16, 1024, kLayoutSwizzle128B);
+            while (walk.next(gr)) {
+                if (gr.k0 == gr.k1)
+                    continue;
+                const uint32_t idesc = F::kIdesc | (1u << 7) | (1u << 10) |
+                                       ((uint32_t)gr.unit.ncol << 17) | (8u << 24); // N = 8 ncol
+                const uint32_t acc = tmem + buf * kAccCols;
+                wait(&acc_empty[buf], aphase ^ 1);
+                uint32_t add = 0u;
+                for (int kt = gr.k0; kt < gr.k1; ++kt) {
+                    wait(&full_bar[stage], phase);
+                    __syncwarp();
+                    tc_fence_after();
+                    if (elect_one()) {
+                        const uint32_t tsf = tmem + kSfCol + stage * kSlotCols;
+                        const uint64_t adesc = desc0 + (uint64_t)((stage * stage_bytes) >> 4);
+                        const uint64_t bdesc = adesc + (16384u >> 4);
+#pragma unroll
+                        for (int kb = 0; kb < 4; ++kb)
+                            tc_mma_fp4<F>(acc, adesc + (uint64_t)(2 * kb), bdesc + (uint64_t)(2 * kb),
+                                          idesc | sf_id_bits<F>(kb), tsf + sf_atom<F>(kb) * 4,
+                                          tsf + 16 + sf_atom<F>(kb) * 4, kb > 0 ? 1u : add);
+                        tc_commit(&empty_bar[stage]);
+                    }
+                    add = 1u;
+                    __syncwarp();
+                    next_stage();
+                }
+                if (elect_one())
+                    tc_commit(&acc_full[buf]);
                 __syncwarp();
-                if (lane == 0)
-                    mbar_arrive(&acc_empty[buf]);
                 buf ^= 1;
                 if (buf == 0)
                     aphase ^= 1;
             }
-            if constexpr (!DOWN) {
+        } else {
+            // ------------------------------- epilogue (warps 2..5) --------------------------
+            const int q = warp & 3, r = q * 32 + lane; // this thread's accumulator row
+            const int et = tid - 64;
+            [[maybe_unused]] const float *gsp = DOWN ? p.down_gs : p.up_gs;
+            if constexpr (DOWN) {
+                for (int i = et; i < p.T * 128; i += 128)
+                    s_out[i] = 0.0f; // [T][128]
                 named_bar_sync(1, 128);
-                const int f = et & 63;
-                if (gr.first + f < p.F)
-                    for (int c = et >> 6; c < ncol; c += 2) {
-                        const float ga = s_out[c * 128 + f], up = s_out[c * 128 + 64 + f];
-                        p.sh.h[(int64_t)(gr.unit.row0 + c) * p.F + gr.first + f] =
-                            ga / (1.0f + __expf(-ga)) * up;
+            }
+            while (walk.next(gr)) {
+                const int ncol = gr.unit.ncol;
+                if (gr.k0 < gr.k1) {
+                    wait(&acc_full[buf], aphase);
+                    __syncwarp();
+                    tc_fence_after();
+                    const uint32_t trow = tmem + ((uint32_t)(q * 32) << 16) + buf * kAccCols;
+                    [[maybe_unused]] const float gs = F::kMx ? 1.0f : __ldg(gsp + gr.unit.expert);
+                    for (int c0 = 0; c0 < ncol; c0 += 4) { // four tokens' columns at a time
+                        uint32_t v[4][8];
+#pragma unroll
+                        for (int c = 0; c < 4; ++c) {
+                            tmem_ld_32x32b_x8(trow + min(c0 + c, ncol - 1) * kTerms, v[c]);
+                        }
+                        tmem_ld_wait();
+#pragma unroll
+                        for (int c = 0; c < 4; ++c) {
+                            if (c0 + c >= ncol)
+                                break;
+                            float s = 0.0f; // the smallest terms first
+#pragma unroll
+                            for (int j = kTerms - 1; j >= 0; --j)
+                                s += __uint_as_float(v[c][j]);
+                            const int row = gr.unit.row0 + c0 + c;
+                            if constexpr (!F::kMx)
+                                s *= gs * row_factor(__ldcg((DOWN ? p.sh.h_max : p.sh.x_max) + row));
+                            if constexpr (DOWN) {
+                                float *sum = s_out + (int)l.tok[row] * 128 + r;
+                                *sum = fmaf(s, l.wt[row], *sum);
+                            } else
+                                s_out[(c0 + c) * 128 + r] = s; // gate rows 0..63, up rows 64..127
+                        }
                     }
-                named_bar_sync(1, 128);
-            } else if (gr.last) {
-                // this job's sums: y, or a split's share of it
-                const int64_t col = (int64_t)gr.first * kDownRows + r;
-                float *part = p.sh.partial +
-                              ((int64_t)gr.first * p.splits + gr.split) * p.T * kDownRows + r;
-                for (int t = 0; t < p.T; ++t) {
-                    const float s = s_out[t * 128 + r];
-                    s_out[t * 128 + r] = 0.0f;
-                    if (p.splits > 1)
-                        part[t * kDownRows] = s;
-                    else if (col < p.H)
-                        p.y[t * p.H + col] = __float2bfloat16_rn(s);
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0)
+                        mbar_arrive(&acc_empty[buf]);
+                    buf ^= 1;
+                    if (buf == 0)
+                        aphase ^= 1;
+                }
+                if constexpr (!DOWN) {
+                    named_bar_sync(1, 128);
+                    // eight columns of h a thread
+                    const int c = et >> 3, f = (et & 7) * 8;
+                    const int64_t col = gr.first + f, row = gr.unit.row0 + c;
+                    const bool on = c < ncol && col < p.F;
+                    float h[8] = {};
+                    if (on) {
+                        const float *ga = s_out + c * 128 + f;
+#pragma unroll
+                        for (int i = 0; i < 8; ++i)
+                            h[i] = ga[i] / (1.0f + __expf(-ga[i])) * ga[64 + i];
+                    }
+                    if constexpr (F::kMx) {
+                        uint8_t *sc = p.sh.h_scales + row * kTerms * p.sh.h_pitch;
+                        put_terms<false>(h, col, p.F, p.sh.h_codes + row * kTerms * (p.F >> 1), sc,
+                                         p.sh.h_pitch, c < ncol);
+                        if (c < ncol && gr.first + kUpRows >= p.F) // zero scales behind the row
+                            for (int64_t b = (gr.first + kUpRows) / 32 + (et & 7); b < p.sh.h_pitch;
+                                 b += 8)
+                                for (int j = 0; j < kTerms; ++j)
+                                    sc[j * p.sh.h_pitch + b] = 0;
+                    } else {
+                        uint32_t m = 0u;
+#pragma unroll
+                        for (int i = 0; i < 8; ++i)
+                            m = max(m, __float_as_uint(h[i]) & 0x7FFFFFFFu);
+#pragma unroll
+                        for (int o = 1; o < 8; o <<= 1)
+                            m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
+                        if (on) {
+                            float4 *dst = reinterpret_cast<float4 *>(p.sh.h + row * p.F + col);
+                            dst[0] = make_float4(h[0], h[1], h[2], h[3]);
+                            dst[1] = make_float4(h[4], h[5], h[6], h[7]);
+                        }
+                        if (c < ncol && (et & 7) == 0)
+                            atomicMax(p.sh.h_max + row, m); // in any order the same
+                    }
+                    named_bar_sync(1, 128);
+                } else if (gr.last) {
+                    // this job's sums, four columns a thread: y, or a split's share of it
+                    named_bar_sync(1, 128);
+                    const int64_t col = (int64_t)gr.first * kDownRows + (et & 31) * 4;
+                    float *part = p.sh.partial +
+                                  ((int64_t)gr.first * p.splits + gr.split) * p.T * kDownRows;
+                    for (int i = et; i < p.T * 32; i += 128) {
+                        float4 *sum = reinterpret_cast<float4 *>(s_out) + i;
+                        const float4 v = *sum;
+                        *sum = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                        if (p.splits > 1)
+                            reinterpret_cast<float4 *>(part)[i] = v;
+                        else if (col < p.H)
+                            put_y(p.y + (i >> 5) * p.H + col, v);
+                    }
+                    named_bar_sync(1, 128);
                 }
             }
         }
+    };
+
+    const std::integral_constant<bool, false> kUp;
+    const std::integral_constant<bool, true> kDown;
+    start(kUp);
+    {
+        const MoeChunks ch(n_rows, p.H);
+        if constexpr (NV) { // the largest values of the rows whose chunks this CTA has
+            for (int i = blockIdx.x * kThreads + tid; i < n_rows; i += gridDim.x * kThreads)
+                p.sh.h_max[i] = 0u;
+            if (tid < kMoeMaxTokens)
+                s_max[tid] = 0u;
+            __syncthreads();
+            const int64_t n = p.H >> 3;
+            if (ch.first < ch.last)
+                for (int64_t r = ch.first / ch.per; r <= (ch.last - 1) / ch.per; ++r) {
+                    const int t = l.tok[r];
+                    uint32_t m = 0u; // of both halves' magnitudes
+                    for (int64_t i = tid; i < n; i += kThreads) {
+                        const uint4 v = __ldg(p.x + t * n + i);
+                        m = max_u16x2(m, max_u16x2(max_u16x2(v.x & kAbs16x2, v.y & kAbs16x2),
+                                                   max_u16x2(v.z & kAbs16x2, v.w & kAbs16x2)));
+                    }
+                    m = __reduce_max_sync(0xFFFFFFFFu, max(m & 0xFFFFu, m >> 16));
+                    if (lane == 0)
+                        atomicMax(&s_max[t], m << 16);
+                }
+            __syncthreads();
+        }
+        write_terms<NV>(ch, p.H, p.sh.x_codes, p.sh.x_scales, p.sh.x_pitch, warp,
+                        [&](int64_t row, int64_t c0, float(&v)[8]) {
+                            const int t = l.tok[row];
+                            const uint4 u = __ldg(p.x + ((t * p.H + c0) >> 3));
+                            const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+                            const float f = NV ? row_inverse(s_max[t]) : 1.0f;
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) {
+                                v[2 * i] = __uint_as_float(w[i] << 16) * f;
+                                v[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u) * f;
+                            }
+                            if (NV && c0 == 0)
+                                p.sh.x_max[row] = s_max[t];
+                        });
+    }
+    grid_sync(); // the terms of x
+    products(kUp);
+    start(kDown);
+    grid_sync(); // h
+    if constexpr (NV) {
+        write_terms<NV>(MoeChunks(n_rows, p.F), p.F, p.sh.h_codes, p.sh.h_scales, p.sh.h_pitch,
+                        warp, [&](int64_t row, int64_t c0, float(&v)[8]) {
+                            const float4 *src =
+                                reinterpret_cast<const float4 *>(p.sh.h + row * p.F + c0);
+                            const float4 a = __ldcg(src), b = __ldcg(src + 1);
+                            const float f = row_inverse(__ldcg(p.sh.h_max + row));
+                            const float u[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+#pragma unroll
+                            for (int i = 0; i < 8; ++i)
+                                v[i] = u[i] * f;
+                        });
+        grid_sync(); // the terms of h
+    }
+    products(kDown);
+    if (p.splits > 1) {
+        grid_sync(); // the splits' sums
+        const int64_t n = (int64_t)p.T * (p.H >> 2);
+        for (int64_t i = (int64_t)blockIdx.x * kThreads + tid; i < n;
+             i += (int64_t)gridDim.x * kThreads) { // four columns a thread, in split order
+            const int64_t t = i / (p.H >> 2), c = (i % (p.H >> 2)) * 4;
+            const float *src =
+                p.sh.partial + ((c / kDownRows) * p.splits * p.T + t) * kDownRows + c % kDownRows;
+            float4 s = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll 4
+            for (int k = 0; k < p.splits; ++k) {
+                const float4 v =
+                    __ldcg(reinterpret_cast<const float4 *>(src + (int64_t)k * p.T * kDownRows));
+                s.x += v.x;
+                s.y += v.y;
+                s.z += v.z;
+                s.w += v.w;
+            }
+            put_y(p.y + t * p.H + c, s);
+        }
+    }
+    if (warp == 1) { // every MMA issued has completed before TMEM is freed
+        if (elect_one())
+            tc_commit(&drain_bar);
+        if (!mbar_wait(&drain_bar, 0, kWaitLimit))
+            give_up();
+        __syncwarp();
     }
     tc_fence_before();
-    __syncthreads();
+    if (__syncthreads_or(dead)) { // copies of a run that was given up land within microseconds
+        for (int i = 0; i < 1000; ++i)
+            __nanosleep(1000);
+    }
     if (warp == 1) {
         tc_fence_after();
         tmem_dealloc(tmem, 512);
     }
 }
 
-// y from the splits' sums, in split order; four columns a thread.
-__global__ void __launch_bounds__(256)
-    moe_sum_kernel(const float *partial, int splits, int T, int64_t H, __nv_bfloat16 *y)
-{
-    pdl_launch_dependents();
-    pdl_wait();
-    const int64_t n = (int64_t)T * (H >> 2);
-    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n; i += (int64_t)gridDim.x * 256) {
-        const int64_t t = i / (H >> 2), c = (i % (H >> 2)) * 4;
-        const float *src = partial + ((c / kDownRows) * splits * T + t) * kDownRows + c % kDownRows;
-        float4 s = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-#pragma unroll 4
-        for (int k = 0; k < splits; ++k) {
-            const float4 v = __ldcg(reinterpret_cast<const float4 *>(src + (int64_t)k * T * kDownRows));
-            s.x += v.x;
-            s.y += v.y;
-            s.z += v.z;
-            s.w += v.w;
-        }
-        const __nv_bfloat162 lo = __floats2bfloat162_rn(s.x, s.y), hi = __floats2bfloat162_rn(s.z, s.w);
-        *reinterpret_cast<uint2 *>(y + t * H + c) =
-            make_uint2(*reinterpret_cast<const uint32_t *>(&lo), *reinterpret_cast<const uint32_t *>(&hi));
-    }
-}
-
-template <typename K, typename... Args>
-cudaError_t launch_after(K kernel, int grid, int threads, size_t smem, cudaStream_t s, Args... args)
-{
-    cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3((unsigned)grid, 1, 1);
-    cfg.blockDim = dim3((unsigned)threads, 1, 1);
-    cfg.dynamicSmemBytes = smem;
-    cfg.stream = s;
-    cudaLaunchAttribute at[1];
-    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    at[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = at;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, kernel, args...);
-}
-
-template <class F, bool DOWN>
-cudaError_t launch_gemm(MoeGemm g, const CUtensorMap &tmA, const CUtensorMap &tmB, cudaStream_t s)
-{
-    static std::once_flag flags[64];
-    int dev = 0;
-    cudaGetDevice(&dev);
-    cudaError_t e = cudaSuccess;
-    std::call_once(flags[dev & 63], [&]() {
-        e = cudaFuncSetAttribute(moe_gemm_kernel<F, DOWN>,
-                                 cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxSmem);
-    });
-    if (e != cudaSuccess)
-        return e;
-    const int fixed = 2 * kSfRing * 2 * 128 * 4 * F::kAtoms + (DOWN ? g.T : kCols) * 128 * 4 +
-                      9 * g.n_slots;
-    const int stage = 16384 + g.b_rows * 128;
-    const int fit = (kMaxSmem - fixed) / stage;
-    g.stages = fit < kMaxStages ? fit : kMaxStages;
-    return launch_after(moe_gemm_kernel<F, DOWN>, num_sms(), kThreads,
-                        (size_t)g.stages * stage + fixed, s, tmA, tmB, g);
-}
-
-// CTAs per 128-row block of y.
+// Jobs per 128-row block of y: as many as give every SM one, or more where that would leave over 5%
+// more of the SMs idle (at most twice as many, four for many blocks: each costs T x 512 bytes of sums
+// written and read).
 int moe_splits(int64_t H)
 {
-    const int64_t s = num_sms() / ((H + kDownRows - 1) / kDownRows);
-    return (int)(s < 1 ? 1 : s);
+    const int64_t sms = num_sms(), blocks = (H + kDownRows - 1) / kDownRows;
+    const int64_t one = sms / blocks, lo = one < 1 ? 1 : one, hi = one < 2 ? 4 : 2 * one + 1;
+    auto used = [&](int64_t s) {
+        const int64_t jobs = blocks * s, rounds = (jobs + sms - 1) / sms;
+        return (double)jobs / (double)(rounds * sms);
+    };
+    int64_t best = lo;
+    for (int64_t s = lo + 1; s <= hi; ++s)
+        if (used(s) > used(best) + 0.05)
+            best = s;
+    return (int)best;
 }
 
 // The workspace: offsets of MoeShared's arrays for T tokens of k experts.
 struct MoeWs {
-    size_t x_codes, x_scales, x_factor, h, h_codes, h_scales, h_factor, units, counts, tok, wt,
-        partial, total;
+    size_t x_codes, x_scales, x_max, h, h_codes, h_scales, h_max, partial, total;
 };
 
 MoeWs moe_ws(int64_t T, int64_t k, int64_t F, int64_t H)
@@ -1061,66 +1226,65 @@ MoeWs moe_ws(int64_t T, int64_t k, int64_t F, int64_t H)
     };
     const size_t n = (size_t)T * (size_t)k, blocks = (size_t)((H + kDownRows - 1) / kDownRows);
     const int splits = moe_splits(H);
-    MoeWs w;
-    const size_t x_pitch = (size_t)(H / 16 + 15) / 16 * 16, h_pitch = (size_t)(F / 16 + 15) / 16 * 16;
-    w.x_codes = take((size_t)T * kTerms * (size_t)H / 2);
-    w.x_scales = take((size_t)T * kTerms * x_pitch);
-    w.x_factor = take((size_t)T * 4);
+    MoeWs w; // (the larger one, NVFP4's, for both formats)
+    w.x_codes = take(n * kTerms * (size_t)H / 2);
+    w.x_scales = take(n * kTerms * (size_t)((H + 255) / 256 * 16));
+    w.x_max = take(n * 4);
     w.h = take(n * (size_t)F * 4);
     w.h_codes = take(n * kTerms * (size_t)F / 2);
-    w.h_scales = take(n * kTerms * h_pitch);
-    w.h_factor = take(n * 4);
-    w.units = take(n * 4);
-    w.counts = take(8);
-    w.tok = take(n);
-    w.wt = take(n * 4);
+    w.h_scales = take(n * kTerms * (size_t)((F + 255) / 256 * 16));
+    w.h_max = take(n * 4);
     w.partial = take(splits > 1 ? blocks * splits * (size_t)T * kDownRows * 4 : 0);
     w.total = at;
     return w;
 }
 
 template <class F>
-cudaError_t launch_experts(MoeGemm g, const uint2 *x, const int *ids,
-                           const float *weights, int k, int E, const uint8_t *up_codes,
-                           const uint8_t *up_scales, const float *up_gs, const uint8_t *down_codes,
-                           const uint8_t *down_scales, const float *down_gs, cudaStream_t s)
+cudaError_t launch_experts(MoeGemm g, const uint8_t *up_codes, const uint8_t *down_codes,
+                           cudaStream_t s)
 {
-    constexpr bool NV = !F::kMx;
-    // scale bytes of a term row: whole 16-byte pieces, so that every k-tile's lie inside
-    g.sh.x_pitch = (g.H / F::kBlock + 15) / 16 * 16;
-    g.sh.h_pitch = (g.F / F::kBlock + 15) / 16 * 16;
-    g.b_rows = (g.T < kCols ? g.T : kCols) * kTerms;
-    g.dense = g.T <= kCols;
+    // scale bytes of a term row: whole k-tiles
+    g.sh.x_pitch = (g.H + 255) / 256 * 4 * F::kAtoms;
+    g.sh.h_pitch = (g.F + 255) / 256 * 4 * F::kAtoms;
+    const int cols = g.T < kCols ? g.T : kCols, per = cols < 4 ? cols : 4; // tokens: a stage, a box
+    g.box = per * kTerms;
+    g.stage_bytes = 16384 + (cols + per - 1) / per * g.box * 128;
     CUtensorMap up, down, xt, ht;
-    const int64_t n = (int64_t)g.T * k;
-    if (!make_fp4_codes_map(&up, up_codes, (int64_t)E * 2 * g.F, g.H, 64) ||
-        !make_fp4_codes_map(&down, down_codes, (int64_t)E * g.H, g.F, 64) ||
-        !make_fp4_codes_map(&xt, g.sh.x_codes, (int64_t)g.T * kTerms, g.H,
-                            g.dense ? g.b_rows : kTerms) ||
-        !make_fp4_codes_map(&ht, g.sh.h_codes, n * kTerms, g.F, g.b_rows))
+    const int64_t n = (int64_t)g.T * g.k;
+    if (!make_fp4_codes_map(&up, up_codes, (int64_t)g.E * 2 * g.F, g.H, 64) ||
+        !make_fp4_codes_map(&down, down_codes, (int64_t)g.E * g.H, g.F, 64) ||
+        !make_fp4_codes_map(&xt, g.sh.x_codes, n * kTerms, g.H, g.box) ||
+        !make_fp4_codes_map(&ht, g.sh.h_codes, n * kTerms, g.F, g.box))
         return cudaErrorInvalidValue;
-    cudaError_t e = launch_after(moe_prepare_kernel<NV>, g.T + 1, kPrepThreads,
-                                 lists_smem(g.T, k, E), s, g.sh, x, ids, weights, g.T, k, E,
-                                 g.H);
+    static std::once_flag flags[64];
+    int dev = 0;
+    cudaGetDevice(&dev);
+    cudaError_t e = cudaSuccess;
+    std::call_once(flags[dev & 63], [&]() {
+        e = cudaFuncSetAttribute(moe_experts_kernel<F>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 kMaxSmem);
+    });
     if (e != cudaSuccess)
         return e;
-    MoeGemm u = g, d = g;
-    u.a_scales = up_scales;
-    u.a_rows = (int64_t)E * 2 * g.F;
-    u.gs = up_gs;
-    d.a_scales = down_scales;
-    d.a_rows = (int64_t)E * g.H;
-    d.gs = down_gs;
-    if ((e = launch_gemm<F, false>(u, up, xt, s)) != cudaSuccess)
-        return e;
-    if ((e = launch_after(moe_terms_kernel<NV>, (int)n, kTermThreads, (size_t)0, s, g.sh, g.F)) !=
-        cudaSuccess)
-        return e;
-    if ((e = launch_gemm<F, true>(d, down, ht, s)) != cudaSuccess || g.splits == 1)
-        return e;
-    const int64_t need = ((int64_t)g.T * (g.H / 4) + 255) / 256, cap = (int64_t)num_sms() * 4;
-    return launch_after(moe_sum_kernel, (int)(need < cap ? need : cap), 256, (size_t)0, s,
-                        g.sh.partial, g.splits, g.T, g.H, g.y);
+    const int fixed = 2 * kSfRing * 2 * 128 * 4 * F::kAtoms + (g.T > kCols ? g.T : kCols) * 128 * 4 +
+                      9 * g.T * g.k;
+    const int fit = (kMaxSmem - fixed) / g.stage_bytes;
+    g.stages = fit < kMaxStages ? fit : kMaxStages;
+    // (build_lists' temporaries, 12 E + 6 T k <= 18 KB, lie in the first two stages)
+    const size_t smem = (size_t)g.stages * g.stage_bytes + fixed;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3((unsigned)num_sms(), 1, 1);
+    cfg.blockDim = dim3(kThreads, 1, 1);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cudaLaunchAttribute at[2];
+    at[0].id = cudaLaunchAttributeCooperative; // the CTAs wait for one another: all resident
+    at[0].val.cooperative = 1;
+    at[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[1].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 2;
+    return cudaLaunchKernelEx(&cfg, moe_experts_kernel<F>, up, down, xt, ht, g);
 }
 
 } // namespace
@@ -1157,27 +1321,31 @@ cudaError_t launch_moe_experts(const void *x, int64_t T, int64_t H, int64_t F, i
     const MoeWs w = moe_ws(T, k, F, H);
     uint8_t *b = reinterpret_cast<uint8_t *>(ws);
     auto f32 = [&](size_t o) { return reinterpret_cast<float *>(b + o); };
-    auto i32 = [&](size_t o) { return reinterpret_cast<int *>(b + o); };
     MoeGemm g{};
-    g.sh = MoeShared{b + w.x_codes, b + w.x_scales, f32(w.x_factor), 0,
-                     f32(w.h), b + w.h_codes, b + w.h_scales, f32(w.h_factor), 0,
-                     reinterpret_cast<uint32_t *>(b + w.units), i32(w.counts), b + w.tok, f32(w.wt),
-                     f32(w.partial)};
+    auto u32 = [&](size_t o) { return reinterpret_cast<uint32_t *>(b + o); };
+    g.sh = MoeShared{b + w.x_codes, b + w.x_scales, b + w.h_codes, b + w.h_scales, 0, 0,
+                     u32(w.x_max), u32(w.h_max), f32(w.h), f32(w.partial)};
+    g.x = reinterpret_cast<const uint4 *>(x);
+    g.ids = ids;
+    g.weights = weights;
     g.T = (int)T;
-    g.n_slots = (int)T * k;
+    g.k = k;
+    g.E = E;
     g.H = H;
     g.F = F;
+    g.up_scales = up_scales;
+    g.down_scales = down_scales;
+    g.up_gs = up_gs;
+    g.down_gs = down_gs;
     g.splits = moe_splits(H);
     g.blocks = (int)((H + kDownRows - 1) / kDownRows);
     g.y = reinterpret_cast<__nv_bfloat16 *>(y);
+    g.barrier = grid_barrier_for(s);
     g.status = device_status_ptr();
-    if (!g.status)
+    if (!g.status || !g.barrier)
         return cudaErrorInvalidValue;
-    const uint2 *xv = reinterpret_cast<const uint2 *>(x);
-    return mx ? launch_experts<FmtMxfp4>(g, xv, ids, weights, k, E, up_codes, up_scales, up_gs,
-                                         down_codes, down_scales, down_gs, s)
-              : launch_experts<FmtNvfp4>(g, xv, ids, weights, k, E, up_codes, up_scales, up_gs,
-                                         down_codes, down_scales, down_gs, s);
+    return mx ? launch_experts<FmtMxfp4>(g, up_codes, down_codes, s)
+              : launch_experts<FmtNvfp4>(g, up_codes, down_codes, s);
 }
 
 } // namespace nvfp4
