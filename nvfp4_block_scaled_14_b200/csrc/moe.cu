@@ -8,7 +8,7 @@
 // The weights go to the FP4 tensor cores as they are stored. Those multiply FP4 by FP4 only, so an
 // activation is split into eight FP4 terms, each the FP4 form of what the ones before leave
 // (put_terms), and the eight products are added: the weights lose nothing and the activations at
-// most 2^-22 (MXFP4) of their block's largest value, or 2^-19 (NVFP4) of their row's, while the terms' columns cost the otherwise idle MMA
+// most 2^-22 (MXFP4) of their block's largest value, or 2^-18 (NVFP4) of their row's, while the terms' columns cost the otherwise idle MMA
 // 8 of its up to 256 columns a token. (Decoding the weights to f16 on the CUDA cores for mma.sync
 // took 40-54 issue slots per 16 x 32 codes, as long as HBM takes to deliver them, and ran at a
 // quarter of it: 64 tokens, 64 experts of 2048 x 1024, top 8: 135 us.)
@@ -213,8 +213,8 @@ __device__ __forceinline__ MoeUnit unpack_unit(uint32_t u)
 
 // What the CTAs of one call share in the workspace. Rows: the (expert, token) pairs, in expert order.
 struct MoeShared {
-    uint8_t *x_codes, *x_scales; // terms of the rows' x: [rows * 8][H / 2], [rows * 8][x_pitch]
-    uint8_t *h_codes, *h_scales; // terms of the rows' h = silu(gate) * up
+    uint8_t *x_codes, *h_codes;  // terms of the rows' x and h = silu(gate) * up: [rows * 8][cols / 2]
+    uint8_t *x_scales, *h_scales; // (MXFP4) first terms' scales: [rows][pitch]
     int64_t x_pitch, h_pitch;
     uint32_t *x_max, *h_max;     // [rows] (NVFP4): bits of the row's largest magnitude
     float *h;                    // [rows][F] (NVFP4)
@@ -315,79 +315,99 @@ __device__ __forceinline__ void build_lists(const MoeLists &l, const int *ids, c
     }
 }
 
-// Activations as kTerms FP4 terms. A block's first term has the power of two as its scale with which
-// its largest value lies in 3..6 steps: a rounding leaves at most one step (between 4 and 6), a 1/5 of
-// that value. The second term's step is a quarter of that, each further one's an eighth of the one
-// before: what is left is at most 4 of these steps, and half a step after the rounding. So the scales
-// follow from the first one, a term costs a lane no exchange, every subtraction is exact, and the
-// eight terms leave at most 2^-21 of the first step, 2^-22 of the block's largest value. Steps end at
-// the format's smallest scale: MXFP4 (E8M0, blocks of 32) 2^-127. NVFP4 (E4M3, blocks of 16) has
-// 2^8 .. 2^-9 only, of the row divided by a power of two that brings its largest value to 512..1024:
-// 2^-10 is left, 2^-19 of that value. (The first version gave each term the best scale for what the
-// terms before left; a block's maximum for every term took the 512 x 1024 values of 64 tokens 10 us.)
-// A NaN or an infinity: the block's first scale is NaN (MXFP4), or the row's factor is (NVFP4), and
-// so the row's results are.
+// Activations as kTerms FP4 terms: the digits of a fixed-point number to base 8. -4 .. 3 are E2M1
+// values, and with digits of that range the 3-bit fields of X + 4 (1 + 8 + 64 + ...) are the digits
+// plus 4; one byte permute looks up four codes. Term j's scale is 8^-j times the first one's.
+//   MXFP4: X = v / 2^(E - 21), E the exponent of the block's largest value (32 values): eight digits,
+//     scales 2^E .. 2^(E - 21). Off by at most half a unit: 2^-22 of the block's largest value (and
+//     2^-128, where E < -106 is taken as -106). Only 2^E is stored.
+//   NVFP4: E4M3 holds 2^8 .. 2^-9 only, so the row is divided by a power of two that brings its
+//     largest value to 2^8 .. 2^9, X = v * 2^9, six digits of scales 2^8 .. 2^-7 and one of -2 .. 1 of
+//     scale 2^-9: the same scales for every block, none stored. Off by at most 2^-10: 2^-18 of the
+//     row's largest value.
+// The subtraction form (each term the E2M1 rounding of what the ones before leave, at a scale of its
+// own maximum) cost 16 conversions a quarter of the rate of other instructions a value: the 512 x 1024
+// values of 64 tokens took 10 us, this takes 2.
+// A NaN or an infinity: the block's scale is NaN (MXFP4), or the row's factor is (NVFP4), and so the
+// row's results are.
 //
 // v: values c0 .. c0 + 7 of a row of `cols`, lane i's c0 being lane 0's + 8 i in aligned groups of four
-// lanes; zeros behind the row's end. codes, scales: the row's first term. Called by whole warps.
+// lanes; zeros behind the row's end. codes: the row's first term; scales: the row's. Called by whole
+// warps.
 template <bool NV>
 __device__ __forceinline__ void put_terms(const float (&v)[8], int64_t c0, int64_t cols,
                                           uint8_t *codes, uint8_t *scales, int64_t pitch, bool live)
 {
-    constexpr int kBlock = NV ? 16 : 32;
-    constexpr uint32_t kLow = NV ? 127 - 9 : 0;
-    uint32_t m = 0u;
-#pragma unroll
-    for (int i = 0; i < 8; ++i)
-        m = max(m, __float_as_uint(v[i]) & 0x7FFFFFFFu);
-    m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 1));
-    if constexpr (!NV)
-        m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 2));
-    uint32_t b = mx_scale_byte(m, true); // of the power of two, also where E4M3 holds it
-    const bool bad = b == kMxNan;
-    if constexpr (NV)
-        b = min(max(b, kLow), 127u + 8u);
-    const float inv = mx_inverse(b);
-    float2 r[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-        r[i] = bad ? make_float2(0.0f, 0.0f)
-                   : __fmul2_rn(make_float2(v[2 * i], v[2 * i + 1]), make_float2(inv, inv));
+    constexpr float kMagic = 12582912.0f; // 1.5 * 2^23: the sum's low bits are the rounded integer
+    constexpr uint32_t kDigits = 044444444u;
     const bool on = live && c0 < cols;
-    const bool put_scale = live && c0 % kBlock == 0 && c0 / kBlock < pitch;
-    codes += c0 >> 1;
-    scales += c0 / kBlock;
+    float unit = 512.0f;
+    bool bad = false;
+    if constexpr (!NV) {
+        uint32_t m = 0u;
 #pragma unroll
-    for (int j = 0; j < kTerms; ++j) {
-        if (j > 0) {
-            const uint32_t d = min(j == 1 ? 2u : 3u, b - kLow);
-            b -= d;
-            const float up = __uint_as_float((127u + d) << 23);
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-                r[i] = __fmul2_rn(r[i], make_float2(up, up));
-        }
-        const float y[8] = {r[0].x, r[0].y, r[1].x, r[1].y, r[2].x, r[2].y, r[3].x, r[3].y};
-        const uint32_t w = cvt_e2m1x8(y);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const float2 q = e2m1x2_to_f32x2(w >> (8 * i) & 0xFFu);
-            r[i] = __fadd2_rn(r[i], make_float2(-q.x, -q.y));
-        }
-        if (on)
-            *reinterpret_cast<uint32_t *>(codes + j * (cols >> 1)) = w;
-        if (put_scale) {
-            const uint32_t e4 = b >= 127u - 6u ? (b - 120u) << 3 : 1u << (b - kLow);
-            scales[j * pitch] = on ? (uint8_t)(NV ? e4 : b) : (uint8_t)0;
-        }
+        for (int i = 0; i < 8; ++i)
+            m = max(m, __float_as_uint(v[i]) & 0x7FFFFFFFu);
+        m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 1));
+        m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 2));
+        const uint32_t b = max(m >> 23, 21u); // E8M0 byte; 255: NaN
+        bad = b == 255u;
+        unit = __uint_as_float((275u - (bad ? 254u : b)) << 23); // 2^(21 - E)
+        if (live && c0 % 32 == 0 && c0 / 32 < pitch)
+            scales[c0 / 32] = on ? (uint8_t)b : (uint8_t)21;
     }
+    uint32_t p[2][4]; // two values' codes, a byte a digit: digits 7..4, 3..0
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        uint32_t u = __float_as_uint(fmaf(v[i], unit, kMagic)) - __float_as_uint(kMagic);
+        if constexpr (NV) { // the digit of scale 2^-9 is digit 6, digit 7 is 0
+            u += 4u * 01111110u / 2u + 2u;
+            u = (u & ~3u) << 4 | ((u & 3u) + 2u) << 3 | 4u;
+        } else {
+            u = bad ? kDigits : u + kDigits;
+        }
+        u += (u & 0xFFF000u) * 15u; // 3-bit fields to nibbles: halves to 16 bits,
+        u += (u & 0x0FC00FC0u) * 3u; // six bits to bytes,
+        u += u & 0x38383838u;
+        const uint32_t lo = i & 1 ? 0xA0C0D0E0u : 0x0A0C0D0Eu, hi = i & 1 ? 0x50402000u : 0x05040200u;
+        const uint32_t a = __byte_perm(lo, hi, u), b = __byte_perm(lo, hi, u >> 16);
+        p[0][i >> 1] = i & 1 ? p[0][i >> 1] | a : a;
+        p[1][i >> 1] = i & 1 ? p[1][i >> 1] | b : b;
+    }
+    codes += c0 >> 1;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) { // four bytes of four words -> four words of one digit each
+        const uint32_t t0 = __byte_perm(p[h][0], p[h][1], 0x5140);
+        const uint32_t t1 = __byte_perm(p[h][2], p[h][3], 0x5140);
+        const uint32_t t2 = __byte_perm(p[h][0], p[h][1], 0x7362);
+        const uint32_t t3 = __byte_perm(p[h][2], p[h][3], 0x7362);
+        const uint32_t w[4] = {__byte_perm(t0, t1, 0x5410), __byte_perm(t0, t1, 0x7632),
+                               __byte_perm(t2, t3, 0x5410), __byte_perm(t2, t3, 0x7632)};
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            if (on)
+                *reinterpret_cast<uint32_t *>(codes + (7 - 4 * h - i) * (cols >> 1)) = w[i];
+    }
+}
+
+// Scale bytes of term j of eight, four of a word of the first term's (MXFP4), or all of NVFP4's.
+__device__ __forceinline__ uint32_t mx_term_scales(uint32_t first, int j)
+{
+    return first - 0x03030303u * (uint32_t)j;
+}
+
+__device__ __forceinline__ uint32_t nv_term_scales(int j)
+{
+    // E4M3 of 2^8, 2^5, 2^2, 2^-1, 2^-4, 2^-7, 2^-9, 2^-9
+    const uint64_t all = 0x0101041830486078ull;
+    return (uint32_t)(all >> (8 * j) & 0xFFu) * 0x01010101u;
 }
 
 // The power of two that a row with the largest magnitude m (bits) is divided by: kept where both it
 // and its inverse are normal.
 __device__ __forceinline__ uint32_t row_exponent(uint32_t m)
 {
-    return (uint32_t)min(max((int)(m >> 23) - 9, 1), 253);
+    return (uint32_t)min(max((int)(m >> 23) - 8, 1), 253);
 }
 
 __device__ __forceinline__ float row_inverse(uint32_t m)
@@ -425,8 +445,8 @@ __device__ __forceinline__ void write_terms(const MoeChunks &ch, int64_t cols, u
         float v[8] = {};
         if (c0 < cols)
             load(row, c0, v);
-        put_terms<NV>(v, c0, cols, codes + row * kTerms * (cols >> 1), scales + row * kTerms * pitch,
-                      pitch, true);
+        put_terms<NV>(v, c0, cols, codes + row * kTerms * (cols >> 1), scales + row * pitch, pitch,
+                      true);
     }
 }
 
@@ -578,10 +598,11 @@ __device__ __noinline__ void fetch_scales_general(uint32_t dst, const uint8_t *s
     }
 }
 
-// 128 rows' scale bytes (SB a row at `sm`) -> the TMEM columns of F::kAtoms atoms, this warp's lane
-// quarter: lane r's word i of an atom is row r + 32 i's.
+// 128 rows' scale bytes (SB a row at `sm`; MXFP4: less `less`) -> the TMEM columns of F::kAtoms atoms,
+// this warp's lane quarter: lane r's word i of an atom is row r + 32 i's.
 template <class F>
-__device__ __forceinline__ void feed_rows(const uint8_t *sm, uint32_t tcol, int lane)
+__device__ __forceinline__ void feed_rows(const uint8_t *sm, uint32_t tcol, int lane,
+                                          uint32_t less = 0u)
 {
     constexpr int SB = 4 * F::kAtoms;
     uint32_t r[4 * F::kAtoms];
@@ -589,8 +610,8 @@ __device__ __forceinline__ void feed_rows(const uint8_t *sm, uint32_t tcol, int 
     for (int i = 0; i < 4; ++i) {
         if constexpr (F::kMx) {
             const uint2 v = *reinterpret_cast<const uint2 *>(sm + (lane + 32 * i) * SB);
-            r[i] = v.x;
-            r[4 + i] = v.y;
+            r[i] = v.x - less;
+            r[4 + i] = v.y - less;
         } else {
             const uint4 v = *reinterpret_cast<const uint4 *>(sm + (lane + 32 * i) * SB);
             r[i] = v.x;
@@ -648,7 +669,7 @@ template <class F, bool DOWN> struct ScaleRow {
             asrc = (DOWN ? p.down_scales : p.up_scales) + (a_on ? row * srow + (int64_t)kt * SB : 0);
             b_on = r / kTerms < g.unit.ncol; // a token of the column tile
             bsrc = (DOWN ? p.sh.h_scales : p.sh.x_scales) +
-                   ((int64_t)g.unit.row0 * kTerms + r) * (DOWN ? p.sh.h_pitch : p.sh.x_pitch) +
+                   (int64_t)(g.unit.row0 + r / kTerms) * (DOWN ? p.sh.h_pitch : p.sh.x_pitch) +
                    (int64_t)kt * SB;
         }
         if (more) {
@@ -661,12 +682,8 @@ template <class F, bool DOWN> struct ScaleRow {
                 else
                     fetch_scales_general<SB>(dst, asrc, min(SB, srow - kt * SB));
             }
-            if (terms) {
-                if (b_on)
-                    cp_async<SB>(dst + 128 * SB, bsrc);
-                else
-                    zero(dst + 128 * SB);
-            }
+            if (F::kMx && terms && b_on) // (the MMA reads no other columns)
+                cp_async<SB>(dst + 128 * SB, bsrc);
             asrc += a_on ? 2 * SB : 0;
             bsrc += 2 * SB;
             kt += 2;
@@ -775,7 +792,21 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = tmem_slot;
+    if constexpr (NV)
+        if (warp >= 6 && warp < 10) { // the terms' scales, the same in every stage
+            uint32_t w[16];
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
+                w[i] = nv_term_scales(lane & 7);
+            for (int i = 0; i < p.stages; ++i)
+                tmem_st_32x32b_x16(tmem + ((uint32_t)((warp & 3) * 32) << 16) + kSfCol +
+                                       i * kSlotCols + 16, w);
+            tmem_st_wait();
+            tc_fence_before(); // (the products are several barriers away)
+        }
     pdl_wait(); // the ids, the activations
+    for (int64_t i = blockIdx.x * kThreads + tid; i < p.T * (p.H >> 6); i += gridDim.x * kThreads)
+        asm volatile("prefetch.global.L2 [%0];" ::"l"(p.x + i * 8)); // while the lists are built
 
     bool dead = false; // a wait gave up: run on without waiting
     auto give_up = [&]() {
@@ -934,7 +965,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                     tc_fence_after();
                     const uint8_t *src = my_ring + rslot * kSfRows;
                     feed_rows<F>(src, tbase + stage * kSlotCols, lane);
-                    feed_rows<F>(src + 128 * SB, tbase + stage * kSlotCols + 16, lane);
+                    if constexpr (F::kMx) // row r: term r % 8
+                        feed_rows<F>(src + 128 * SB, tbase + stage * kSlotCols + 16, lane,
+                                     mx_term_scales(0u, 0) - mx_term_scales(0u, lane & 7));
                     tmem_st_wait();
                     tc_fence_before();
                     __syncwarp();
@@ -1047,14 +1080,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                             h[i] = ga[i] / (1.0f + __expf(-ga[i])) * ga[64 + i];
                     }
                     if constexpr (F::kMx) {
-                        uint8_t *sc = p.sh.h_scales + row * kTerms * p.sh.h_pitch;
+                        uint8_t *sc = p.sh.h_scales + row * p.sh.h_pitch;
                         put_terms<false>(h, col, p.F, p.sh.h_codes + row * kTerms * (p.F >> 1), sc,
                                          p.sh.h_pitch, c < ncol);
-                        if (c < ncol && gr.first + kUpRows >= p.F) // zero scales behind the row
+                        if (c < ncol && gr.first + kUpRows >= p.F) // finite scales behind the row
                             for (int64_t b = (gr.first + kUpRows) / 32 + (et & 7); b < p.sh.h_pitch;
                                  b += 8)
-                                for (int j = 0; j < kTerms; ++j)
-                                    sc[j * p.sh.h_pitch + b] = 0;
+                                sc[b] = 21;
                     } else {
                         uint32_t m = 0u;
 #pragma unroll
@@ -1226,13 +1258,13 @@ MoeWs moe_ws(int64_t T, int64_t k, int64_t F, int64_t H)
     };
     const size_t n = (size_t)T * (size_t)k, blocks = (size_t)((H + kDownRows - 1) / kDownRows);
     const int splits = moe_splits(H);
-    MoeWs w; // (the larger one, NVFP4's, for both formats)
+    MoeWs w; // (what either format needs)
     w.x_codes = take(n * kTerms * (size_t)H / 2);
-    w.x_scales = take(n * kTerms * (size_t)((H + 255) / 256 * 16));
+    w.x_scales = take(n * (size_t)((H + 255) / 256 * 8));
     w.x_max = take(n * 4);
     w.h = take(n * (size_t)F * 4);
     w.h_codes = take(n * kTerms * (size_t)F / 2);
-    w.h_scales = take(n * kTerms * (size_t)((F + 255) / 256 * 16));
+    w.h_scales = take(n * (size_t)((F + 255) / 256 * 8));
     w.h_max = take(n * 4);
     w.partial = take(splits > 1 ? blocks * splits * (size_t)T * kDownRows * 4 : 0);
     w.total = at;
@@ -1243,9 +1275,9 @@ template <class F>
 cudaError_t launch_experts(MoeGemm g, const uint8_t *up_codes, const uint8_t *down_codes,
                            cudaStream_t s)
 {
-    // scale bytes of a term row: whole k-tiles
-    g.sh.x_pitch = (g.H + 255) / 256 * 4 * F::kAtoms;
-    g.sh.h_pitch = (g.F + 255) / 256 * 4 * F::kAtoms;
+    // scale bytes of a row (MXFP4): whole k-tiles
+    g.sh.x_pitch = (g.H + 255) / 256 * 8;
+    g.sh.h_pitch = (g.F + 255) / 256 * 8;
     const int cols = g.T < kCols ? g.T : kCols, per = cols < 4 ? cols : 4; // tokens: a stage, a box
     g.box = per * kTerms;
     g.stage_bytes = 16384 + (cols + per - 1) / per * g.box * 128;
@@ -1323,7 +1355,7 @@ cudaError_t launch_moe_experts(const void *x, int64_t T, int64_t H, int64_t F, i
     auto f32 = [&](size_t o) { return reinterpret_cast<float *>(b + o); };
     MoeGemm g{};
     auto u32 = [&](size_t o) { return reinterpret_cast<uint32_t *>(b + o); };
-    g.sh = MoeShared{b + w.x_codes, b + w.x_scales, b + w.h_codes, b + w.h_scales, 0, 0,
+    g.sh = MoeShared{b + w.x_codes, b + w.h_codes, b + w.x_scales, b + w.h_scales, 0, 0,
                      u32(w.x_max), u32(w.h_max), f32(w.h), f32(w.partial)};
     g.x = reinterpret_cast<const uint4 *>(x);
     g.ids = ids;

@@ -210,20 +210,19 @@ def blocks_max(v):
 
 
 def terms_error(v):
-    """Bound on what eight FP4 terms leave of v. A term's rounding leaves at most 1/5 of its block's
-    largest remainder (MXFP4, scales rounded up to a power of two: codes between 4 and 6 are 1 off at
-    most, of a largest value of 5 or more there) or 0.18 (NVFP4: 1 of 6 / (1 + 1/16), or saturation
-    at 6 of 6.4): 5^-8 < 2^-18 of the block's largest value. NVFP4 scales end at 2^-10 (half the
-    smallest), a remainder of 6 * 2^-10, with the row's largest value at 1344 or more: 2^-17 of it."""
-    return 2.0 ** -18 * blocks_max(v) + 2.0 ** -17 * v.abs().max()
+    """Bound on what eight FP4 terms leave of v: half a unit of a fixed-point number. MXFP4: of units
+    2^-21 of the power of two at or below the block's largest value. NVFP4: units of 2^-9, the row's
+    largest value being divided to 2^8 or more: 2^-18 of it."""
+    return 2.0 ** -22 * blocks_max(v) + 2.0 ** -18 * v.abs().max()
 
 
 def experts_reference(x, ids, p, up, down):
     """y and a bound on |y_kernel - y| before y's own rounding, in float64.
 
     a = Wg x: inputs off by terms_error, and fp32 sums over the terms, whose sizes add up to at most
-    |x| + blocks_max(x) / 2 a value (a term exceeds what is left by at most its rounding: twice
-    1/5 + 1/25 + ...): K/16 additions, each off by at most 2^-22 of the sum of the sizes. silu has
+    4 |x| a value (digits of -4 .. 3 to base 8: with a leading digit d >= 1 in size the ones behind
+    add up to at most 4/7 of its unit, so |x| >= 3/7 and the sizes are at most d + 4/7; the ratio is
+    largest at d = 1, 11/3): K/16 additions, each off by at most 2^-22 of the sum of the sizes. silu has
     slope at most 1.1 and |silu(a)| <= |a|; expf, the division and the products add 2^-20 relative.
     h is kept in fp32 and enters the down product the same way; the weighted sum over rows and
     splits adds 2^-18 relative of its terms' sizes."""
@@ -235,7 +234,7 @@ def experts_reference(x, ids, p, up, down):
 
     def product_error(w, v, dv):
         w = w.abs()
-        sizes = w @ (v.abs() + dv + 0.5 * blocks_max(v.abs() + dv))
+        sizes = w @ (4 * (v.abs() + dv))
         return w @ (dv + terms_error(v.abs() + dv)) + v.numel() / 16 * 2.0 ** -22 * sizes
     for t in range(T):
         for s in range(ids.shape[1]):
