@@ -2280,9 +2280,19 @@ LinearPlan plan_linear(int64_t M, int64_t N, int64_t K, unsigned flags)
     return p;
 }
 
-bool make_fp4_codes_map(CUtensorMap *m, const void *base, int64_t rows, int64_t K, int box_rows)
+bool make_fp4_codes_map(CUtensorMap *m, const void *base, int64_t mats, int64_t rows, int64_t K,
+                        int box_mats, int box_rows)
 {
-    return encode_fn() && make_codes_map(m, base, rows, K, box_rows);
+    if (!encode_fn())
+        return false;
+    cuuint64_t dims[3] = {(cuuint64_t)(K / 2), (cuuint64_t)rows, (cuuint64_t)mats};
+    cuuint64_t strides[2] = {(cuuint64_t)(K / 2), (cuuint64_t)(rows * (K / 2))};
+    cuuint32_t box[3] = {128u, (cuuint32_t)box_rows, (cuuint32_t)box_mats};
+    cuuint32_t estr[3] = {1u, 1u, 1u};
+    return encode_fn()(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void *>(base), dims,
+                       strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                       CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                       CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 cudaError_t launch_linear_nvfp4_out(const uint8_t *a_codes, const uint8_t *a_sf, const float *a_gs,

@@ -479,9 +479,8 @@ struct MoeGemm {
 // A run of k-tiles of one tile, whose sums stay in one accumulator.
 struct MoeGroup {
     MoeUnit unit;
-    int64_t ra0, ra1; // rows of the stacked weights of the tile's two 64-row halves
     int k0, k1;       // k-tiles (none: an empty job)
-    int first;        // gate/up: first column of h; down: the block of y
+    int first;        // the tile's first column of h (gate/up) or of y (down)
     int split;
     bool last;        // down: the job's last run
 };
@@ -526,8 +525,6 @@ template <bool DOWN> struct MoeWalk {
             --rest;
             g.unit = unpack_unit(units[u]);
             g.first = tile * kUpRows;
-            g.ra0 = (int64_t)g.unit.expert * 2 * p.F + g.first;
-            g.ra1 = g.ra0 + p.F;
             g.k0 = 0;
             g.k1 = st.up_kt;
             if (++tile == st.up_tiles) {
@@ -545,8 +542,8 @@ template <bool DOWN> struct MoeWalk {
                 u = (int)(a / (uint32_t)st.down_kt);
                 tile = (int)(a % (uint32_t)st.down_kt);
             }
-            g.first = (int)((uint32_t)job / (uint32_t)p.splits);
-            g.split = job - g.first * p.splits;
+            g.split = (int)((uint32_t)job % (uint32_t)p.splits);
+            g.first = (int)((uint32_t)job / (uint32_t)p.splits) * kDownRows;
             if (rest == 0) {
                 g.unit = MoeUnit{0, 0, 0};
                 g.k0 = g.k1 = 0;
@@ -554,8 +551,6 @@ template <bool DOWN> struct MoeWalk {
                 return true;
             }
             g.unit = unpack_unit(units[u]);
-            g.ra0 = (int64_t)g.unit.expert * p.H + (int64_t)g.first * kDownRows;
-            g.ra1 = g.ra0 + 64;
             g.k0 = tile;
             g.k1 = min(tile + rest, st.down_kt);
             rest -= g.k1 - g.k0;
@@ -664,8 +659,11 @@ template <class F, bool DOWN> struct ScaleRow {
             kend = g.k1;
             if (kt >= kend)
                 continue;
-            const int64_t row = r < 64 ? g.ra0 + r : g.ra1 + (r - 64);
-            a_on = row < (int64_t)p.E * (DOWN ? p.H : 2 * p.F);
+            // rows of the stacked weights; gate/up: 64 of gate, the same of up
+            const int at = g.first + (DOWN ? r : r & 63);
+            const int64_t row = DOWN ? g.unit.expert * p.H + at
+                                     : (2 * g.unit.expert + (r >> 6)) * p.F + at;
+            a_on = at < (DOWN ? p.H : p.F);
             asrc = (DOWN ? p.down_scales : p.up_scales) + (a_on ? row * srow + (int64_t)kt * SB : 0);
             b_on = r / kTerms < g.unit.ncol; // a token of the column tile
             bsrc = (DOWN ? p.sh.h_scales : p.sh.x_scales) +
@@ -867,7 +865,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int feed_row = (tid - 192) & 127; // a feeder thread's row
     const uint32_t ring_row = smem_u32(my_ring) + feed_row * SB;
 
-    // The weights' tiles of a phase's k-tiles `skip` .. `count` - 1 (warp 0's lane 0).
+    // The weights' tiles of a phase's k-tiles `skip` .. `count` - 1 (warp 0).
     auto load_weights = [&](auto down, int skip, int count) -> int {
         constexpr bool DOWN = decltype(down)::value;
         MoeWalk<DOWN> walk(p, l.units, s_start);
@@ -875,18 +873,19 @@ __global__ void __launch_bounds__(kThreads, 1)
         int n = 0;
         const CUtensorMap *tm = DOWN ? &tmDown : &tmUp;
         while (n < count && walk.next(gr)) {
-            const int y0 = (int)gr.ra0, y1 = (int)gr.ra1;
+            const int z = DOWN ? gr.unit.expert : 2 * gr.unit.expert; // gate's rows, then up's
             for (int kt = gr.k0; kt < gr.k1 && n < count; ++kt, ++n) {
                 if (n < skip)
                     continue;
-                uint8_t *a = smem + stage * stage_bytes;
                 uint64_t *bar = &full_bar[stage];
                 wait(&empty_bar[stage], phase ^ 1);
+                dead = __any_sync(0xFFFFFFFFu, dead);
                 if (dead)
                     return n;
-                mbar_arrive_expect_tx(bar, 16384u);
-                tma_load_2d(a, tm, bar, kt * 128, y0);
-                tma_load_2d(a + 8192, tm, bar, kt * 128, y1);
+                if (elect_one()) {
+                    mbar_arrive_expect_tx(bar, 16384u);
+                    tma_load_3d(smem + stage * stage_bytes, tm, bar, kt * 128, gr.first, z);
+                }
                 next_stage();
             }
         }
@@ -899,9 +898,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     auto start = [&](auto down) {
         constexpr bool DOWN = decltype(down)::value;
         if (warp == 0) {
-            if (lane == 0)
-                ahead = load_weights(down, 0, p.stages);
-            __syncwarp();
+            ahead = load_weights(down, 0, p.stages);
         } else if (warp >= 6 && warp < 14) {
             named_bar_sync(3 + group, 128); // the ring's last rows have been read
             ScaleRow<F, DOWN> row(p, l.units, s_start, feed_row, ring_row, turn & 1, rslot);
@@ -917,9 +914,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         MoeWalk<DOWN> walk(p, l.units, s_start);
         MoeGroup gr;
         if (warp == 0) {
-            if (lane == 0)
-                load_weights(down, ahead, 0x7FFFFFFF);
-            __syncwarp();
+            load_weights(down, ahead, 0x7FFFFFFF);
         } else if (warp == 14) {
             // ------------------------------- the term rows' TMA producer --------------------
             const CUtensorMap *tm = DOWN ? &tmH : &tmX;
@@ -937,8 +932,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                         mbar_arrive_expect_tx(bar, bytes);
                     __syncwarp();
                     if (lane < n)
-                        tma_load_2d(smem + stage * stage_bytes + 16384 + lane * p.box * 128, tm, bar,
-                                    kt * 128, row);
+                        tma_load_3d(smem + stage * stage_bytes + 16384 + lane * p.box * 128, tm, bar,
+                                    kt * 128, row, 0);
                     __syncwarp();
                     next_stage();
                 }
@@ -991,7 +986,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                 uint32_t add = 0u;
                 for (int kt = gr.k0; kt < gr.k1; ++kt) {
                     wait(&full_bar[stage], phase);
-                    __syncwarp();
                     tc_fence_after();
                     if (elect_one()) {
                         const uint32_t tsf = tmem + kSfCol + stage * kSlotCols;
@@ -1005,7 +999,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                         tc_commit(&empty_bar[stage]);
                     }
                     add = 1u;
-                    __syncwarp();
                     next_stage();
                 }
                 if (elect_one())
@@ -1107,9 +1100,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                 } else if (gr.last) {
                     // this job's sums, four columns a thread: y, or a split's share of it
                     named_bar_sync(1, 128);
-                    const int64_t col = (int64_t)gr.first * kDownRows + (et & 31) * 4;
+                    const int64_t col = gr.first + (et & 31) * 4;
                     float *part = p.sh.partial +
-                                  ((int64_t)gr.first * p.splits + gr.split) * p.T * kDownRows;
+                                  ((int64_t)(gr.first / kDownRows) * p.splits + gr.split) * p.T * kDownRows;
                     for (int i = et; i < p.T * 32; i += 128) {
                         float4 *sum = reinterpret_cast<float4 *>(s_out) + i;
                         const float4 v = *sum;
@@ -1283,10 +1276,10 @@ cudaError_t launch_experts(MoeGemm g, const uint8_t *up_codes, const uint8_t *do
     g.stage_bytes = 16384 + (cols + per - 1) / per * g.box * 128;
     CUtensorMap up, down, xt, ht;
     const int64_t n = (int64_t)g.T * g.k;
-    if (!make_fp4_codes_map(&up, up_codes, (int64_t)g.E * 2 * g.F, g.H, 64) ||
-        !make_fp4_codes_map(&down, down_codes, (int64_t)g.E * g.H, g.F, 64) ||
-        !make_fp4_codes_map(&xt, g.sh.x_codes, n * kTerms, g.H, g.box) ||
-        !make_fp4_codes_map(&ht, g.sh.h_codes, n * kTerms, g.F, g.box))
+    if (!make_fp4_codes_map(&up, up_codes, 2 * g.E, g.F, g.H, 2, kUpRows) ||
+        !make_fp4_codes_map(&down, down_codes, g.E, g.H, g.F, 1, kDownRows) ||
+        !make_fp4_codes_map(&xt, g.sh.x_codes, 1, n * kTerms, g.H, 1, g.box) ||
+        !make_fp4_codes_map(&ht, g.sh.h_codes, 1, n * kTerms, g.F, 1, g.box))
         return cudaErrorInvalidValue;
     static std::once_flag flags[64];
     int dev = 0;

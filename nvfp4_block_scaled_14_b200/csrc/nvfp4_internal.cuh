@@ -113,8 +113,10 @@ cudaError_t launch_linear_xq(const LinearPlan &pl, const void *x, int x_bf16,
                              int64_t M, int64_t N, int64_t K, int out_bf16, void *y,
                              float *x_gs_out, unsigned flags, cudaStream_t s, nvfp4_status *st);
 
-// Packed FP4 codes [rows x K/2] bytes as a TMA map, box 128 bytes x box_rows, 128B swizzle.
-bool make_fp4_codes_map(CUtensorMap *m, const void *base, int64_t rows, int64_t K, int box_rows);
+// Packed FP4 codes of `mats` matrices [rows x K/2] bytes behind one another as a TMA map, box 128
+// bytes x box_rows x box_mats, 128B swizzle.
+bool make_fp4_codes_map(CUtensorMap *m, const void *base, int64_t mats, int64_t rows, int64_t K,
+                        int box_mats, int box_rows);
 
 // The same linear layer on MXFP4 operands (plan_linear plans both formats).
 cudaError_t launch_linear_mx(const LinearPlan &p, const uint8_t *a_codes, const uint8_t *a_sf,
