@@ -243,14 +243,15 @@ __device__ __forceinline__ void build_lists(const MoeLists &l, const int *ids, c
     int16_t *s_ids = reinterpret_cast<int16_t *>(s_w + T * k);
     const int n = T * k, tid = threadIdx.x;
     auto count = [&](int e) { return __popc(mask[2 * e]) + __popc(mask[2 * e + 1]); };
-    int id = tid < n ? __ldg(ids + tid) : -1; // on its way while the masks are cleared
+    const int id = tid < n ? __ldg(ids + tid) : -1; // on their way while the masks are cleared
+    const float wt = tid < n ? __ldg(weights + tid) : 0.0f;
     for (int i = tid; i < 2 * E; i += kThreads)
         mask[i] = 0u;
     __syncthreads();
     for (int i = tid; i < n; i += kThreads) {
         const int e = i == tid ? id : __ldg(ids + i), t = i / k;
         const bool on = e >= 0 && e < E;
-        s_w[i] = __ldg(weights + i);
+        s_w[i] = i == tid ? wt : __ldg(weights + i);
         s_ids[i] = on ? (int16_t)e : (int16_t)-1;
         if (on)
             atomicOr(&mask[2 * e + (t >> 5)], 1u << (t & 31));
@@ -422,13 +423,14 @@ __device__ __forceinline__ float row_factor(uint32_t m)
 
 // A CTA's share of the rows' 256-value chunks, one warp each.
 struct MoeChunks {
-    int64_t per, first, last;
+    uint32_t per, first, last; // (32 bits: the terms would pass the memory before)
 
-    __device__ __forceinline__ MoeChunks(int64_t rows, int64_t cols)
+    __device__ __forceinline__ MoeChunks(int rows, int64_t cols)
     {
-        per = (cols + 255) >> 8;
-        first = rows * per * blockIdx.x / gridDim.x;
-        last = rows * per * (blockIdx.x + 1) / gridDim.x;
+        per = (uint32_t)((cols + 255) >> 8);
+        const uint32_t n = (uint32_t)rows * per, q = n / gridDim.x, r = n % gridDim.x;
+        first = blockIdx.x * q + min(blockIdx.x, r);
+        last = first + q + (blockIdx.x < r ? 1u : 0u);
     }
 };
 
@@ -440,8 +442,8 @@ __device__ __forceinline__ void write_terms(const MoeChunks &ch, int64_t cols, u
     const int lane = threadIdx.x & 31;
     if (warp == 0)
         return;
-    for (int64_t i = ch.first + warp - 1; i < ch.last; i += kThreads / 32 - 1) {
-        const int64_t row = i / ch.per, c0 = (i % ch.per) * 256 + lane * 8;
+    for (uint32_t i = ch.first + warp - 1; i < ch.last; i += kThreads / 32 - 1) {
+        const int64_t row = i / ch.per, c0 = (int64_t)(i - (uint32_t)row * ch.per) * 256 + lane * 8;
         float v[8] = {};
         if (c0 < cols)
             load(row, c0, v);
@@ -1131,7 +1133,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             __syncthreads();
             const int64_t n = p.H >> 3;
             if (ch.first < ch.last)
-                for (int64_t r = ch.first / ch.per; r <= (ch.last - 1) / ch.per; ++r) {
+                for (uint32_t r = ch.first / ch.per; r <= (ch.last - 1) / ch.per; ++r) {
                     const int t = l.tok[r];
                     uint32_t m = 0u; // of both halves' magnitudes
                     for (int64_t i = tid; i < n; i += kThreads) {
