@@ -192,7 +192,8 @@ __global__ void __cluster_dims__(kRouteCluster, 1, 1) __launch_bounds__(kRouteTh
 
 constexpr int kTerms = 8;  // FP4 terms of an activation: the rows of one swizzle atom
 constexpr int kCols = 16;  // tokens of a column tile: 128 MMA columns
-constexpr int kThreads = 480;
+constexpr int kFeeders = 2; // groups of four warps
+constexpr int kThreads = 32 * (7 + 4 * kFeeders);
 constexpr int kUpRows = 64, kDownRows = 128; // rows of F, of H, per tile
 
 // A column tile: up to kCols of the (expert, token) rows of one expert. Packed: 9 bits of expert, 11
@@ -624,9 +625,10 @@ __device__ __forceinline__ void feed_rows(const uint8_t *sm, uint32_t tcol, int 
 }
 
 // A scale feeder thread's row: its scale bytes of every other k-tile, from `first` on (k-tiles count on
-// from one run into the next), into a ring of kSfRing rows of 128 of weights and 128 of terms.
+// from one run into the next), into a ring of kSfRing slots of 128 rows of weights and (MXFP4) 128 of terms.
 template <class F, bool DOWN> struct ScaleRow {
     static constexpr int SB = 4 * F::kAtoms; // bytes of a row and k-tile
+    static constexpr int kSlot = (F::kMx ? 2 : 1) * 128 * SB;
     const MoeGemm &p;
     MoeWalk<DOWN> walk;
     uint32_t ring; // this row's slot 0
@@ -673,7 +675,7 @@ template <class F, bool DOWN> struct ScaleRow {
                    (int64_t)kt * SB;
         }
         if (more) {
-            const uint32_t dst = ring + slot * (2 * 128 * SB);
+            const uint32_t dst = ring + slot * kSlot;
             if (weights) {
                 if (!a_on)
                     zero(dst);
@@ -684,9 +686,9 @@ template <class F, bool DOWN> struct ScaleRow {
             }
             if (F::kMx && terms && b_on) // (the MMA reads no other columns)
                 cp_async<SB>(dst + 128 * SB, bsrc);
-            asrc += a_on ? 2 * SB : 0;
-            bsrc += 2 * SB;
-            kt += 2;
+            asrc += a_on ? kFeeders * SB : 0;
+            bsrc += kFeeders * SB;
+            kt += kFeeders;
             slot = slot + 1 == kSfRing ? 0 : slot + 1;
         }
         asm volatile("cp.async.commit_group;" ::: "memory");
@@ -740,7 +742,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 {
     constexpr bool NV = !F::kMx;
     constexpr int SB = 4 * F::kAtoms;          // scale bytes of a row and k-tile
-    constexpr int kSfRows = 2 * 128 * SB;      // weights' and terms' rows of one k-tile
+    constexpr int kSfRows = ScaleRow<F, false>::kSlot;
     constexpr uint32_t kAccCols = 128, kSfCol = 2 * kAccCols, kSlotCols = 32;
     extern __shared__ __align__(1024) uint8_t smem[];
     __shared__ __align__(8) uint64_t full_bar[kMaxStages], empty_bar[kMaxStages];
@@ -760,7 +762,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     const int stage_bytes = p.stage_bytes;
     uint8_t *sf_ring = smem + p.stages * stage_bytes;
-    float *s_out = reinterpret_cast<float *>(sf_ring + 2 * kSfRing * kSfRows);
+    float *s_out = reinterpret_cast<float *>(sf_ring + kFeeders * kSfRing * kSfRows);
     MoeLists l;
     l.wt = s_out + (p.T > kCols ? p.T : kCols) * 128;
     l.units = reinterpret_cast<uint32_t *>(l.wt + p.T * p.k);
@@ -778,7 +780,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         mbar_init(&drain_bar, 1);
         fence_barrier_init();
     }
-    if (tid == 32 * 14) {
+    if (tid == kThreads - 1) {
         tma_prefetch_desc(&tmUp);
         tma_prefetch_desc(&tmX);
         tma_prefetch_desc(&tmDown);
@@ -861,9 +863,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             phase ^= 1;
         }
     };
-    const int group = (warp - 6) >> 2; // a feeder's: takes every other k-tile
-    int rslot = 0, turn = group;
-    uint8_t *my_ring = sf_ring + (group & 1) * kSfRing * kSfRows;
+    const int group = warp >= 6 && warp < 6 + 4 * kFeeders ? (warp - 6) >> 2 : 0; // a feeder's
+    int rslot = 0, turn = group; // k-tiles until the group's next one
+    uint8_t *my_ring = sf_ring + group * kSfRing * kSfRows;
     const int feed_row = (tid - 192) & 127; // a feeder thread's row
     const uint32_t ring_row = smem_u32(my_ring) + feed_row * SB;
 
@@ -901,9 +903,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         constexpr bool DOWN = decltype(down)::value;
         if (warp == 0) {
             ahead = load_weights(down, 0, p.stages);
-        } else if (warp >= 6 && warp < 14) {
+        } else if (warp >= 6 && warp < 6 + 4 * kFeeders) {
             named_bar_sync(3 + group, 128); // the ring's last rows have been read
-            ScaleRow<F, DOWN> row(p, l.units, s_start, feed_row, ring_row, turn & 1, rslot);
+            ScaleRow<F, DOWN> row(p, l.units, s_start, feed_row, ring_row, turn, rslot);
 #pragma unroll 1
             for (int i = 0; i < kSfAhead; ++i)
                 row.load(true, false);
@@ -917,7 +919,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         MoeGroup gr;
         if (warp == 0) {
             load_weights(down, ahead, 0x7FFFFFFF);
-        } else if (warp == 14) {
+        } else if (warp == 6 + 4 * kFeeders) {
             // ------------------------------- the term rows' TMA producer --------------------
             const CUtensorMap *tm = DOWN ? &tmH : &tmX;
             while (walk.next(gr)) {
@@ -943,22 +945,23 @@ __global__ void __launch_bounds__(kThreads, 1)
         } else if (warp >= 6) {
             // ------------------------------- scale feeders ----------------------------------
             const int q = warp & 3;                // lane quarter of TMEM
-            ScaleRow<F, DOWN> row(p, l.units, s_start, feed_row, ring_row, turn & 1, rslot);
+            ScaleRow<F, DOWN> row(p, l.units, s_start, feed_row, ring_row, turn, rslot);
 #pragma unroll 1
             for (int i = 0; i < kSfAhead; ++i)
                 row.load(false, true); // (the weights' are on their way since before the barrier)
             const uint32_t tbase = tmem + ((uint32_t)(q * 32) << 16) + kSfCol;
             while (walk.next(gr)) {
                 for (int kt = gr.k0; kt < gr.k1; ++kt) {
-                    if (turn++ & 1) {
+                    if (turn > 0) {
+                        --turn;
                         next_stage();
                         continue;
                     }
+                    turn = kFeeders - 1;
                     asm volatile("cp.async.wait_group %0;" ::"n"(kSfAhead - 1) : "memory");
+                    if (q == 2) // one warp of the group polls, the others sleep at the barrier
+                        wait(&empty_bar[stage], phase ^ 1);
                     named_bar_sync(3 + group, 128); // the rows are here, the last ones read
-                    row.load(true, true);
-                    wait(&empty_bar[stage], phase ^ 1);
-                    __syncwarp();
                     tc_fence_after();
                     const uint8_t *src = my_ring + rslot * kSfRows;
                     feed_rows<F>(src, tbase + stage * kSlotCols, lane);
@@ -970,6 +973,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     __syncwarp();
                     if (lane == 0)
                         mbar_arrive(&full_bar[stage]);
+                    row.load(true, true);
                     rslot = rslot + 1 == kSfRing ? 0 : rslot + 1;
                     next_stage();
                 }
@@ -1023,8 +1027,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             while (walk.next(gr)) {
                 const int ncol = gr.unit.ncol;
                 if (gr.k0 < gr.k1) {
-                    wait(&acc_full[buf], aphase);
-                    __syncwarp();
+                    if (q == 2)
+                        wait(&acc_full[buf], aphase);
+                    named_bar_sync(1, 128);
                     tc_fence_after();
                     const uint32_t trow = tmem + ((uint32_t)(q * 32) << 16) + buf * kAccCols;
                     [[maybe_unused]] const float gs = F::kMx ? 1.0f : __ldg(gsp + gr.unit.expert);
@@ -1293,8 +1298,8 @@ cudaError_t launch_experts(MoeGemm g, const uint8_t *up_codes, const uint8_t *do
     });
     if (e != cudaSuccess)
         return e;
-    const int fixed = 2 * kSfRing * 2 * 128 * 4 * F::kAtoms + (g.T > kCols ? g.T : kCols) * 128 * 4 +
-                      9 * g.T * g.k;
+    const int fixed = kFeeders * kSfRing * ScaleRow<F, false>::kSlot +
+                      (g.T > kCols ? g.T : kCols) * 128 * 4 + 9 * g.T * g.k;
     const int fit = (kMaxSmem - fixed) / g.stage_bytes;
     g.stages = fit < kMaxStages ? fit : kMaxStages;
     // (build_lists' temporaries, 12 E + 6 T k <= 18 KB, lie in the first two stages)
