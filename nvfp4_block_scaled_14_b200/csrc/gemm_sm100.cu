@@ -840,6 +840,58 @@ __device__ __forceinline__ void stage_store_tile_halves(const GemmParams &p, con
     store(1);
 }
 
+// The same for fp32 output: four quarters of 64 columns, two boxes of 32 columns each, the next
+// quarter's TMEM loads in flight while one is staged.
+template <typename Release>
+__device__ __forceinline__ void stage_store_tile_quarters(const GemmParams &p,
+                                                          const CUtensorMap *tmY, uint8_t *stg,
+                                                          uint32_t trow, int r, float alpha,
+                                                          bool issuer, int64_t yrow, int64_t ycol,
+                                                          Release release)
+{
+    const uint32_t s = smem_u32(stg);
+    auto quarter = [&](const uint32_t (&v)[64], int h) {
+        if (h > 0) {
+            if (issuer)
+                bulk_wait_group_read0(); // the last quarter has left the staging tile
+            named_bar_sync(1, 128);
+        }
+#pragma unroll
+        for (int g = 0; g < 16; ++g) { // 16-byte pieces, 128B swizzle
+            const uint32_t at = s + (g >> 3) * (128 * 128) + r * 128 + (((g & 7) ^ (r & 7)) << 4);
+            sts128(at, __float_as_uint(__uint_as_float(v[4 * g]) * alpha),
+                   __float_as_uint(__uint_as_float(v[4 * g + 1]) * alpha),
+                   __float_as_uint(__uint_as_float(v[4 * g + 2]) * alpha),
+                   __float_as_uint(__uint_as_float(v[4 * g + 3]) * alpha));
+        }
+        fence_proxy_async_smem();
+        named_bar_sync(1, 128);
+        if (issuer) {
+#pragma unroll
+            for (int b = 0; b < 2; ++b) {
+                const int64_t col = ycol + (2 * h + b) * 32;
+                if (yrow < p.rows_a && col < p.rows_b)
+                    tma_store_2d(tmY, stg + b * (128 * 128), (int)col, (int)yrow);
+            }
+            bulk_commit_group();
+        }
+    };
+    uint32_t va[64], vb[64];
+    tmem_ld_64cols(trow, va);
+    tmem_ld_wait();
+    tmem_ld_64cols(trow + 64, vb);
+    quarter(va, 0);
+    tmem_ld_wait();
+    tmem_ld_64cols(trow + 128, va);
+    quarter(vb, 1);
+    tmem_ld_wait();
+    tmem_ld_64cols(trow + 192, vb);
+    quarter(va, 2);
+    tmem_ld_wait();
+    release();
+    quarter(vb, 3);
+}
+
 // Shared-memory and TMEM layout of the pair kernel. bf16 output: five operand stages and a 32 KB
 // bf16 staging tile (the output leaves in two halves), four scale slots; quantizing epilogue:
 // four stages and 64 KB of staging (fp32 columns 128-255 of each row), two scale slots and 128
@@ -893,7 +945,7 @@ __device__ __forceinline__ void tc_mma_bf16_pair(uint32_t d_tmem, uint64_t adesc
                  : "memory");
 }
 
-template <bool QOUT, bool LR, class F>
+template <bool QOUT, bool LR, class F, bool F32>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     nvfp4_gemm_pair_kernel(const __grid_constant__ CUtensorMap tmA,
                            const __grid_constant__ CUtensorMap tmB,
@@ -904,7 +956,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                            const __grid_constant__ CUtensorMap tmU, const GemmParams p)
 {
     using C = Pair<QOUT, F>;
-    static_assert(!F::kMx || (!QOUT && !LR), "MXFP4: plain bf16 output only");
+    static_assert(!F::kMx || (!QOUT && !LR), "MXFP4: plain bf16 or fp32 output only");
+    static_assert(!F32 || (!QOUT && !LR), "fp32: plain output only");
     extern __shared__ __align__(1024) uint8_t smem[];
     if ((smem_u32(smem) & 1023u) != 0) {
         if (threadIdx.x == 0)
@@ -1221,13 +1274,20 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             if (threadIdx.x == 64)
                 bulk_wait_group_read0(); // the previous tile's second half has left the staging
             named_bar_sync(1, 128);
-            stage_store_tile_halves(p, &tmY, smem + C::kOffStaging, trow, q * 32 + lane, alpha,
-                                    threadIdx.x == 64, ta * 256 + rank * 128, tb * 256, [&]() {
-                                        tc_fence_before();
-                                        __syncwarp();
-                                        if (lane == 0)
-                                            mbar_arrive_remote(leader_acc_empty); // read
-                                    });
+            auto release = [&]() {
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0)
+                    mbar_arrive_remote(leader_acc_empty); // this CTA's accumulator is read
+            };
+            if constexpr (F32)
+                stage_store_tile_quarters(p, &tmY, smem + C::kOffStaging, trow, q * 32 + lane,
+                                          alpha, threadIdx.x == 64, ta * 256 + rank * 128,
+                                          tb * 256, release);
+            else
+                stage_store_tile_halves(p, &tmY, smem + C::kOffStaging, trow, q * 32 + lane, alpha,
+                                        threadIdx.x == 64, ta * 256 + rank * 128, tb * 256,
+                                        release);
             acc_phase ^= 1;
         }
     }
@@ -1243,34 +1303,51 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     }
 }
 
-// Sum split-K partials in split order, scale by alpha, cast, store.
+// Sum split-K partials in split order, scale by alpha, cast, store. Without swap a thread takes four
+// columns of a row (the partials' rows are padded to whole tiles): bound by reading them from L2.
+template <bool SWAP>
 __global__ void splitk_reduce_kernel(const float *__restrict__ partial, int splits,
                                      int64_t rows_a, int64_t rows_b, int64_t a_pad,
                                      int64_t b_pad, const float *__restrict__ a_gs,
                                      const float *__restrict__ w_gs, void *__restrict__ y,
-                                     int64_t ldy, int out_bf16, int swap)
+                                     int64_t ldy, int out_bf16)
 {
     const float alpha = a_gs ? __fmul_rn(*a_gs, *w_gs) : 1.0f; // MXFP4: no global scales
-    const int64_t total = rows_a * rows_b;
-    for (int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; i < total;
-         i += (int64_t)gridDim.x * blockDim.x) {
-        int64_t a, b;
-        if (swap) {
-            a = i % rows_a;
-            b = i / rows_a;
-        } else {
-            a = i / rows_b;
-            b = i % rows_b;
-        }
-        float acc = 0.0f;
-        for (int s = 0; s < splits; ++s)
-            acc += partial[((int64_t)s * a_pad + a) * b_pad + b];
+    auto put = [&](int64_t off, float acc) {
         const float r = acc * alpha;
-        const int64_t off = swap ? (b * ldy + a) : (a * ldy + b);
         if (out_bf16)
             reinterpret_cast<__nv_bfloat16 *>(y)[off] = __float2bfloat16_rn(r);
         else
             reinterpret_cast<float *>(y)[off] = r;
+    };
+    if constexpr (SWAP) {
+        const int64_t total = rows_a * rows_b;
+        for (int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; i < total;
+             i += (int64_t)gridDim.x * blockDim.x) {
+            const int64_t a = i % rows_a, b = i / rows_a;
+            float acc = 0.0f;
+            for (int s = 0; s < splits; ++s)
+                acc += partial[((int64_t)s * a_pad + a) * b_pad + b];
+            put(b * ldy + a, acc);
+        }
+    } else {
+        const int64_t quads = (rows_b + 3) / 4;
+        for (int64_t a = blockIdx.x; a < rows_a; a += gridDim.x)
+            for (int64_t q = threadIdx.x; q < quads; q += blockDim.x) {
+                const float4 *src = reinterpret_cast<const float4 *>(partial + a * b_pad) + q;
+                float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll 4
+                for (int s = 0; s < splits; ++s) {
+                    const float4 v = src[(int64_t)s * a_pad * (b_pad >> 2)];
+                    acc.x += v.x;
+                    acc.y += v.y;
+                    acc.z += v.z;
+                    acc.w += v.w;
+                }
+                const float r[4] = {acc.x, acc.y, acc.z, acc.w};
+                for (int i = 0; i < 4 && 4 * q + i < rows_b; ++i)
+                    put(a * ldy + 4 * q + i, r[i]);
+            }
     }
 }
 
@@ -1977,14 +2054,16 @@ bool make_sf_map(CUtensorMap *m, const void *base, int64_t rows, int64_t K, int 
                        CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// bf16 output Y [rows x cols], box 64 columns x 128 rows, 128B swizzle (TMA store).
-bool make_out_map(CUtensorMap *m, void *base, int64_t rows, int64_t cols)
+// Output Y [rows x cols] (bf16 or fp32), box 128 bytes x 128 rows, 128B swizzle (TMA store).
+bool make_out_map(CUtensorMap *m, void *base, int64_t rows, int64_t cols, int bf16 = 1)
 {
+    const cuuint64_t esz = bf16 ? 2 : 4;
     cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows};
-    cuuint64_t strides[1] = {(cuuint64_t)(cols * 2)};
-    cuuint32_t box[2] = {64u, 128u};
+    cuuint64_t strides[1] = {(cuuint64_t)cols * esz};
+    cuuint32_t box[2] = {(cuuint32_t)(128 / esz), 128u};
     cuuint32_t estr[2] = {1u, 1u};
-    return encode_fn()(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, base, dims, strides, box, estr,
+    return encode_fn()(m, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32,
+                       2, base, dims, strides, box, estr,
                        CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
                        CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                        CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
@@ -2046,7 +2125,7 @@ cudaError_t launch_bn(const LinearPlan &pl, const uint8_t *a_codes, const uint8_
 }
 
 // LR: lr_t (T' [M x lr_rank] bf16) and lr_u (U [N x lr_rank] bf16) feed the low-rank k-tiles.
-template <bool QOUT, bool LR = false, class F = FmtNvfp4>
+template <bool QOUT, bool LR = false, class F = FmtNvfp4, bool F32 = false>
 cudaError_t launch_pair(const uint8_t *a_codes, const uint8_t *a_sf, const uint8_t *w_codes,
                         const uint8_t *w_sf, int64_t M, int64_t N, int64_t K, GemmParams gp,
                         cudaStream_t s, nvfp4_status *st, const void *lr_t = nullptr,
@@ -2058,7 +2137,7 @@ cudaError_t launch_pair(const uint8_t *a_codes, const uint8_t *a_sf, const uint8
     std::memset(&tmU, 0, sizeof(tmU));
     if (!encode_fn() || !make_codes_map(&tmA, a_codes, M, K, 128) ||
         !make_codes_map(&tmB, w_codes, N, K, 128) || !make_sf_map<F>(&tmSFA, a_sf, M, K, 1) ||
-        !make_sf_map<F>(&tmSFB, w_sf, N, K, 2) || (!QOUT && !make_out_map(&tmY, gp.y, M, N)) ||
+        !make_sf_map<F>(&tmSFB, w_sf, N, K, 2) || (!QOUT && !make_out_map(&tmY, gp.y, M, N, !F32)) ||
         (LR && (!make_bf16_kmajor_map(&tmT, lr_t, M, lr_rank, 128) ||
                 !make_bf16_kmajor_map(&tmU, lr_u, N, lr_rank, 128)))) {
         *st = NVFP4_ERR_CUDA;
@@ -2070,7 +2149,7 @@ cudaError_t launch_pair(const uint8_t *a_codes, const uint8_t *a_sf, const uint8
     cudaGetDevice(&dev);
     cudaError_t attr_err = cudaSuccess;
     std::call_once(flags[dev & 63], [&]() {
-        attr_err = cudaFuncSetAttribute(nvfp4_gemm_pair_kernel<QOUT, LR, F>,
+        attr_err = cudaFuncSetAttribute(nvfp4_gemm_pair_kernel<QOUT, LR, F, F32>,
                                         cudaFuncAttributeMaxDynamicSharedMemorySize,
                                         Pair<QOUT, F>::kSmemBytes);
     });
@@ -2097,7 +2176,7 @@ cudaError_t launch_pair(const uint8_t *a_codes, const uint8_t *a_sf, const uint8
     at[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = at;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, nvfp4_gemm_pair_kernel<QOUT, LR, F>, tmA, tmB, tmSFA, tmSFB,
+    return cudaLaunchKernelEx(&cfg, nvfp4_gemm_pair_kernel<QOUT, LR, F, F32>, tmA, tmB, tmSFA, tmSFB,
                               tmY, tmT, tmU, gp);
 }
 
@@ -2373,9 +2452,17 @@ cudaError_t launch_linear_fmt(const LinearPlan &pl, const uint8_t *a_codes, cons
         default: return launch_smallm<128, false, F>(pl, ca, sa, cb, sb, K, sp, s, st);
         }
     }
-    if (!pl.swap_ab && pl.splits == 1 && out_bf16 && N % 8 == 0 &&
-        (reinterpret_cast<uintptr_t>(y) & 15u) == 0 && kUsePairKernel)
-        return launch_pair<false, false, F>(a_codes, a_sf, w_codes, w_sf, M, N, K, gp, s, st);
+    if (!pl.swap_ab && pl.splits == 1 && (reinterpret_cast<uintptr_t>(y) & 15u) == 0 &&
+        kUsePairKernel) { // TMA stores rows of whole 16-byte pieces
+        if (out_bf16 && N % 8 == 0)
+            return launch_pair<false, false, F>(a_codes, a_sf, w_codes, w_sf, M, N, K, gp, s, st);
+        // fp32 on MXFP4 operands only (4096 x 2048, K 2000: 28 us from the 1-SM kernel, 19 us);
+        // the NVFP4 layer keeps the kernel that its fp32 results come from.
+        if constexpr (F::kMx)
+            if (!out_bf16 && N % 4 == 0)
+                return launch_pair<false, false, F, true>(a_codes, a_sf, w_codes, w_sf, M, N, K,
+                                                          gp, s, st);
+    }
     switch (pl.bn) {
     case 8: e = launch_bn<8, F>(pl, ca, sa, cb, sb, K, gp, s, st); break;
     case 16: e = launch_bn<16, F>(pl, ca, sa, cb, sb, K, gp, s, st); break;
@@ -2386,14 +2473,17 @@ cudaError_t launch_linear_fmt(const LinearPlan &pl, const uint8_t *a_codes, cons
     }
     if (e != cudaSuccess || pl.splits == 1)
         return e;
-    const int64_t total = pl.rows_a * pl.rows_b;
-    int64_t g = (total + 255) / 256;
+    const float *part = reinterpret_cast<const float *>(ws);
+    const int64_t a_pad = pl.tiles_a * 128, b_pad = pl.tiles_b * pl.bn;
     const int64_t cap = (int64_t)num_sms() * 8;
-    if (g > cap)
-        g = cap;
-    splitk_reduce_kernel<<<(unsigned)g, 256, 0, s>>>(
-        reinterpret_cast<const float *>(ws), pl.splits, pl.rows_a, pl.rows_b, pl.tiles_a * 128,
-        pl.tiles_b * pl.bn, a_gs, w_gs, y, N, out_bf16, pl.swap_ab ? 1 : 0);
+    const int64_t want = pl.swap_ab ? (pl.rows_a * pl.rows_b + 255) / 256 : pl.rows_a;
+    const unsigned g = (unsigned)(want < cap ? want : cap);
+    if (pl.swap_ab)
+        splitk_reduce_kernel<true><<<g, 256, 0, s>>>(part, pl.splits, pl.rows_a, pl.rows_b, a_pad,
+                                                     b_pad, a_gs, w_gs, y, N, out_bf16);
+    else
+        splitk_reduce_kernel<false><<<g, 256, 0, s>>>(part, pl.splits, pl.rows_a, pl.rows_b, a_pad,
+                                                      b_pad, a_gs, w_gs, y, N, out_bf16);
     return cudaGetLastError();
 }
 
