@@ -375,6 +375,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
+    pdl_wait(); // operands, scales, partials and Y belong to the stream's earlier work
 
     const int64_t tiles_ab = p.tiles_a * p.tiles_b;
 
@@ -631,6 +632,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
     }
 
+    pdl_launch_dependents(); // all of this CTA's work is issued: the next kernel may launch
     if (threadIdx.x == 64)
         bulk_wait_group0(); // bulk stores complete before the CTA's shared memory goes away
     tc_fence_before();
@@ -1312,6 +1314,7 @@ __global__ void splitk_reduce_kernel(const float *__restrict__ partial, int spli
                                      const float *__restrict__ w_gs, void *__restrict__ y,
                                      int64_t ldy, int out_bf16)
 {
+    pdl_wait();
     const float alpha = a_gs ? __fmul_rn(*a_gs, *w_gs) : 1.0f; // MXFP4: no global scales
     auto put = [&](int64_t off, float acc) {
         const float r = acc * alpha;
@@ -2119,9 +2122,8 @@ cudaError_t launch_bn(const LinearPlan &pl, const uint8_t *a_codes, const uint8_
     int64_t grid = gp.units < num_sms() ? gp.units : num_sms();
     if (grid < 1)
         grid = 1;
-    nvfp4_gemm_kernel<BN, F><<<(unsigned)grid, kThreads, C::kSmemBytes, s>>>(tmA, tmB, tmSFA,
-                                                                             tmSFB, tmY, gp);
-    return cudaGetLastError();
+    return launch_pdl(nvfp4_gemm_kernel<BN, F>, dim3((unsigned)grid), kThreads, C::kSmemBytes, s, tmA,
+                      tmB, tmSFA, tmSFB, tmY, gp);
 }
 
 // LR: lr_t (T' [M x lr_rank] bf16) and lr_u (U [N x lr_rank] bf16) feed the low-rank k-tiles.
@@ -2478,13 +2480,9 @@ cudaError_t launch_linear_fmt(const LinearPlan &pl, const uint8_t *a_codes, cons
     const int64_t cap = (int64_t)num_sms() * 8;
     const int64_t want = pl.swap_ab ? (pl.rows_a * pl.rows_b + 255) / 256 : pl.rows_a;
     const unsigned g = (unsigned)(want < cap ? want : cap);
-    if (pl.swap_ab)
-        splitk_reduce_kernel<true><<<g, 256, 0, s>>>(part, pl.splits, pl.rows_a, pl.rows_b, a_pad,
-                                                     b_pad, a_gs, w_gs, y, N, out_bf16);
-    else
-        splitk_reduce_kernel<false><<<g, 256, 0, s>>>(part, pl.splits, pl.rows_a, pl.rows_b, a_pad,
-                                                      b_pad, a_gs, w_gs, y, N, out_bf16);
-    return cudaGetLastError();
+    return launch_pdl(pl.swap_ab ? splitk_reduce_kernel<true> : splitk_reduce_kernel<false>, dim3(g),
+                      256, 0, s, part, pl.splits, pl.rows_a, pl.rows_b, a_pad, b_pad, a_gs, w_gs, y, N,
+                      out_bf16);
 }
 
 } // namespace

@@ -113,6 +113,25 @@ cudaError_t launch_linear_xq(const LinearPlan &pl, const void *x, int x_bf16,
                              int64_t M, int64_t N, int64_t K, int out_bf16, void *y,
                              float *x_gs_out, unsigned flags, cudaStream_t s, nvfp4_status *st);
 
+// A launch that may set up while the stream's previous kernel ends: the kernel calls pdl_wait()
+// before it touches anything that others write or read.
+template <typename... P, typename... A>
+cudaError_t launch_pdl(void (*kernel)(P...), dim3 grid, int threads, size_t smem, cudaStream_t s,
+                       A... args)
+{
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3((unsigned)threads, 1, 1);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, static_cast<P>(args)...);
+}
+
 // Packed FP4 codes of `mats` matrices [rows x K/2] bytes behind one another as a TMA map, box 128
 // bytes x box_rows x box_mats, 128B swizzle.
 bool make_fp4_codes_map(CUtensorMap *m, const void *base, int64_t mats, int64_t rows, int64_t K,
