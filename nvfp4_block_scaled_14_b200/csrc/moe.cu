@@ -6,10 +6,9 @@
 // with e = ids[t,k]. With at most 64 tokens the cost is reading the met experts' weights once.
 //
 // The weights go to the FP4 tensor cores as they are stored. Those multiply FP4 by FP4 only, so an
-// activation is split into eight FP4 terms, each the FP4 form of what the ones before leave
-// (put_terms), and the eight products are added: the weights lose nothing and the activations at
-// most 2^-22 (MXFP4) of their block's largest value, or 2^-18 (NVFP4) of their row's, while the terms' columns cost the otherwise idle MMA
-// 8 of its up to 256 columns a token. (Decoding the weights to f16 on the CUDA cores for mma.sync
+// activation is split into eight FP4 terms (put_terms) and the eight products are added: the weights
+// lose nothing and the activations at most 2^-22 (MXFP4) of their block's largest value, or 2^-18
+// (NVFP4) of their row's, while the terms cost the otherwise idle MMA eight columns a token. (Decoding the weights to f16 on the CUDA cores for mma.sync
 // took 40-54 issue slots per 16 x 32 codes, as long as HBM takes to deliver them, and ran at a
 // quarter of it: 64 tokens, 64 experts of 2048 x 1024, top 8: 135 us.)
 #include <mutex>
@@ -190,9 +189,14 @@ __global__ void __cluster_dims__(kRouteCluster, 1, 1) __launch_bounds__(kRouteTh
 // Experts
 // ---------------------------------------------------------------------------------------
 
-constexpr int kTerms = 8;  // FP4 terms of an activation: the rows of one swizzle atom
-constexpr int kCols = 16;  // tokens of a column tile: 128 MMA columns
-constexpr int kFeeders = 2; // groups of four warps
+constexpr int kTerms = 8; // FP4 terms of an activation: the rows of one swizzle atom
+// Tokens of a column tile: 128 MMA columns. An expert with more tokens streams its weights once per
+// tile (tiles of 8: 64 tokens, 64 experts of 2048 x 1024, top 8, 77 us instead of 67; larger tiles'
+// two accumulators and the scales pass TMEM).
+constexpr int kCols = 16;
+// Groups of four scale-feeder warps, in turn: one takes 750 cycles a k-tile (64 tokens: 71 us instead
+// of 67), a third gives nothing (68.9 against 68.5).
+constexpr int kFeeders = 2;
 constexpr int kThreads = 32 * (7 + 4 * kFeeders);
 constexpr int kUpRows = 64, kDownRows = 128; // rows of F, of H, per tile
 
@@ -624,8 +628,9 @@ __device__ __forceinline__ void feed_rows(const uint8_t *sm, uint32_t tcol, int 
         tmem_st_32x32b_x16(tcol, r);
 }
 
-// A scale feeder thread's row: its scale bytes of every other k-tile, from `first` on (k-tiles count on
-// from one run into the next), into a ring of kSfRing slots of 128 rows of weights and (MXFP4) 128 of terms.
+// A scale feeder thread's row: its scale bytes of every kFeeders-th k-tile, from `first` on (k-tiles
+// count on from one run into the next), into a ring of kSfRing slots of 128 rows of weights and
+// (MXFP4) 128 of terms.
 template <class F, bool DOWN> struct ScaleRow {
     static constexpr int SB = 4 * F::kAtoms; // bytes of a row and k-tile
     static constexpr int kSlot = (F::kMx ? 2 : 1) * 128 * SB;
@@ -715,8 +720,8 @@ __device__ __forceinline__ void put_y(__nv_bfloat16 *y, const float4 &v)
 // rows of each token of a column tile the N side (8..128 columns), so the weights go from HBM to the
 // tensor cores as they are stored and the sum of a token's eight columns is the product with its
 // full-precision value. Roles:
-//   warp 0       TMA producer of the weights: per 256-wide k-tile the tile's two 64-row halves (the
-//                next phase's first stages before the barriers);
+//   warp 0       TMA producer of the weights: per 256-wide k-tile one box of 128 rows (the next
+//                phase's first stages before the barriers);
 //   warp 14      TMA producer of the term rows: a box per four tokens of the column tile;
 //   warps 6..13  scale feeders, two groups in turn: the rows' linear scale bytes to shared memory by
 //                cp.async ahead of time, then to the stage's TMEM columns in the MMA's layout (one
@@ -729,10 +734,17 @@ __device__ __forceinline__ void put_y(__nv_bfloat16 *y, const float4 &v)
 //                sums of every column tile are added to [T][128] sums in shared memory, which go to y
 //                or, split by split, to the workspace.
 // A stage's bytes and scales complete one barrier, and the MMAs that have read them another.
-// Bound by HBM: a k-tile's 16 KB take 370 ns of an SM's share, its four MMAs of N = 64 about 70 ns; a
-// role must therefore take fewer than 700 cycles a k-tile, which is why each is a warp of its own with
-// few instructions a step. Waits are bounded; after one that gave up the roles run on without waiting
-// and the status word says so.
+// Measured, with the router, ids and inputs new each call: 64 tokens, 64 MXFP4 experts of 2048 x 1024,
+// top 8: 67 us (214 MB of met weights: 3.2 TB/s); 16 tokens, 28 of 32 NVFP4 experts of 4096 x 1280, top
+// 4: 72 us; one token, 6 experts of 2048 x 1408: 28 us. Of the 64 tokens' 60 us in this kernel, gate/up
+// take 26 (22 at the copy rate), down 17 (11), the rest are lists (3), terms (2.5), the barriers with
+// the wait for the slowest CTA (9) and the sums. Products are bound by HBM and by the roles' latency
+// together: a k-tile's 16 KB take 700 cycles of an SM's share, and the MMA warp's step (a completed
+// wait is 95 cycles, four MMAs and a commit 300) leaves little of that; with all weights in L2 the
+// whole call still takes 63 us, and separate rings for weights and terms, with a second wait and
+// commit a step, took 77. So a role is a warp of its own with few instructions a step, and in a group
+// of warps one polls while the others sleep at a named barrier. Waits are bounded; after one that gave
+// up the roles run on without waiting, no further copies are issued, and the status word says so.
 template <class F>
 __global__ void __launch_bounds__(kThreads, 1)
     moe_experts_kernel(const __grid_constant__ CUtensorMap tmUp,
@@ -1225,22 +1237,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
 }
 
-// Jobs per 128-row block of y: as many as give every SM one, or more where that would leave over 5%
-// more of the SMs idle (at most twice as many, four for many blocks: each costs T x 512 bytes of sums
-// written and read).
+// Jobs per 128-row block of y: as many as give every SM at most one. (Two a CTA where that leaves SMs
+// idle, 288 jobs instead of 128 for 32 blocks, costs more in sums written and read than it fills: 16
+// tokens, H 4096: 71.6 us against 72.6.)
 int moe_splits(int64_t H)
 {
-    const int64_t sms = num_sms(), blocks = (H + kDownRows - 1) / kDownRows;
-    const int64_t one = sms / blocks, lo = one < 1 ? 1 : one, hi = one < 2 ? 4 : 2 * one + 1;
-    auto used = [&](int64_t s) {
-        const int64_t jobs = blocks * s, rounds = (jobs + sms - 1) / sms;
-        return (double)jobs / (double)(rounds * sms);
-    };
-    int64_t best = lo;
-    for (int64_t s = lo + 1; s <= hi; ++s)
-        if (used(s) > used(best) + 0.05)
-            best = s;
-    return (int)best;
+    const int64_t s = num_sms() / ((H + kDownRows - 1) / kDownRows);
+    return (int)(s < 1 ? 1 : s);
 }
 
 // The workspace: offsets of MoeShared's arrays for T tokens of k experts.

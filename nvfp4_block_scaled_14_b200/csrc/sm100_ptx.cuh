@@ -48,18 +48,6 @@ __device__ __forceinline__ float e4m3_to_f32(uint32_t b)
     return __half2float(__half(hr));
 }
 
-// Two E4M3 bytes (the low 16 bits) -> two fp32 (exact).
-__device__ __forceinline__ float2 e4m3x2_to_f32x2(uint32_t b)
-{
-    uint32_t h2;
-    const uint16_t in = (uint16_t)b;
-    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h2) : "h"(in));
-    __half2_raw r;
-    r.x = (unsigned short)(h2 & 0xFFFFu);
-    r.y = (unsigned short)(h2 >> 16);
-    return __half22float2(__half2(r));
-}
-
 // One byte of two E2M1 codes -> two fp32 (low nibble first), exact.
 __device__ __forceinline__ float2 e2m1x2_to_f32x2(uint32_t byte)
 {
@@ -381,12 +369,6 @@ __device__ __forceinline__ void fence_proxy_async_smem()
 __device__ __forceinline__ void named_bar_sync(uint32_t id, uint32_t nthreads)
 {
     asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(nthreads) : "memory");
-}
-
-// Arrive on a named barrier without waiting for it.
-__device__ __forceinline__ void named_bar_arrive(uint32_t id, uint32_t nthreads)
-{
-    asm volatile("bar.arrive %0, %1;" ::"r"(id), "r"(nthreads) : "memory");
 }
 
 __device__ __forceinline__ void sts128(uint32_t saddr, uint32_t a, uint32_t b, uint32_t c,
