@@ -88,6 +88,9 @@ __global__ void __launch_bounds__(kThreads)
     const int lane_r = tid / kLanesPerRow, lane_c = tid % kLanesPerRow;
     const int col = lane_c * (16 * kVec / kEsz); // this lane's first column of the tile
     const bool col_ok = c0 + col < p.cols;
+    // Half of the lanes take their second vector first: eight lanes' 16-byte shared stores at a stride
+    // of 32 bytes then meet every bank once.
+    const int flip = COLS && kVec == 2 ? (lane_c >> 2) & 1 : 0;
 
     uint4 v[kPasses][kVec];
 #pragma unroll
@@ -101,7 +104,7 @@ __global__ void __launch_bounds__(kThreads)
                 reinterpret_cast<const uint8_t *>(p.x) + (r * p.cols + c0 + col) * kEsz);
 #pragma unroll
             for (int j = 0; j < kVec; ++j)
-                v[i][j] = __ldg(src + j);
+                v[i][j] = __ldg(src + (j ^ flip));
         }
     }
     if constexpr (COLS) {
@@ -111,7 +114,7 @@ __global__ void __launch_bounds__(kThreads)
                 reinterpret_cast<uint4 *>(dyn + (i * kRowsPerPass + lane_r) * kPitch) + lane_c * kVec;
 #pragma unroll
             for (int j = 0; j < kVec; ++j)
-                dst[j] = v[i][j];
+                dst[j ^ flip] = v[i][j];
         }
     }
     if constexpr (ROWS) {
@@ -149,12 +152,14 @@ __global__ void __launch_bounds__(kThreads)
                     const uint32_t hi = mx_codes_bf16x8(b.x, b.y, b.z, b.w, inv);
                     if (live)
                         *reinterpret_cast<uint2 *>(dst) =
-                            sb == kMxNan ? make_uint2(0u, 0u) : make_uint2(lo, hi);
+                            sb == kMxNan ? make_uint2(0u, 0u)
+                                         : make_uint2(flip ? hi : lo, flip ? lo : hi);
                 } else if (live) {
                     *reinterpret_cast<uint32_t *>(dst) = sb == kMxNan ? 0u : lo;
                 }
             } else {
-                const uint32_t w = mx_codes_f32x8(a, b, inv);
+                const uint32_t ab = mx_codes_f32x8(a, b, inv); // four codes in either half
+                const uint32_t w = flip ? __byte_perm(ab, 0u, 0x1032) : ab;
                 if (live)
                     *reinterpret_cast<uint32_t *>(dst) = sb == kMxNan ? 0u : w;
             }
@@ -202,10 +207,15 @@ __global__ void __launch_bounds__(kThreads)
                 for (int q = 0; q < 4; ++q) {
                     float y[8];
 #pragma unroll
-                    for (int k = 0; k < 8; ++k)
-                        y[k] = __fmul_rn(__uint_as_float(h ? u[8 * q + k] & 0xFFFF0000u
-                                                           : u[8 * q + k] << 16),
-                                         inv);
+                    for (int k = 0; k < 8; k += 2) {
+                        const uint32_t a = u[8 * q + k], b = u[8 * q + k + 1];
+                        const float2 f = __fmul2_rn(
+                            make_float2(__uint_as_float(h ? a & 0xFFFF0000u : a << 16),
+                                        __uint_as_float(h ? b & 0xFFFF0000u : b << 16)),
+                            make_float2(inv, inv));
+                        y[k] = f.x;
+                        y[k + 1] = f.y;
+                    }
                     w[q] = cvt_e2m1x8(y);
                 }
                 put(2 * cp + h, blk, w, sb);
@@ -228,8 +238,12 @@ __global__ void __launch_bounds__(kThreads)
                 for (int q = 0; q < 4; ++q) {
                     float y[8];
 #pragma unroll
-                    for (int k = 0; k < 8; ++k)
-                        y[k] = __fmul_rn(u[8 * q + k], inv);
+                    for (int k = 0; k < 8; k += 2) {
+                        const float2 f = __fmul2_rn(make_float2(u[8 * q + k], u[8 * q + k + 1]),
+                                                    make_float2(inv, inv));
+                        y[k] = f.x;
+                        y[k + 1] = f.y;
+                    }
                     w[q] = cvt_e2m1x8(y);
                 }
                 put(c, blk, w, sb);
