@@ -50,6 +50,15 @@ __device__ __forceinline__ uint32_t max_u16x2(uint32_t a, uint32_t b)
 
 constexpr uint32_t kAbs16x2 = 0x7FFF7FFFu;
 
+// max(|a|, |b|) per bf16 half, NaN if either is, the sign bits left to be masked: one instruction for
+// a mask and a maximum.
+__device__ __forceinline__ uint32_t max_abs_bf16x2(uint32_t a, uint32_t b)
+{
+    uint32_t d;
+    asm("max.NaN.xorsign.abs.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+    return d;
+}
+
 // Eight bf16 (four words) -> eight E2M1 codes of x * inv.
 __device__ __forceinline__ uint32_t mx_codes_bf16x8(uint32_t a, uint32_t b, uint32_t c, uint32_t d,
                                                     float inv)
