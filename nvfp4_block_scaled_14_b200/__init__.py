@@ -644,7 +644,9 @@ def moe_experts(x: torch.Tensor, ids: torch.Tensor, weights: torch.Tensor,
     y[t] = sum_s weights[t, s] * down_e (silu(gate_e x[t]) * (up_e x[t])), e = ids[t, s].
 
     x [T, H] bf16; ids int32 and weights fp32 [T, k] (an id outside the experts names none);
-    gate_up: E x [2F, H] (gate rows first); down: E x [H, F]; both NVFP4 or both MXFP4."""
+    gate_up: E x [2F, H] (gate rows first); down: E x [H, F]; both NVFP4 or both MXFP4. x and the
+    hidden values are not rounded to 4 bits (off by at most 2^-22 of the largest of 32 for MXFP4,
+    2^-18 of the row's largest for NVFP4 weights); the same call gives the same bits."""
     if not isinstance(x, torch.Tensor) or x.dtype != torch.bfloat16 or x.dim() != 2 or \
             not x.is_cuda:
         raise TypeError("moe_experts expects 2-D CUDA bfloat16 activations")

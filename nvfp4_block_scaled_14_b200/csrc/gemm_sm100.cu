@@ -3,7 +3,10 @@
 // Y = dequant(A) . dequant(W)^T with A [M x K] and W [N x K] in NVFP4: E2M1 codes, one E4M3
 // scale per 16 values along K, one fp32 global scale per tensor ("Qwen-Image NVFP4 on a 16 GB
 // Ada GPU", "What NVFP4 is and how it differs from NF4": on Blackwell the tensor cores
-// multiply in FP4 with weights and activations both in 4 bits).
+// multiply in FP4 with weights and activations both in 4 bits). The same kernels take MXFP4
+// operands (template parameter F, fp4_format.cuh): one E8M0 scale per 32 values, two scale atoms a
+// k-tile instead of four, kind::mxf4 with scale_vec::2X, no global scale. M 4096, N 12288, K 4096
+// bf16 out: 86 us (4770 TFLOP/s).
 //
 // Kernel structure (one CTA per SM, persistent over work units, 10 warps):
 //   warp 0      TMA producer: per 256-wide k-tile loads the A tile (128 rows x 128 B of packed
@@ -29,7 +32,7 @@
 // nvfp4_gemm_pair_kernel instead: the two CTAs of a cluster share 256 x 256 tiles
 // (tcgen05 cta_group::2, M256 x N256 x K64 MMAs issued by the leader; each CTA loads 128 rows
 // of A and 128 rows of B and holds its 128 rows of the accumulator), with the same warp roles.
-// Its bf16 epilogue stores the first half of a tile before it hands the accumulator back and
+// Its bf16 (MXFP4: or fp32) epilogue stores the first half of a tile before it hands the accumulator back and
 // the second half after; the NVFP4-output form parks half of the accumulator in spare TMEM
 // columns and the other half in shared memory, so the whole tile is activated and quantized
 // while the next tile's MMAs run.
