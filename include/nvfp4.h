@@ -456,7 +456,7 @@ typedef enum { NVFP4_EXPERTS_NVFP4 = 0, NVFP4_EXPERTS_MXFP4 = 1 } nvfp4_experts_
  * results of its token NaN or infinite and no other token's. One cooperative kernel, one CTA on every
  * SM, with a bounded grid barrier of the library's (as the single-pass quantizers); an expert that no
  * token names is not read.
- * H, F: multiples of 32. E: 1..512. top_k: 1..32.
+ * H, F: multiples of 32, E * 2F and E * H below 2^31. E: 1..512. top_k: 1..32.
  * ws: nvfp4_moe_workspace_bytes(T, H, F, top_k) bytes (any contents).
  */
 size_t nvfp4_moe_workspace_bytes(int64_t T, int64_t H, int64_t F, int64_t top_k);

@@ -650,7 +650,7 @@ nvfp4_status nvfp4_moe_experts(const void *x_bf16, int64_t T, int64_t H, int64_t
         return NVFP4_ERR_INVALID_ARG;
     if (T < 0 || T > kMoeMaxTokens || H < 32 || H >= kMaxDim || H % 32 != 0 || F < 32 ||
         F >= kMaxDim / 2 || F % 32 != 0 || E < 1 || E > kMoeMaxExperts || top_k < 1 ||
-        top_k > kMoeMaxTopK)
+        top_k > kMoeMaxTopK || E * 2 * F >= kMaxDim || E * H >= kMaxDim) // (stacked rows in int32)
         return NVFP4_ERR_SHAPE;
     if (T == 0)
         return NVFP4_OK;

@@ -53,6 +53,8 @@ def test_experts_refusals(lib):
     assert call(F=0) == L.NVFP4_ERR_SHAPE
     assert call(E=513) == L.NVFP4_ERR_SHAPE
     assert call(k=33) == L.NVFP4_ERR_SHAPE
+    assert call(E=512, F=1 << 21) == L.NVFP4_ERR_SHAPE       # 2^31 stacked gate/up rows
+    assert call(E=512, H=1 << 22) == L.NVFP4_ERR_SHAPE       # 2^31 stacked down rows
     assert call(x=None) == L.NVFP4_ERR_INVALID_ARG
     assert call(fmt=0) == L.NVFP4_ERR_INVALID_ARG            # NVFP4 without global scales
     assert call(fmt=0, ugs=FAKE, dgs=FAKE + 2) == L.NVFP4_ERR_ALIGNMENT
@@ -273,7 +275,11 @@ def some_ids(T, k, E, seed):
 
 EXPERT_SHAPES = [(1, 32, 32, 1, 1), (1, 2048, 1408, 8, 4), (2, 160, 96, 3, 2), (5, 96, 416, 4, 3),
                  (8, 256, 256, 2, 2), (9, 128, 160, 1, 1), (17, 288, 224, 2, 1),
-                 (33, 544, 64, 5, 4), (64, 512, 256, 8, 8), (64, 128, 128, 512, 2)]
+                 (33, 544, 64, 5, 4), (64, 512, 256, 8, 8), (64, 128, 128, 512, 2),
+                 (64, 64, 32, 40, 32),      # the most rows
+                 (16, 1056, 1312, 2, 2),    # scale rows that end inside a k-tile
+                 (2, 9600, 64, 2, 2),       # one CTA per block of y
+                 (5, 20480, 96, 3, 2)]      # more blocks of y than SMs
 
 
 @pytest.mark.gpu

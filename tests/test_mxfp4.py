@@ -269,7 +269,7 @@ def check_product(y, va, vw, what=""):
 SHAPES = [(1, 8, 32), (1, 4096, 2048), (3, 130, 96), (8, 1000, 4096), (16, 1001, 2080),
           (17, 264, 64), (33, 2048, 1056), (64, 384, 512), (128, 520, 1024), (128, 40000, 256),
           (129, 256, 256), (200, 256, 8192), (257, 1001, 2080), (300, 520, 160),
-          (513, 1024, 1376)]
+          (513, 1024, 1376), (1999, 2052, 160), (2100, 1044, 2080), (1290, 2050, 288)]
 
 
 @pytest.mark.gpu
@@ -324,6 +324,20 @@ def test_training_products(cuda, M, N, K):
     for a, b, out in ((x_, w_, torch.bfloat16), (d_, wt, torch.bfloat16), (dt, xt, torch.float32)):
         check_product(nv.linear_mxfp4(a, b, out), val(a), val(b))
     assert nv.linear_mxfp4(dt, xt).shape == (N, K)
+
+
+@pytest.mark.gpu
+def test_linear_writes_nothing_outside_y(cuda):
+    # fp32 and bf16 y between guard bytes, rows and columns that end inside a tile
+    M, N, K, pad = 1300, 2060, 96, 256
+    a, va = operand(M, K, 7)
+    w, vw = operand(N, K, 8)
+    for dt, esz in ((torch.float32, 4), (torch.bfloat16, 2)):
+        buf = torch.full((M * N * esz + 2 * pad,), 0xA5, dtype=torch.uint8, device="cuda")
+        y = buf[pad:-pad].view(dt).view(M, N)
+        check_product(nv.linear_mxfp4(a, w, dt, out=y), va, vw)
+        torch.cuda.synchronize()
+        assert (buf[:pad] == 0xA5).all() and (buf[-pad:] == 0xA5).all()
 
 
 @pytest.mark.gpu
