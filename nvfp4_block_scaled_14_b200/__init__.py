@@ -456,26 +456,31 @@ def _check_mx(what, q, device, swizzled=False):
     layout, or linear)."""
     if not isinstance(q, MXFP4Tensor):
         raise TypeError(f"{what} expects MXFP4Tensor operands")
-    if q.cols % 32 or q.rows < 0 or q.cols < 0:
+    rows, cols = q.rows, q.cols
+    if cols % 32 or rows < 0 or cols < 0:
         raise ValueError(f"{what}: cols must be a multiple of 32")
-    _check_array(what, "codes", q.codes, device, torch.uint8, (q.rows, q.cols // 2))
+    _check_array(what, "codes", q.codes, device, torch.uint8, (rows, cols // 2))
     if swizzled:
         if q.scales_swz is None:
             raise ValueError(f"{what} needs the swizzled scales")
         _check_array(what, "scales_swz", q.scales_swz, device, torch.uint8,
-                     (_mx_swizzled_bytes(q.rows, q.cols),))
+                     (_mx_swizzled_bytes(rows, cols),))
     else:
         if q.scales_lin is None:
             raise ValueError(f"{what} needs the linear scales")
-        _check_array(what, "scales_lin", q.scales_lin, device, torch.uint8,
-                     (q.rows, q.cols // 32))
+        _check_array(what, "scales_lin", q.scales_lin, device, torch.uint8, (rows, cols // 32))
+
+
+def _empty(rows, cols, dtype, device):
+    """torch.empty((rows, cols)), by the constructor that takes two thirds of its time."""
+    return torch.empty_strided((rows, cols), (cols, 1), dtype=dtype, device=device)
 
 
 def _mx_out(what, out, rows, cols, dtype, device):
     if dtype not in _OUT_TYPES:
         raise TypeError(f"{what}: out_dtype must be float32 or bfloat16")
     if out is None:
-        return torch.empty((rows, cols), dtype=dtype, device=device)
+        return _empty(rows, cols, dtype, device)
     _check_array(what, "out", out, device, dtype, (rows, cols))
     return out
 
@@ -630,8 +635,8 @@ def moe_route(x: torch.Tensor, w: torch.Tensor, top_k: int, bias: torch.Tensor =
     _check_array("moe_route", "bias", bias, dev, torch.float32, (E,))
     if not 1 <= top_k <= min(E, 32):
         raise ValueError("moe_route: top_k must be 1..min(experts, 32)")
-    ids = torch.empty((T, top_k), dtype=torch.int32, device=dev)
-    weights = torch.empty((T, top_k), dtype=torch.float32, device=dev)
+    ids = _empty(T, top_k, torch.int32, dev)
+    weights = _empty(T, top_k, torch.float32, dev)
     _launch("nvfp4_moe_route", dev, x.data_ptr(), w.data_ptr(), _ptr(bias), T, H, E, top_k,
             int(renormalize), ids.data_ptr(), weights.data_ptr())
     return ids, weights
@@ -678,7 +683,7 @@ def moe_experts(x: torch.Tensor, ids: torch.Tensor, weights: torch.Tensor,
             ("down global_scale", down.global_scale, torch.float32, (E,))):
         _check_array("moe_experts", name, t, dev, dtype, shape)
     if out is None:
-        out = torch.empty((T, H), dtype=torch.bfloat16, device=dev)
+        out = _empty(T, H, torch.bfloat16, dev)
     else:
         _check_array("moe_experts", "out", out, dev, torch.bfloat16, (T, H))
     ws_bytes = _moe_workspace_size(dev.index, T, H, F, k)
