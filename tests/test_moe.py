@@ -318,9 +318,10 @@ def test_experts_ids_outside_and_repeated(cuda, fmt):
 
 
 @pytest.mark.gpu
-def test_experts_nonfinite_token_stays_alone(cuda):
+@pytest.mark.parametrize("fmt", ["mxfp4", "nvfp4"])
+def test_experts_nonfinite_token_stays_alone(cuda, fmt):
     T, H, F, E, k = 10, 128, 64, 2, 2
-    up, down = make_experts(E, 2 * F, H, "mxfp4", 1), make_experts(E, H, F, "mxfp4", 2)
+    up, down = make_experts(E, 2 * F, H, fmt, 1), make_experts(E, H, F, fmt, 2)
     x = torch.randn(T, H, device="cuda", generator=gen(3)).bfloat16()
     ids, p = some_ids(T, k, E, 4)
     y = check_experts(x, ids, p, up, down)
