@@ -486,16 +486,13 @@ def _mx_out(what, out, rows, cols, dtype, device):
 
 
 def _mx_alloc(rows, cols, device, swizzled, linear):
-    """An MXFP4Tensor whose arrays are views of one allocation."""
-    n_codes = rows * (cols // 2)
-    n_swz = _mx_swizzled_bytes(rows, cols) if swizzled else 0
-    buf = torch.empty(n_codes + n_swz + (rows * (cols // 32) if linear else 0),
-                      dtype=torch.uint8, device=device)
-    return MXFP4Tensor(
-        buf.as_strided((rows, cols // 2), (cols // 2, 1)),
-        buf.as_strided((n_swz,), (1,), n_codes) if swizzled else None,
-        buf.as_strided((rows, cols // 32), (cols // 32, 1), n_codes + n_swz) if linear else None,
-        rows, cols)
+    """An MXFP4Tensor [rows, cols] with uninitialized arrays, and their addresses."""
+    u8 = torch.uint8
+    codes = _empty(rows, cols // 2, u8, device)
+    swz = torch.empty(_mx_swizzled_bytes(rows, cols), dtype=u8, device=device) if swizzled else None
+    lin = _empty(rows, cols // 32, u8, device) if linear else None
+    return MXFP4Tensor(codes, swz, lin, rows, cols), (
+        codes.data_ptr(), swz.data_ptr() if swizzled else None, lin.data_ptr() if linear else None)
 
 
 def quantize_mxfp4(x: torch.Tensor, scale_rule: str = "floor", orient: str = "rows",
@@ -518,13 +515,15 @@ def quantize_mxfp4(x: torch.Tensor, scale_rule: str = "floor", orient: str = "ro
     rows, cols = x.shape
     if cols % 32:
         raise ValueError("quantize_mxfp4: cols must be a multiple of 32")
-    qr = _mx_alloc(rows, cols, x.device, swizzled, linear) if orient != "cols" else None
-    qc = _mx_alloc(cols, -(-rows // 32) * 32, x.device, swizzled, linear) \
-        if orient != "rows" else None
-    ptrs = [_ptr(t) for q in (qr, qc)
-            for t in ((q.codes, q.scales_swz, q.scales_lin) if q else (None,) * 3)]
-    _launch("nvfp4_quantize_mxfp4", x.device, x.data_ptr(), _OUT_TYPES[x.dtype], rows, cols,
-            _MX_RULES[scale_rule], *ptrs)
+    dev = x.device
+    qr = qc = None
+    to_r = to_c = (None, None, None)
+    if orient != "cols":
+        qr, to_r = _mx_alloc(rows, cols, dev, swizzled, linear)
+    if orient != "rows":
+        qc, to_c = _mx_alloc(cols, -(-rows // 32) * 32, dev, swizzled, linear)
+    _launch("nvfp4_quantize_mxfp4", dev, x.data_ptr(), _OUT_TYPES[x.dtype], rows, cols,
+            _MX_RULES[scale_rule], *to_r, *to_c)
     return (qr, qc) if orient == "both" else qr or qc
 
 
