@@ -428,7 +428,7 @@ __device__ __forceinline__ float row_factor(uint32_t m)
 
 // A CTA's share of the rows' 256-value chunks, one warp each.
 struct MoeChunks {
-    uint32_t per, first, last; // (32 bits: the terms would pass the memory before)
+    uint32_t per, first, last; // (32 bits, as in MoeStart)
 
     __device__ __forceinline__ MoeChunks(int rows, int64_t cols)
     {
@@ -492,8 +492,8 @@ struct MoeGroup {
     bool last;        // down: the job's last run
 };
 
-// Where a CTA's share begins, computed once (in shared memory). k-tiles and 64-column tiles of the
-// longest allowed axes times the 2048 rows pass 32 bits only where the weights pass the memory.
+// Where a CTA's share begins, computed once (in shared memory). 32 bits hold the tile counts: the
+// weights' stacked rows are below 2^31, and an expert has at most four column tiles.
 struct MoeStart {
     int up_kt, up_tiles, down_kt; // k-tiles of H, 64-column tiles of F, k-tiles of F
     int runs, u, tile;            // gate/up: runs of this CTA, the first one's column tile and tile
@@ -729,10 +729,9 @@ __device__ __forceinline__ void put_y(__nv_bfloat16 *y, const float4 &v)
 //   warp 1       MMA issuer; accumulators alternate between two TMEM buffers, so that a tile's
 //                epilogue overlaps the next tile's MMAs;
 //   warps 2..5   epilogue. Gate/up: a tile is 64 gate rows and the same 64 up rows; they meet in
-//                shared memory and silu(gate) * up, in fp32, is split into terms or (NVFP4)
-//                goes to the workspace. Down: the weighted
-//                sums of every column tile are added to [T][128] sums in shared memory, which go to y
-//                or, split by split, to the workspace.
+//                shared memory and silu(gate) * up, in fp32, is split into terms or (NVFP4) goes to
+//                the workspace. Down: the weighted sums of every column tile are added to [T][128]
+//                sums in shared memory, which go to y or, split by split, to the workspace.
 // A stage's bytes and scales complete one barrier, and the MMAs that have read them another.
 // Measured, with the router, ids and inputs new each call: 64 tokens, 64 MXFP4 experts of 2048 x 1024,
 // top 8: 67 us (214 MB of met weights: 3.2 TB/s); 16 tokens, 28 of 32 NVFP4 experts of 4096 x 1280, top
