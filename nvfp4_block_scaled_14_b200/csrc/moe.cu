@@ -8,9 +8,10 @@
 // The weights go to the FP4 tensor cores as they are stored. Those multiply FP4 by FP4 only, so an
 // activation is split into eight FP4 terms (put_terms) and the eight products are added: the weights
 // lose nothing and the activations at most 2^-22 (MXFP4) of their block's largest value, or 2^-18
-// (NVFP4) of their row's, while the terms cost the otherwise idle MMA eight columns a token. (Decoding the weights to f16 on the CUDA cores for mma.sync
-// took 40-54 issue slots per 16 x 32 codes, as long as HBM takes to deliver them, and ran at a
-// quarter of it: 64 tokens, 64 experts of 2048 x 1024, top 8: 135 us.)
+// (NVFP4) of their row's, while the terms cost the otherwise idle MMA eight columns a token.
+// (Decoding the weights to f16 on the CUDA cores for mma.sync took 40-54 issue slots per 16 x 32
+// codes, as long as HBM takes to deliver them, and ran at a quarter of it: 64 tokens, 64 experts of
+// 2048 x 1024, top 8: 135 us.)
 #include <mutex>
 #include <type_traits>
 
@@ -331,9 +332,8 @@ __device__ __forceinline__ void build_lists(const MoeLists &l, const int *ids, c
 //     largest value to 2^8 .. 2^9, X = v * 2^9, six digits of scales 2^8 .. 2^-7 and one of -2 .. 1 of
 //     scale 2^-9: the same scales for every block, none stored. Off by at most 2^-10: 2^-18 of the
 //     row's largest value.
-// The subtraction form (each term the E2M1 rounding of what the ones before leave, at a scale of its
-// own maximum) cost 16 conversions a quarter of the rate of other instructions a value: the 512 x 1024
-// values of 64 tokens took 10 us, this takes 2.
+// Each term as the E2M1 rounding of what the ones before leave, at the best scale for that (a block
+// maximum and a conversion both ways a term), took the 512 x 1024 values of 64 tokens 10 us, against 2.
 // A NaN or an infinity: the block's scale is NaN (MXFP4), or the row's factor is (NVFP4), and so the
 // row's results are.
 //
