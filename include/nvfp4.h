@@ -451,7 +451,8 @@ typedef enum { NVFP4_EXPERTS_NVFP4 = 0, NVFP4_EXPERTS_MXFP4 = 1 } nvfp4_experts_
  * b = 16 and up_gs, down_gs E fp32 global scales for NVFP4, b = 32 and NULL for MXFP4.
  * The activations are not quantized to 4 bits: the FP4 tensor cores multiply the exact weights with
  * x, and with h = silu(.) * (.) in fp32, as the sum of eight FP4 terms that lose at most 2^-22 of the
- * largest value of 32 (MXFP4; and 2^-128), or 2^-18 of the row's largest value (NVFP4). Sums are fp32
+ * largest value of a block of 32 (MXFP4) or 16 (NVFP4; a block whose largest value is below 2^-17 of
+ * its row's counts as having that), and 2^-128. Sums are fp32
  * and run in a fixed order: the same call gives the same bits. A NaN or an infinity in x makes the
  * results of its token NaN or infinite and no other token's. One cooperative kernel, one CTA on every
  * SM, with a bounded grid barrier of the library's (as the single-pass quantizers); an expert that no

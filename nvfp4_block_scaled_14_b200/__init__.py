@@ -649,8 +649,9 @@ def moe_experts(x: torch.Tensor, ids: torch.Tensor, weights: torch.Tensor,
 
     x [T, H] bf16; ids int32 and weights fp32 [T, k] (an id outside the experts names none);
     gate_up: E x [2F, H] (gate rows first); down: E x [H, F]; both NVFP4 or both MXFP4. x and the
-    hidden values are not rounded to 4 bits (off by at most 2^-22 of the largest of 32 for MXFP4,
-    2^-18 of the row's largest for NVFP4 weights); the same call gives the same bits."""
+    hidden values are not rounded to 4 bits: off by at most 2^-22 of the largest of a block of 32
+    (MXFP4 weights) or 16 (NVFP4; at least 2^-39 of the row's largest). The same call gives the
+    same bits."""
     if not isinstance(x, torch.Tensor) or x.dtype != torch.bfloat16 or x.dim() != 2 or \
             not x.is_cuda:
         raise TypeError("moe_experts expects 2-D CUDA bfloat16 activations")

@@ -7,8 +7,8 @@
 //
 // The weights go to the FP4 tensor cores as they are stored. Those multiply FP4 by FP4 only, so an
 // activation is split into eight FP4 terms (put_terms) and the eight products are added: the weights
-// lose nothing and the activations at most 2^-22 (MXFP4) of their block's largest value, or 2^-18
-// (NVFP4) of their row's, while the terms cost the otherwise idle MMA eight columns a token.
+// lose nothing and the activations at most 2^-22 of their block's largest value, while the terms cost
+// the otherwise idle MMA eight columns a token.
 // (Decoding the weights to f16 on the CUDA cores for mma.sync took 40-54 issue slots per 16 x 32
 // codes, as long as HBM takes to deliver them, and ran at a quarter of it: 64 tokens, 64 experts of
 // 2048 x 1024, top 8: 135 us.)
@@ -224,12 +224,13 @@ static_assert(kMoeMaxTokens <= 4 * kCols, "an expert's column tiles count in two
 
 // What the CTAs of one call share in the workspace. Rows: the (expert, token) pairs, in expert order.
 struct MoeShared {
-    uint8_t *x_codes, *h_codes;  // terms of the rows' x and h = silu(gate) * up: [rows * 8][cols / 2]
-    uint8_t *x_scales, *h_scales; // (MXFP4) first terms' scales: [rows][pitch]
-    int64_t x_pitch, h_pitch;
-    uint32_t *x_max, *h_max;     // [rows] (NVFP4): bits of the row's largest magnitude
-    float *h;                    // [rows][F] (NVFP4)
-    float *partial;              // [128-row blocks of y][splits][T][128]
+    // terms of the rows' x and h = silu(gate) * up, k-tile by k-tile: [rows][k-tiles][8 terms][128
+    // bytes]. NVFP4's h lies there in fp32 first, whose 256 values of a k-tile take the same bytes.
+    uint8_t *x_codes, *h_codes;
+    uint8_t *x_scales, *h_scales; // the terms' block scales (first term's): [rows][k-tiles][SB bytes]
+    int64_t x_kt, h_kt;           // k-tiles of a row
+    uint32_t *x_max, *h_max;      // [rows] (NVFP4): bits of the row's largest magnitude
+    float *partial;               // [128-row blocks of y][splits][T][128]
 };
 
 // ---- lists and terms ----------------------------------------------------------------------
@@ -328,65 +329,70 @@ __device__ __forceinline__ void build_lists(const MoeLists &l, const int *ids, c
     }
 }
 
-// Activations as kTerms FP4 terms: the digits of a fixed-point number to base 8. -4 .. 3 are E2M1
+constexpr int kTileBytes = kTerms * 128; // a row's terms of a k-tile
+
+// Activations as kTerms FP4 terms: the digits of a fixed-point number to base 8, X = v / 2^(E - 21),
+// E the exponent of the block's largest value (32 values for MXFP4, 16 for NVFP4). -4 .. 3 are E2M1
 // values, and with digits of that range the 3-bit fields of X + 4 (1 + 8 + 64 + ...) are the digits
-// plus 4; one byte permute looks up four codes. Term j's scale is 8^-j times the first one's.
-//   MXFP4: X = v / 2^(E - 21), E the exponent of the block's largest value (32 values): eight digits,
-//     scales 2^E .. 2^(E - 21). Off by at most half a unit: 2^-22 of the block's largest value (and
-//     2^-128, where E < -106 is taken as -106). Only 2^E is stored.
-//   NVFP4: E4M3 holds 2^8 .. 2^-9 only, so the row is divided by a power of two that brings its
-//     largest value to 2^8 .. 2^9, X = v * 2^9, six digits of scales 2^8 .. 2^-7 and one of -2 .. 1 of
-//     scale 2^-9: the same scales for every block, none stored. Off by at most 2^-10: 2^-18 of the
-//     row's largest value.
+// plus 4; one byte permute looks up four codes. Term j stands for digit * 2^(E - 3j). Off by at most
+// half a unit: 2^-22 of the block's largest value (and 2^-128, where E < -106 is taken as -106).
+//   MXFP4: term j's scale is 2^(E - 3j). Only 2^E is stored.
+//   NVFP4: E4M3 holds the powers 2^8 .. 2^-9 only. Every term has the block's scale 2^(8 - (R - E)), R
+//     the exponent of the row's largest value; the sums of term j's column are multiplied by
+//     2^(R - 8 - 3j) instead, which is the same for the whole row (term_sum, row_factor). Blocks below
+//     2^-17 of the row's largest value are taken at that exponent: off by 2^-39 of the row's largest.
+//     (The eight scales spread over E4M3's range, one exponent a row, left 2^-18 of it.)
 // Each term as the E2M1 rounding of what the ones before leave, at the best scale for that (a block
 // maximum and a conversion both ways a term), took the 512 x 1024 values of 64 tokens 10 us, against 2.
 // A NaN or an infinity: the block's scale is NaN (MXFP4), or the row's factor is (NVFP4), and so the
 // row's results are.
 //
 // v: values c0 .. c0 + 7 of a row of `cols`, lane i's c0 being lane 0's + 8 i in aligned groups of four
-// lanes; zeros behind the row's end. codes: the row's first term; scales: the row's. Called by whole
-// warps.
+// lanes; zeros behind the row's end. codes, scales: the row's; row_e: row_exponent of it (NVFP4). Codes
+// behind the row's end are left: the weights are zero there. Called by whole warps.
 template <bool NV>
 __device__ __forceinline__ void put_terms(const float (&v)[8], int64_t c0, int64_t cols,
-                                          uint8_t *codes, uint8_t *scales, int64_t pitch, bool live)
+                                          uint8_t *codes, uint8_t *scales, int64_t kt, bool live,
+                                          uint32_t row_e)
 {
     constexpr float kMagic = 12582912.0f; // 1.5 * 2^23: the sum's low bits are the rounded integer
     constexpr uint32_t kDigits = 044444444u;
+    constexpr int kBlock = NV ? 16 : 32, kPerTile = 256 / kBlock;
     const bool on = live && c0 < cols;
-    float unit = 512.0f;
-    bool bad = false;
-    if constexpr (!NV) {
-        uint32_t m = 0u;
+    uint32_t m = 0u;
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
-            m = max(m, __float_as_uint(v[i]) & 0x7FFFFFFFu);
-        m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 1));
+    for (int i = 0; i < 8; ++i)
+        m = max(m, __float_as_uint(v[i]) & 0x7FFFFFFFu);
+    m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 1));
+    if constexpr (!NV)
         m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 2));
-        const uint32_t b = max(m >> 23, 21u); // E8M0 byte; 255: NaN
-        bad = b == 255u;
-        unit = __uint_as_float((275u - (bad ? 254u : b)) << 23); // 2^(21 - E)
-        if (live && c0 % 32 == 0 && c0 / 32 < pitch)
-            scales[c0 / 32] = on ? (uint8_t)b : (uint8_t)21;
+    uint32_t b = max(m >> 23, 21u); // E + 127, MXFP4's scale byte; 255: NaN or infinity
+    const bool bad = b == 255u;
+    uint32_t byte = b;
+    if constexpr (NV) {
+        b = min(max(b, row_e - min(row_e, 17u)), row_e);
+        const uint32_t d = row_e - b; // E4M3 of 2^(8 - d)
+        byte = d < 15u ? (15u - d) << 3 : 8u >> (d - 14u);
+    } else {
+        b = bad ? 254u : b;
     }
+    const float unit = __uint_as_float((275u - b) << 23); // 2^(21 - E)
+    if (live && c0 % kBlock == 0 && c0 / kBlock < kt * kPerTile)
+        scales[c0 / kBlock] = on ? (uint8_t)byte : NV ? (uint8_t)0 : (uint8_t)21;
     uint32_t p[2][4]; // two values' codes, a byte a digit: digits 7..4, 3..0
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
         uint32_t u = __float_as_uint(fmaf(v[i], unit, kMagic)) - __float_as_uint(kMagic);
-        if constexpr (NV) { // the digit of scale 2^-9 is digit 6, digit 7 is 0
-            u += 4u * 01111110u / 2u + 2u;
-            u = (u & ~3u) << 4 | ((u & 3u) + 2u) << 3 | 4u;
-        } else {
-            u = bad ? kDigits : u + kDigits;
-        }
+        u = bad ? kDigits : u + kDigits;
         u += (u & 0xFFF000u) * 15u; // 3-bit fields to nibbles: halves to 16 bits,
         u += (u & 0x0FC00FC0u) * 3u; // six bits to bytes,
         u += u & 0x38383838u;
         const uint32_t lo = i & 1 ? 0xA0C0D0E0u : 0x0A0C0D0Eu, hi = i & 1 ? 0x50402000u : 0x05040200u;
-        const uint32_t a = __byte_perm(lo, hi, u), b = __byte_perm(lo, hi, u >> 16);
+        const uint32_t a = __byte_perm(lo, hi, u), b4 = __byte_perm(lo, hi, u >> 16);
         p[0][i >> 1] = i & 1 ? p[0][i >> 1] | a : a;
-        p[1][i >> 1] = i & 1 ? p[1][i >> 1] | b : b;
+        p[1][i >> 1] = i & 1 ? p[1][i >> 1] | b4 : b4;
     }
-    codes += c0 >> 1;
+    codes += (c0 >> 8) * kTileBytes + ((c0 & 255) >> 1);
 #pragma unroll
     for (int h = 0; h < 2; ++h) { // four bytes of four words -> four words of one digit each
         const uint32_t t0 = __byte_perm(p[h][0], p[h][1], 0x5140);
@@ -398,38 +404,37 @@ __device__ __forceinline__ void put_terms(const float (&v)[8], int64_t c0, int64
 #pragma unroll
         for (int i = 0; i < 4; ++i)
             if (on)
-                *reinterpret_cast<uint32_t *>(codes + (7 - 4 * h - i) * (cols >> 1)) = w[i];
+                *reinterpret_cast<uint32_t *>(codes + (7 - 4 * h - i) * 128) = w[i];
     }
 }
 
-// Scale bytes of term j of eight, four of a word of the first term's (MXFP4), or all of NVFP4's.
+// Scale bytes of term j of eight, four of a word of the first term's (MXFP4).
 __device__ __forceinline__ uint32_t mx_term_scales(uint32_t first, int j)
 {
     return first - 0x03030303u * (uint32_t)j;
 }
 
-__device__ __forceinline__ uint32_t nv_term_scales(int j)
+// A token's product from its eight columns' sums, the smallest terms first. (NVFP4: in units of
+// row_factor; term j counts 8^-j, an exact factor.)
+template <bool NV> __device__ __forceinline__ float term_sum(const uint32_t (&v)[kTerms])
 {
-    // E4M3 of 2^8, 2^5, 2^2, 2^-1, 2^-4, 2^-7, 2^-9, 2^-9
-    const uint64_t all = 0x0101041830486078ull;
-    return (uint32_t)(all >> (8 * j) & 0xFFu) * 0x01010101u;
+    float s = 0.0f;
+#pragma unroll
+    for (int j = kTerms - 1; j >= 0; --j)
+        s = NV ? fmaf(s, 0.125f, __uint_as_float(v[j])) : s + __uint_as_float(v[j]);
+    return s;
 }
 
-// The power of two that a row with the largest magnitude m (bits) is divided by: kept where both it
-// and its inverse are normal.
+// R + 127 of a row with the largest magnitude m (bits), and what its first column is multiplied by,
+// 2^(R - 8) (NaN where m is NaN or infinite).
 __device__ __forceinline__ uint32_t row_exponent(uint32_t m)
 {
-    return (uint32_t)min(max((int)(m >> 23) - 8, 1), 253);
-}
-
-__device__ __forceinline__ float row_inverse(uint32_t m)
-{
-    return __uint_as_float((254u - row_exponent(m)) << 23);
+    return min(max(m >> 23, 21u), 254u);
 }
 
 __device__ __forceinline__ float row_factor(uint32_t m)
 {
-    return __uint_as_float(m >= 0x7F800000u ? 0x7FC00000u : row_exponent(m) << 23);
+    return __uint_as_float(m >= 0x7F800000u ? 0x7FC00000u : (row_exponent(m) - 8u) << 23);
 }
 
 // A CTA's share of the rows' 256-value chunks, one warp each.
@@ -445,10 +450,12 @@ struct MoeChunks {
     }
 };
 
-// Terms of the CTA's chunks, by all warps but warp 0; load(row, c0, v): eight values.
-template <bool NV, typename Load>
+// Terms of the CTA's chunks, by all warps but warp 0; load(row, c0, v): eight values; row_e(row):
+// the row's exponent (NVFP4). A chunk's values may lie where its terms go.
+template <bool NV, typename Load, typename RowE>
 __device__ __forceinline__ void write_terms(const MoeChunks &ch, int64_t cols, uint8_t *codes,
-                                            uint8_t *scales, int64_t pitch, int warp, Load load)
+                                            uint8_t *scales, int64_t kt, int warp, Load load,
+                                            RowE row_e)
 {
     const int lane = threadIdx.x & 31;
     if (warp == 0)
@@ -458,8 +465,9 @@ __device__ __forceinline__ void write_terms(const MoeChunks &ch, int64_t cols, u
         float v[8] = {};
         if (c0 < cols)
             load(row, c0, v);
-        put_terms<NV>(v, c0, cols, codes + row * kTerms * (cols >> 1), scales + row * pitch, pitch,
-                      true);
+        __syncwarp(); // every lane has its values
+        put_terms<NV>(v, c0, cols, codes + row * kt * kTileBytes,
+                      scales + row * kt * (NV ? 16 : 8), kt, true, row_e(row));
     }
 }
 
@@ -482,7 +490,7 @@ struct MoeGemm {
     const uint8_t *up_scales, *down_scales; // linear
     const float *up_gs, *down_gs;           // [E] (NVFP4)
     int stages, stage_bytes; // operand ring
-    int box;                 // term rows of a TMA box
+    int box;                 // tokens of a TMA box of terms
     int splits, blocks;      // down: CTAs per 128-row block of y, blocks
     __nv_bfloat16 *y;
     GridBarrier *barrier;
@@ -616,9 +624,10 @@ __device__ __noinline__ void fetch_scales_general(uint32_t dst, const uint8_t *s
     }
 }
 
-// 128 rows' scale bytes (SB a row at `sm`; MXFP4: less `less`) -> the TMEM columns of F::kAtoms atoms,
-// this warp's lane quarter: lane r's word i of an atom is row r + 32 i's.
-template <class F>
+// 128 rows' scale bytes (SB a row at `sm`; MXFP4: less `less`; SHARE: eight rows have one row of
+// bytes) -> the TMEM columns of F::kAtoms atoms, this warp's lane quarter: lane r's word i of an atom
+// is row r + 32 i's.
+template <class F, bool SHARE = false>
 __device__ __forceinline__ void feed_rows(const uint8_t *sm, uint32_t tcol, int lane,
                                           uint32_t less = 0u)
 {
@@ -631,7 +640,8 @@ __device__ __forceinline__ void feed_rows(const uint8_t *sm, uint32_t tcol, int 
             r[i] = v.x - less;
             r[4 + i] = v.y - less;
         } else {
-            const uint4 v = *reinterpret_cast<const uint4 *>(sm + (lane + 32 * i) * SB);
+            const int row = lane + 32 * i;
+            const uint4 v = *reinterpret_cast<const uint4 *>(sm + (SHARE ? row >> 3 : row) * SB);
             r[i] = v.x;
             r[4 + i] = v.y;
             r[8 + i] = v.z;
@@ -645,11 +655,12 @@ __device__ __forceinline__ void feed_rows(const uint8_t *sm, uint32_t tcol, int 
 }
 
 // A scale feeder thread's row: its scale bytes of every kFeeders-th k-tile, from `first` on (k-tiles
-// count on from one run into the next), into a ring of kSfRing slots of 128 rows of weights and
-// (MXFP4) 128 of terms.
+// count on from one run into the next), into a ring of kSfRing slots of 128 rows of weights and 128 of
+// terms (NVFP4: 16 of tokens, whose eight terms share their scales).
 template <class F, bool DOWN> struct ScaleRow {
     static constexpr int SB = 4 * F::kAtoms; // bytes of a row and k-tile
-    static constexpr int kSlot = (F::kMx ? 2 : 1) * 128 * SB;
+    static constexpr int kRowsPerToken = F::kMx ? kTerms : 1;
+    static constexpr int kSlot = (128 + kCols * kRowsPerToken) * SB;
     const MoeGemm &p;
     MoeWalk<DOWN> walk;
     uint32_t ring; // this row's slot 0
@@ -690,10 +701,10 @@ template <class F, bool DOWN> struct ScaleRow {
                                      : (2 * g.unit.expert + (r >> 6)) * p.F + at;
             a_on = at < (DOWN ? p.H : p.F);
             asrc = (DOWN ? p.down_scales : p.up_scales) + (a_on ? row * srow + (int64_t)kt * SB : 0);
-            b_on = r / kTerms < g.unit.ncol; // a token of the column tile
+            const int token = r / kRowsPerToken;
+            b_on = token < g.unit.ncol; // of the column tile
             bsrc = (DOWN ? p.sh.h_scales : p.sh.x_scales) +
-                   (int64_t)(g.unit.row0 + r / kTerms) * (DOWN ? p.sh.h_pitch : p.sh.x_pitch) +
-                   (int64_t)kt * SB;
+                   ((int64_t)(g.unit.row0 + token) * (DOWN ? p.sh.h_kt : p.sh.x_kt) + kt) * SB;
         }
         if (more) {
             const uint32_t dst = ring + slot * kSlot;
@@ -705,7 +716,7 @@ template <class F, bool DOWN> struct ScaleRow {
                 else
                     fetch_scales_general<SB>(dst, asrc, min(SB, srow - kt * SB));
             }
-            if (F::kMx && terms && b_on) // (the MMA reads no other columns)
+            if (terms && b_on) // (the MMA reads no other columns)
                 cp_async<SB>(dst + 128 * SB, bsrc);
             asrc += a_on ? kFeeders * SB : 0;
             bsrc += kFeeders * SB;
@@ -729,13 +740,13 @@ __device__ __forceinline__ void put_y(__nv_bfloat16 *y, const float4 &v)
 // of its own for each cost 3 to 4 us more):
 //   lists of the (expert, token) rows (every CTA its own) and the rows' terms of x;
 //   gate/up products and, for MXFP4, the terms of h, whose blocks lie in one tile;
-//   terms of h, for NVFP4, whose rows are divided by a power of two of their largest value first;
+//   terms of h, for NVFP4, whose blocks' scales are relative to their row's largest value;
 //   down products;
 //   the splits' sums of y (where a block of y is shared by several CTAs).
 // Products, on the FP4 tensor cores: 128 weight rows are the M side of block-scaled MMAs, eight term
 // rows of each token of a column tile the N side (8..128 columns), so the weights go from HBM to the
-// tensor cores as they are stored and the sum of a token's eight columns is the product with its
-// full-precision value. Roles:
+// tensor cores as they are stored and the sum of a token's eight columns is the product with its value
+// to 2^-22 of the largest of a block. Roles:
 //   warp 0       TMA producer of the weights: per 256-wide k-tile one box of 128 rows (the next
 //                phase's first stages before the barriers);
 //   warp 14      TMA producer of the term rows: a box per four tokens of the column tile;
@@ -821,18 +832,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = tmem_slot;
-    if constexpr (NV)
-        if (warp >= 6 && warp < 10) { // the terms' scales, the same in every stage
-            uint32_t w[16];
-#pragma unroll
-            for (int i = 0; i < 16; ++i)
-                w[i] = nv_term_scales(lane & 7);
-            for (int i = 0; i < p.stages; ++i)
-                tmem_st_32x32b_x16(tmem + ((uint32_t)((warp & 3) * 32) << 16) + kSfCol +
-                                       i * kSlotCols + 16, w);
-            tmem_st_wait();
-            tc_fence_before(); // (the products are several barriers away)
-        }
     pdl_wait(); // the ids, the activations
     for (int64_t i = blockIdx.x * kThreads + tid; i < p.T * (p.H >> 6); i += gridDim.x * kThreads)
         asm volatile("prefetch.global.L2 [%0];" ::"l"(p.x + i * 8)); // while the lists are built
@@ -956,9 +955,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             // ------------------------------- the term rows' TMA producer --------------------
             const CUtensorMap *tm = DOWN ? &tmH : &tmX;
             while (walk.next(gr)) {
-                const int row = gr.unit.row0 * kTerms + lane * p.box;
-                const int n = (gr.unit.ncol * kTerms + p.box - 1) / p.box;
-                const uint32_t bytes = (uint32_t)(n * p.box * 128);
+                const int row = gr.unit.row0 + lane * p.box;
+                const int n = (gr.unit.ncol + p.box - 1) / p.box;
+                const uint32_t bytes = (uint32_t)(n * p.box * kTileBytes);
                 for (int kt = gr.k0; kt < gr.k1 && !dead; ++kt) {
                     uint64_t *bar = &full_bar[stage];
                     wait(&empty_bar[stage], phase ^ 1);
@@ -969,8 +968,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                         mbar_arrive_expect_tx(bar, bytes);
                     __syncwarp();
                     if (lane < n)
-                        tma_load_3d(smem + stage * stage_bytes + 16384 + lane * p.box * 128, tm, bar,
-                                    kt * 128, row, 0);
+                        tma_load_3d(smem + stage * stage_bytes + 16384 + lane * p.box * kTileBytes,
+                                    tm, bar, 0, kt * kTerms, row);
                     __syncwarp();
                     next_stage();
                 }
@@ -1001,6 +1000,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if constexpr (F::kMx) // row r: term r % 8
                         feed_rows<F>(src + 128 * SB, tbase + stage * kSlotCols + 16, lane,
                                      mx_term_scales(0u, 0) - mx_term_scales(0u, lane & 7));
+                    else // row r: token r / 8
+                        feed_rows<F, true>(src + 128 * SB, tbase + stage * kSlotCols + 16, lane);
                     tmem_st_wait();
                     tc_fence_before();
                     __syncwarp();
@@ -1077,13 +1078,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                         for (int c = 0; c < 4; ++c) {
                             if (c0 + c >= ncol)
                                 break;
-                            float s = 0.0f; // the smallest terms first
-#pragma unroll
-                            for (int j = kTerms - 1; j >= 0; --j)
-                                s += __uint_as_float(v[c][j]);
+                            float s = term_sum<NV>(v[c]);
                             const int row = gr.unit.row0 + c0 + c;
-                            if constexpr (!F::kMx)
-                                s *= gs * row_factor(__ldcg((DOWN ? p.sh.h_max : p.sh.x_max) + row));
+                            if constexpr (NV) // (this order: the two factors' product may vanish)
+                                s = s * gs * row_factor(__ldcg((DOWN ? p.sh.h_max : p.sh.x_max) + row));
                             if constexpr (DOWN) {
                                 float *sum = s_out + (int)l.tok[row] * 128 + r;
                                 *sum = fmaf(s, l.wt[row], *sum);
@@ -1113,11 +1111,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                             h[i] = ga[i] / (1.0f + __expf(-ga[i])) * ga[64 + i];
                     }
                     if constexpr (F::kMx) {
-                        uint8_t *sc = p.sh.h_scales + row * p.sh.h_pitch;
-                        put_terms<false>(h, col, p.F, p.sh.h_codes + row * kTerms * (p.F >> 1), sc,
-                                         p.sh.h_pitch, c < ncol);
+                        uint8_t *sc = p.sh.h_scales + row * p.sh.h_kt * SB;
+                        put_terms<false>(h, col, p.F, p.sh.h_codes + row * p.sh.h_kt * kTileBytes, sc,
+                                         p.sh.h_kt, c < ncol, 0u);
                         if (c < ncol && gr.first + kUpRows >= p.F) // finite scales behind the row
-                            for (int64_t b = (gr.first + kUpRows) / 32 + (et & 7); b < p.sh.h_pitch;
+                            for (int64_t b = (gr.first + kUpRows) / 32 + (et & 7); b < p.sh.h_kt * SB;
                                  b += 8)
                                 sc[b] = 21;
                     } else {
@@ -1129,7 +1127,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                         for (int o = 1; o < 8; o <<= 1)
                             m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
                         if (on) {
-                            float4 *dst = reinterpret_cast<float4 *>(p.sh.h + row * p.F + col);
+                            float4 *dst = reinterpret_cast<float4 *>(
+                                p.sh.h_codes + row * p.sh.h_kt * kTileBytes + col * 4);
                             dst[0] = make_float4(h[0], h[1], h[2], h[3]);
                             dst[1] = make_float4(h[4], h[5], h[6], h[7]);
                         }
@@ -1185,37 +1184,38 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
             __syncthreads();
         }
-        write_terms<NV>(ch, p.H, p.sh.x_codes, p.sh.x_scales, p.sh.x_pitch, warp,
+        write_terms<NV>(ch, p.H, p.sh.x_codes, p.sh.x_scales, p.sh.x_kt, warp,
                         [&](int64_t row, int64_t c0, float(&v)[8]) {
                             const int t = l.tok[row];
                             const uint4 u = __ldg(p.x + ((t * p.H + c0) >> 3));
                             const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-                            const float f = NV ? row_inverse(s_max[t]) : 1.0f;
 #pragma unroll
                             for (int i = 0; i < 4; ++i) {
-                                v[2 * i] = __uint_as_float(w[i] << 16) * f;
-                                v[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u) * f;
+                                v[2 * i] = __uint_as_float(w[i] << 16);
+                                v[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
                             }
                             if (NV && c0 == 0)
                                 p.sh.x_max[row] = s_max[t];
-                        });
+                        },
+                        [&](int64_t row) { return NV ? row_exponent(s_max[l.tok[row]]) : 0u; });
     }
     grid_sync(); // the terms of x
     products(kUp);
     start(kDown);
     grid_sync(); // h
     if constexpr (NV) {
-        write_terms<NV>(MoeChunks(n_rows, p.F), p.F, p.sh.h_codes, p.sh.h_scales, p.sh.h_pitch,
-                        warp, [&](int64_t row, int64_t c0, float(&v)[8]) {
-                            const float4 *src =
-                                reinterpret_cast<const float4 *>(p.sh.h + row * p.F + c0);
+        write_terms<NV>(MoeChunks(n_rows, p.F), p.F, p.sh.h_codes, p.sh.h_scales, p.sh.h_kt,
+                        warp,
+                        [&](int64_t row, int64_t c0, float(&v)[8]) {
+                            const float4 *src = reinterpret_cast<const float4 *>(
+                                p.sh.h_codes + row * p.sh.h_kt * kTileBytes + c0 * 4);
                             const float4 a = __ldcg(src), b = __ldcg(src + 1);
-                            const float f = row_inverse(__ldcg(p.sh.h_max + row));
                             const float u[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
 #pragma unroll
                             for (int i = 0; i < 8; ++i)
-                                v[i] = u[i] * f;
-                        });
+                                v[i] = u[i];
+                        },
+                        [&](int64_t row) { return row_exponent(__ldcg(p.sh.h_max + row)); });
         grid_sync(); // the terms of h
     }
     products(kDown);
@@ -1269,7 +1269,7 @@ int moe_splits(int64_t H)
 
 // The workspace: offsets of MoeShared's arrays for T tokens of k experts.
 struct MoeWs {
-    size_t x_codes, x_scales, x_max, h, h_codes, h_scales, h_max, partial, total;
+    size_t x_codes, x_scales, x_max, h_codes, h_scales, h_max, partial, total;
 };
 
 MoeWs moe_ws(int64_t T, int64_t k, int64_t F, int64_t H)
@@ -1282,13 +1282,13 @@ MoeWs moe_ws(int64_t T, int64_t k, int64_t F, int64_t H)
     };
     const size_t n = (size_t)T * (size_t)k, blocks = (size_t)((H + kDownRows - 1) / kDownRows);
     const int splits = moe_splits(H);
-    MoeWs w; // (what either format needs)
-    w.x_codes = take(n * kTerms * (size_t)H / 2);
-    w.x_scales = take(n * (size_t)((H + 255) / 256 * 8));
+    const size_t x_kt = (size_t)(H + 255) / 256, h_kt = (size_t)(F + 255) / 256;
+    MoeWs w; // (of either format: MXFP4 has half the scales and no maxima)
+    w.x_codes = take(n * x_kt * kTileBytes);
+    w.x_scales = take(n * x_kt * 16);
     w.x_max = take(n * 4);
-    w.h = take(n * (size_t)F * 4);
-    w.h_codes = take(n * kTerms * (size_t)F / 2);
-    w.h_scales = take(n * (size_t)((F + 255) / 256 * 8));
+    w.h_codes = take(n * h_kt * kTileBytes);
+    w.h_scales = take(n * h_kt * 16);
     w.h_max = take(n * 4);
     w.partial = take(splits > 1 ? blocks * splits * (size_t)T * kDownRows * 4 : 0);
     w.total = at;
@@ -1299,18 +1299,18 @@ template <class F>
 cudaError_t launch_experts(MoeGemm g, const uint8_t *up_codes, const uint8_t *down_codes,
                            cudaStream_t s)
 {
-    // scale bytes of a row (MXFP4): whole k-tiles
-    g.sh.x_pitch = (g.H + 255) / 256 * 8;
-    g.sh.h_pitch = (g.F + 255) / 256 * 8;
-    const int cols = g.T < kCols ? g.T : kCols, per = cols < 4 ? cols : 4; // tokens: a stage, a box
-    g.box = per * kTerms;
-    g.stage_bytes = 16384 + (cols + per - 1) / per * g.box * 128;
+    g.sh.x_kt = (g.H + 255) / 256;
+    g.sh.h_kt = (g.F + 255) / 256;
+    const int cols = g.T < kCols ? g.T : kCols; // tokens of a stage
+    g.box = cols < 4 ? cols : 4;
+    g.stage_bytes = 16384 + (cols + g.box - 1) / g.box * g.box * kTileBytes;
     CUtensorMap up, down, xt, ht;
     const int64_t n = (int64_t)g.T * g.k;
     if (!make_fp4_codes_map(&up, up_codes, 2 * g.E, g.F, g.H, 2, kUpRows) ||
         !make_fp4_codes_map(&down, down_codes, g.E, g.H, g.F, 1, kDownRows) ||
-        !make_fp4_codes_map(&xt, g.sh.x_codes, 1, n * kTerms, g.H, 1, g.box) ||
-        !make_fp4_codes_map(&ht, g.sh.h_codes, 1, n * kTerms, g.F, 1, g.box))
+        // the terms, a row's k-tiles of 8 x 128 bytes: a box is one k-tile of g.box rows
+        !make_fp4_codes_map(&xt, g.sh.x_codes, n, g.sh.x_kt * kTerms, 256, g.box, kTerms) ||
+        !make_fp4_codes_map(&ht, g.sh.h_codes, n, g.sh.h_kt * kTerms, 256, g.box, kTerms))
         return cudaErrorInvalidValue;
     static std::once_flag flags[64];
     int dev = 0;
@@ -1380,7 +1380,7 @@ cudaError_t launch_moe_experts(const void *x, int64_t T, int64_t H, int64_t F, i
     MoeGemm g{};
     auto u32 = [&](size_t o) { return reinterpret_cast<uint32_t *>(b + o); };
     g.sh = MoeShared{b + w.x_codes, b + w.h_codes, b + w.x_scales, b + w.h_scales, 0, 0,
-                     u32(w.x_max), u32(w.h_max), f32(w.h), f32(w.partial)};
+                     u32(w.x_max), u32(w.h_max), f32(w.partial)};
     g.x = reinterpret_cast<const uint4 *>(x);
     g.ids = ids;
     g.weights = weights;
