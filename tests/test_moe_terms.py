@@ -9,7 +9,7 @@ import nvfp4_block_scaled_14_b200 as nv
 import test_moe as M
 
 TERMS = 8
-FORMATS = ["nvfp4"]
+FORMATS = ["mxfp4", "nvfp4"]
 
 
 def split(v, block, reach):
@@ -107,7 +107,7 @@ def test_each_call_hangs_on_its_digit(fmt, j):
         assert not np.array_equal(compute(x, up, down, fmt, **{name: j}), y)
 
 
-@pytest.mark.parametrize("fmt,block,reach", [("nvfp4", 16, 17)])
+@pytest.mark.parametrize("fmt,block,reach", [("mxfp4", 32, 300), ("nvfp4", 16, 17)])
 def test_split_keeps_the_bound(fmt, block, reach):
     g = np.random.default_rng(3)
     for _ in range(50):
