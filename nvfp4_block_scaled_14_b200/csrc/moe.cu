@@ -1108,7 +1108,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                         const float *ga = s_out + c * 128 + f;
 #pragma unroll
                         for (int i = 0; i < 8; ++i)
-                            h[i] = ga[i] / (1.0f + __expf(-ga[i])) * ga[64 + i];
+                            // (expf: the fast form loses bits with the gate, up to 2^-17 at -70)
+                            h[i] = ga[i] / (1.0f + expf(-ga[i])) * ga[64 + i];
                     }
                     if constexpr (F::kMx) {
                         uint8_t *sc = p.sh.h_scales + row * p.sh.h_kt * SB;

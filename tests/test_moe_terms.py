@@ -191,3 +191,91 @@ def test_experts_within_their_formats_bound(cuda, monkeypatch, T, H, F, E, k, fm
     x[:, 1] = spike
     ids, p = M.some_ids(T, k, E, 4)
     M.check_experts(x.bfloat16(), ids, p, up, down)
+
+
+# ---- silu far below zero ----------------------------------------------------------------------
+#
+# Pairs of hidden values that almost cancel in y: h_a = silu(a) u_a and h_b = silu(b) u_b with gates
+# near -72 and u_b taken to 16 bits such that h_b = h_a (1 + 2^-14). y = h_a - h_b shows errors of
+# silu that are 2^-14 of what they are to y alone.
+
+PAIRS, TOKENS = 16, 16
+
+
+def silu_pairs(seed):
+    """x [TOKENS, H] (all of bf16), gate_up, down, and with what of x: a, b, u_a, u_b, [TOKENS, PAIRS]."""
+    g = np.random.default_rng(seed)
+    bf = lambda v: torch.from_numpy(v).bfloat16().double().numpy()  # noqa: E731
+    x = np.zeros((TOKENS, 128))
+    x[:, :32] = 12.0 + g.integers(-2, 3, (TOKENS, 32)) / 16.0
+    a, b = -6.0 * x[:, 0:32:2], -6.0 * x[:, 1:32:2]
+    silu = lambda v: v / (1.0 + np.exp(-v))  # noqa: E731
+    u_a = bf(np.exp2(20.0 + g.random((TOKENS, PAIRS))))
+    u_b = silu(a) * u_a / silu(b) * (1.0 + 2.0 ** -14)
+    hi = bf(u_b)
+    lo = bf(u_b - hi)
+    x[:, 32:48], x[:, 64:80], x[:, 96:112] = u_a, hi, lo
+    up = np.zeros((64, 128))
+    for q in range(PAIRS):
+        up[2 * q, 2 * q] = up[2 * q + 1, 2 * q + 1] = -6.0
+        up[32 + 2 * q, 32 + q] = up[33 + 2 * q, 64 + q] = up[33 + 2 * q, 96 + q] = 1.0
+    down = np.zeros((128, 32))
+    for q in range(PAIRS):
+        down[q, 2 * q], down[q, 2 * q + 1] = 1.0, -1.0
+    return x, up, down, (a, b, u_a, hi + lo)
+
+
+def check_silu_pairs(y, parts, fmt):
+    """y [TOKENS, PAIRS] against 64 bits. The products before silu are exact sums of few digits. Each
+    hidden value: expf (1 unit in the last place, 2^-23), the sum, the division and the product with u
+    (half of one each): 5 * 2^-24, and u itself, exact or rounded once: 2^-24. The terms leave 2^-22 of
+    the block's largest of either value; the sum of two values' digits is exact in each column and the
+    columns' sum is off by less than 2^-20 of y; y is rounded to bf16 once."""
+    a, b, u_a, u_b = parts
+    h = np.stack([a / (1.0 + np.exp(-a)) * u_a, b / (1.0 + np.exp(-b)) * u_b], -1)  # [T, q, 2]
+    y_ref = h[..., 0] - h[..., 1]
+    size = np.abs(h)
+    block = size.reshape(TOKENS, -1, 16 if fmt == "nvfp4" else 32)
+    top = block.max(-1, keepdims=True).repeat(block.shape[-1], -1).reshape(size.shape)
+    err = (6 * 2.0 ** -24 * size + 2.0 ** -22 * top).sum(-1) + 2.0 ** -20 * np.abs(y_ref)
+    tol = err + 2.0 ** -8 * (np.abs(y_ref) + err)
+    return np.abs(y - y_ref) / tol
+
+
+def single_silu(v, exp):
+    e = exp(-v.astype(np.float32))
+    return v.astype(np.float32) / (np.float32(1.0) + e)
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+def test_silu_check_tells_a_short_exponential(fmt):
+    exact = lambda v: np.exp(v.astype(np.float64)).astype(np.float32)  # noqa: E731
+    # exp as 2^(v log2 e) with the product rounded to fp32
+    short = lambda v: np.exp2((v * np.float32(np.log2(np.e))).astype(np.float64)).astype(  # noqa: E731
+        np.float32)
+    x, up, down, parts = silu_pairs(1)
+    assert torch.equal(torch.from_numpy(x).bfloat16().double(), torch.from_numpy(x))
+    worst = {}
+    for name, exp in (("exact", exact), ("short", short)):
+        a, b, u_a, u_b = parts
+        h = np.stack([single_silu(a, exp) * u_a.astype(np.float32),
+                      single_silu(b, exp) * u_b.astype(np.float32)], -1).reshape(TOKENS, -1)
+        h = np.stack([terms_of(r, fmt).sum(0) for r in h]).reshape(TOKENS, PAIRS, 2)
+        y = torch.from_numpy(h[..., 0] - h[..., 1]).bfloat16().double().numpy()
+        worst[name] = check_silu_pairs(y, parts, fmt).max()
+    assert worst["exact"] <= 1.0 and worst["short"] > 1.5, worst
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("seed", [1, 2])
+def test_silu_far_below_zero(cuda, fmt, seed):
+    x, up, down, parts = silu_pairs(seed)
+    y = nv.moe_experts(torch.from_numpy(x).bfloat16().cuda(),
+                       torch.zeros(TOKENS, 1, dtype=torch.int32, device="cuda"),
+                       torch.ones(TOKENS, 1, device="cuda"), as_experts(up, fmt),
+                       as_experts(down, fmt))
+    y = y.double().cpu().numpy()
+    assert (y[:, PAIRS:] == 0).all()
+    off = check_silu_pairs(y[:, :PAIRS], parts, fmt)
+    assert (off <= 1.0).all(), float(off.max())
