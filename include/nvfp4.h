@@ -501,6 +501,23 @@ nvfp4_status nvfp4_selftest_grid_exchange(int nblk, const float *vals, int skip_
                                           cudaStream_t stream);
 
 /*
+ * Test of the give-up path of nvfp4_moe_experts. The same call with poll limits of the caller's: its
+ * waits give up after wait_limit rounds (0: at once), its grid barriers after barrier_limit, and CTA
+ * absent_cta (-1: none) stays away from the barriers. A call in which a wait gave up records
+ * NVFP4_ERR_TIMEOUT in the status word and returns after about one limit, y undefined: a CTA that gave
+ * up enters no later barrier. The limits are at most the library's own (1 << 20, 1 << 21).
+ * Returns the launch status.
+ */
+nvfp4_status nvfp4_selftest_moe_experts(const void *x_bf16, int64_t T, int64_t H, int64_t F,
+                                        int64_t E, int64_t top_k, const int32_t *ids,
+                                        const float *weights, int format, const uint8_t *up_codes,
+                                        const uint8_t *up_scales, const float *up_gs,
+                                        const uint8_t *down_codes, const uint8_t *down_scales,
+                                        const float *down_gs, void *y_bf16, void *ws,
+                                        size_t ws_bytes, int absent_cta, uint32_t wait_limit,
+                                        uint32_t barrier_limit, cudaStream_t stream);
+
+/*
  * Synchronize the stream, then report and clear the library's device-side status word
  * (set by a kernel whose bounded wait gave up: NVFP4_ERR_TIMEOUT). After a timeout it also
  * resets the library's grid-barrier counters, which an exchange that gave up leaves

@@ -257,6 +257,43 @@ nvfp4_status check_linear_mx(int64_t M, int64_t N, int64_t K, nvfp4_dtype out_dt
     return NVFP4_OK;
 }
 
+// nvfp4_moe_experts, with the waits of its self-test.
+nvfp4_status moe_experts_call(const void *x_bf16, int64_t T, int64_t H, int64_t F, int64_t E,
+                              int64_t top_k, const int32_t *ids, const float *weights, int format,
+                              const uint8_t *up_codes, const uint8_t *up_scales,
+                              const float *up_gs, const uint8_t *down_codes,
+                              const uint8_t *down_scales, const float *down_gs, void *y_bf16,
+                              void *ws, size_t ws_bytes, const MoeWaits *waits,
+                              cudaStream_t stream)
+{
+    if (format != NVFP4_EXPERTS_NVFP4 && format != NVFP4_EXPERTS_MXFP4)
+        return NVFP4_ERR_INVALID_ARG;
+    if (T < 0 || T > kMoeMaxTokens || H < 32 || H >= kMaxDim || H % 32 != 0 || F < 32 ||
+        F >= kMaxDim / 2 || F % 32 != 0 || E < 1 || E > kMoeMaxExperts || top_k < 1 ||
+        top_k > kMoeMaxTopK || E * 2 * F >= kMaxDim || E * H >= kMaxDim) // (stacked rows in int32)
+        return NVFP4_ERR_SHAPE;
+    if (T == 0)
+        return NVFP4_OK;
+    const bool nv = format == NVFP4_EXPERTS_NVFP4;
+    if (!x_bf16 || !ids || !weights || !up_codes || !up_scales || !down_codes || !down_scales ||
+        !y_bf16 || (nv && (!up_gs || !down_gs)))
+        return NVFP4_ERR_INVALID_ARG;
+    if (!aligned16(x_bf16) || !aligned16(up_codes) || !aligned16(up_scales) ||
+        !aligned16(down_codes) || !aligned16(down_scales) || !aligned16(y_bf16) ||
+        !aligned16(ws) || (reinterpret_cast<uintptr_t>(ids) & 3u) ||
+        (reinterpret_cast<uintptr_t>(weights) & 3u) || (reinterpret_cast<uintptr_t>(up_gs) & 3u) ||
+        (reinterpret_cast<uintptr_t>(down_gs) & 3u))
+        return NVFP4_ERR_ALIGNMENT;
+    if (!ws || ws_bytes < moe_workspace_bytes(T, top_k, F, H))
+        return NVFP4_ERR_WORKSPACE;
+    const nvfp4_status st = check_device();
+    if (st != NVFP4_OK)
+        return st;
+    return map_cuda(launch_moe_experts(x_bf16, T, H, F, (int)E, (int)top_k, ids, weights, !nv,
+                                       up_codes, up_scales, up_gs, down_codes, down_scales,
+                                       down_gs, y_bf16, ws, waits, stream));
+}
+
 } // namespace
 
 extern "C" {
@@ -646,32 +683,9 @@ nvfp4_status nvfp4_moe_experts(const void *x_bf16, int64_t T, int64_t H, int64_t
                                const uint8_t *down_scales, const float *down_gs, void *y_bf16,
                                void *ws, size_t ws_bytes, cudaStream_t stream)
 {
-    if (format != NVFP4_EXPERTS_NVFP4 && format != NVFP4_EXPERTS_MXFP4)
-        return NVFP4_ERR_INVALID_ARG;
-    if (T < 0 || T > kMoeMaxTokens || H < 32 || H >= kMaxDim || H % 32 != 0 || F < 32 ||
-        F >= kMaxDim / 2 || F % 32 != 0 || E < 1 || E > kMoeMaxExperts || top_k < 1 ||
-        top_k > kMoeMaxTopK || E * 2 * F >= kMaxDim || E * H >= kMaxDim) // (stacked rows in int32)
-        return NVFP4_ERR_SHAPE;
-    if (T == 0)
-        return NVFP4_OK;
-    const bool nv = format == NVFP4_EXPERTS_NVFP4;
-    if (!x_bf16 || !ids || !weights || !up_codes || !up_scales || !down_codes || !down_scales ||
-        !y_bf16 || (nv && (!up_gs || !down_gs)))
-        return NVFP4_ERR_INVALID_ARG;
-    if (!aligned16(x_bf16) || !aligned16(up_codes) || !aligned16(up_scales) ||
-        !aligned16(down_codes) || !aligned16(down_scales) || !aligned16(y_bf16) ||
-        !aligned16(ws) || (reinterpret_cast<uintptr_t>(ids) & 3u) ||
-        (reinterpret_cast<uintptr_t>(weights) & 3u) || (reinterpret_cast<uintptr_t>(up_gs) & 3u) ||
-        (reinterpret_cast<uintptr_t>(down_gs) & 3u))
-        return NVFP4_ERR_ALIGNMENT;
-    if (!ws || ws_bytes < moe_workspace_bytes(T, top_k, F, H))
-        return NVFP4_ERR_WORKSPACE;
-    const nvfp4_status st = check_device();
-    if (st != NVFP4_OK)
-        return st;
-    return map_cuda(launch_moe_experts(x_bf16, T, H, F, (int)E, (int)top_k, ids, weights, !nv,
-                                       up_codes, up_scales, up_gs, down_codes, down_scales,
-                                       down_gs, y_bf16, ws, stream));
+    return moe_experts_call(x_bf16, T, H, F, E, top_k, ids, weights, format, up_codes, up_scales,
+                            up_gs, down_codes, down_scales, down_gs, y_bf16, ws, ws_bytes, nullptr,
+                            stream);
 }
 
 nvfp4_status nvfp4_calib_percentile_amax(const void *const *batches, int num_batches,
@@ -847,6 +861,24 @@ nvfp4_status nvfp4_selftest_grid_exchange(int nblk, const float *vals, int skip_
         return NVFP4_ERR_WORKSPACE;
     return map_cuda(launch_exchange_selftest(nblk, vals, skip_cta, late_cta, late_ns, poll_limit,
                                              out, ws, stream));
+}
+
+nvfp4_status nvfp4_selftest_moe_experts(const void *x_bf16, int64_t T, int64_t H, int64_t F,
+                                        int64_t E, int64_t top_k, const int32_t *ids,
+                                        const float *weights, int format, const uint8_t *up_codes,
+                                        const uint8_t *up_scales, const float *up_gs,
+                                        const uint8_t *down_codes, const uint8_t *down_scales,
+                                        const float *down_gs, void *y_bf16, void *ws,
+                                        size_t ws_bytes, int absent_cta, uint32_t wait_limit,
+                                        uint32_t barrier_limit, cudaStream_t stream)
+{
+    if (absent_cta < -1 || wait_limit > kMoeWaits.wait_limit ||
+        barrier_limit > kMoeWaits.barrier_limit)
+        return NVFP4_ERR_INVALID_ARG;
+    const MoeWaits waits{wait_limit, barrier_limit, absent_cta};
+    return moe_experts_call(x_bf16, T, H, F, E, top_k, ids, weights, format, up_codes, up_scales,
+                            up_gs, down_codes, down_scales, down_gs, y_bf16, ws, ws_bytes, &waits,
+                            stream);
 }
 
 nvfp4_status nvfp4_sync_status(cudaStream_t stream)

@@ -473,8 +473,7 @@ __device__ __forceinline__ void write_terms(const MoeChunks &ch, int64_t cols, u
 
 // ---- products -----------------------------------------------------------------------------
 
-constexpr uint32_t kBarrierLimit = 1u << 21;
-constexpr uint32_t kWaitLimit = 1u << 20;
+constexpr uint32_t kWaitLimit = kMoeWaits.wait_limit;
 constexpr int kSfAhead = 2;  // a feeder group's k-tiles whose scales are on their way
 constexpr int kSfRing = kSfAhead + 1;
 constexpr int kMaxStages = 8;
@@ -495,6 +494,7 @@ struct MoeGemm {
     __nv_bfloat16 *y;
     GridBarrier *barrier;
     int *status;
+    MoeWaits waits;
 };
 
 // A run of k-tiles of one tile, whose sums stay in one accumulator.
@@ -769,8 +769,10 @@ __device__ __forceinline__ void put_y(__nv_bfloat16 *y, const float4 &v)
 // wait is 95 cycles, four MMAs and a commit 300) leaves little of that; with all weights in L2 the
 // whole call still takes 63 us, and separate rings for weights and terms, with a second wait and
 // commit a step, took 77. So a role is a warp of its own with few instructions a step, and in a group
-// of warps one polls while the others sleep at a named barrier. Waits are bounded; after one that gave
-// up the roles run on without waiting, no further copies are issued, and the status word says so.
+// of warps one polls while the others sleep at a named barrier. Waits are bounded. The first that gives
+// up tells the CTA (s_dead) and the status word: no further tiles are copied and no stage completes any
+// more, each other role stops waiting once one wait of its own has run out or at the next grid barrier,
+// which the CTA does not enter any more, so that a call ends after about one limit.
 template <class F>
 __global__ void __launch_bounds__(kThreads, 1)
     moe_experts_kernel(const __grid_constant__ CUtensorMap tmUp,
@@ -789,6 +791,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     __shared__ int s_counts[2];
     __shared__ uint32_t s_max[kMoeMaxTokens];
     __shared__ MoeStart s_start;
+    __shared__ volatile int s_dead; // a wait of this CTA gave up
     const int tid = threadIdx.x, lane = tid & 31;
     // the same in every lane, and known to be: the roles' loops then run on uniform registers
     const int warp = __shfl_sync(0xFFFFFFFFu, tid >> 5, 0);
@@ -817,6 +820,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         mbar_init(&drain_bar, 1);
         fence_barrier_init();
+        s_dead = 0;
     }
     if (tid == kThreads - 1) {
         tma_prefetch_desc(&tmUp);
@@ -836,13 +840,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int64_t i = blockIdx.x * kThreads + tid; i < p.T * (p.H >> 6); i += gridDim.x * kThreads)
         asm volatile("prefetch.global.L2 [%0];" ::"l"(p.x + i * 8)); // while the lists are built
 
-    bool dead = false; // a wait gave up: run on without waiting
+    bool dead = false; // this thread waits no more
     auto give_up = [&]() {
         dead = true;
+        s_dead = 1;
         atomicExch(p.status, (int)NVFP4_ERR_TIMEOUT);
     };
     auto wait = [&](uint64_t *bar, uint32_t parity) {
-        if (!dead && !mbar_wait(bar, parity, kWaitLimit))
+        if (!dead && !mbar_wait(bar, parity, p.waits.wait_limit))
             give_up();
     };
     // Every CTA's writes so far are visible to every CTA, to its TMA loads too. Warp 0 has weights on
@@ -852,9 +857,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (warp != 0)
             asm volatile("fence.proxy.async;" ::: "memory");
         __syncthreads();
-        if (tid == 32 && !grid_barrier_sync(p.barrier, (int)gridDim.x, (int)blockIdx.x, kBarrierLimit))
+        // (A dead CTA stays away: its arrival would complete, for CTAs still polling, the barrier that
+        // it gave up at.)
+        if (tid == 32 && !s_dead && (int)blockIdx.x != p.waits.absent &&
+            !grid_barrier_sync(p.barrier, (int)gridDim.x, (int)blockIdx.x, p.waits.barrier_limit))
             give_up();
         __syncthreads();
+        dead = s_dead != 0;
         if (warp != 0)
             asm volatile("fence.proxy.async;" ::: "memory");
     };
@@ -915,7 +924,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     continue;
                 uint64_t *bar = &full_bar[stage];
                 wait(&empty_bar[stage], phase ^ 1);
-                dead = __any_sync(0xFFFFFFFFu, dead);
+                dead = __any_sync(0xFFFFFFFFu, s_dead != 0);
                 if (dead)
                     return n;
                 if (elect_one()) {
@@ -961,7 +970,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 for (int kt = gr.k0; kt < gr.k1 && !dead; ++kt) {
                     uint64_t *bar = &full_bar[stage];
                     wait(&empty_bar[stage], phase ^ 1);
-                    dead = __any_sync(0xFFFFFFFFu, dead);
+                    dead = __any_sync(0xFFFFFFFFu, s_dead != 0);
                     if (dead)
                         break;
                     if (lane == 0)
@@ -994,6 +1003,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (q == 2) // one warp of the group polls, the others sleep at the barrier
                         wait(&empty_bar[stage], phase ^ 1);
                     named_bar_sync(3 + group, 128); // the rows are here, the last ones read
+                    const bool live = s_dead == 0;
                     tc_fence_after();
                     const uint8_t *src = my_ring + rslot * kSfRows;
                     feed_rows<F>(src, tbase + stage * kSlotCols, lane);
@@ -1005,7 +1015,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                     tmem_st_wait();
                     tc_fence_before();
                     __syncwarp();
-                    if (lane == 0)
+                    // (once dead, the stage may still lack bytes of its last use: no arrival beyond)
+                    if (lane == 0 && live)
                         mbar_arrive(&full_bar[stage]);
                     row.load(true, true);
                     rslot = rslot + 1 == kSfRing ? 0 : rslot + 1;
@@ -1249,7 +1260,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         __syncwarp();
     }
     tc_fence_before();
-    if (__syncthreads_or(dead)) { // copies of a run that was given up land within microseconds
+    if (__syncthreads_or(dead || s_dead)) { // copies of a run that was given up land within microseconds
         for (int i = 0; i < 1000; ++i)
             __nanosleep(1000);
     }
@@ -1373,7 +1384,7 @@ cudaError_t launch_moe_experts(const void *x, int64_t T, int64_t H, int64_t F, i
                                const uint8_t *up_codes, const uint8_t *up_scales,
                                const float *up_gs, const uint8_t *down_codes,
                                const uint8_t *down_scales, const float *down_gs, void *y, void *ws,
-                               cudaStream_t s)
+                               const MoeWaits *waits, cudaStream_t s)
 {
     const MoeWs w = moe_ws(T, k, F, H);
     uint8_t *b = reinterpret_cast<uint8_t *>(ws);
@@ -1397,6 +1408,7 @@ cudaError_t launch_moe_experts(const void *x, int64_t T, int64_t H, int64_t F, i
     g.splits = moe_splits(H);
     g.blocks = (int)((H + kDownRows - 1) / kDownRows);
     g.y = reinterpret_cast<__nv_bfloat16 *>(y);
+    g.waits = waits ? *waits : kMoeWaits;
     g.barrier = grid_barrier_for(s);
     g.status = device_status_ptr();
     if (!g.status || !g.barrier)

@@ -158,6 +158,13 @@ cudaError_t launch_dequantize_mx(const uint8_t *codes, const uint8_t *lin, int64
 
 // ---- moe.cu --------------------------------------------------------------------------
 constexpr int64_t kMoeMaxTokens = 64, kMoeMaxExperts = 512, kMoeMaxTopK = 32;
+// Poll rounds of the experts' waits and grid barriers; absent: a CTA that stays away from the barriers
+// (-1: none; the self-test).
+struct MoeWaits {
+    uint32_t wait_limit, barrier_limit;
+    int absent;
+};
+constexpr MoeWaits kMoeWaits{1u << 20, 1u << 21, -1};
 size_t moe_workspace_bytes(int64_t T, int64_t k, int64_t F, int64_t H);
 cudaError_t launch_moe_route(const void *x, const void *w, const float *bias, int64_t T, int64_t H,
                              int E, int k, int renorm, int *ids, float *weights, cudaStream_t s);
@@ -166,7 +173,7 @@ cudaError_t launch_moe_experts(const void *x, int64_t T, int64_t H, int64_t F, i
                                const uint8_t *up_codes, const uint8_t *up_scales,
                                const float *up_gs, const uint8_t *down_codes,
                                const uint8_t *down_scales, const float *down_gs, void *y, void *ws,
-                               cudaStream_t s);
+                               const MoeWaits *waits, cudaStream_t s); // waits: null for kMoeWaits
 
 // ---- lowrank_sm100.cu ----------------------------------------------------------------
 // bf16 [rows x cols] row-major tensor map: box 64 columns x box_rows rows, 128B swizzle.
