@@ -141,18 +141,16 @@ __global__ void __launch_bounds__(kThreads)
 #pragma unroll
         for (int i = 0; i < kPasses; ++i) {
             const int row = i * kRowsPerPass + lane_r;
+            static_assert(kVec == 2, "32 bytes a lane: a block is 2 lanes of bf16, 4 of fp32");
             constexpr int kLpb = 32 * kEsz / (16 * kVec); // lanes per block
-            const uint4 a = v[i][0], b = v[i][kVec - 1];
+            const uint4 a = v[i][0], b = v[i][1];
             uint32_t m;
             if constexpr (BF16) {
-                m = max_abs_bf16x2(max_abs_bf16x2(a.x, a.y), max_abs_bf16x2(a.z, a.w));
-                if constexpr (kVec == 2)
-                    m = max_abs_bf16x2(m, max_abs_bf16x2(max_abs_bf16x2(b.x, b.y),
-                                                         max_abs_bf16x2(b.z, b.w)));
+                m = max_abs_bf16x2(
+                    max_abs_bf16x2(max_abs_bf16x2(a.x, a.y), max_abs_bf16x2(a.z, a.w)),
+                    max_abs_bf16x2(max_abs_bf16x2(b.x, b.y), max_abs_bf16x2(b.z, b.w)));
                 m &= kAbs16x2;
                 m = max_u16x2(m, __shfl_xor_sync(0xFFFFFFFFu, m, 1));
-                if constexpr (kLpb == 4)
-                    m = max_u16x2(m, __shfl_xor_sync(0xFFFFFFFFu, m, 2));
                 m = max(m & 0xFFFFu, m >> 16) << 16;
             } else {
                 m = max(max(max(a.x & 0x7FFFFFFFu, a.y & 0x7FFFFFFFu),
@@ -168,15 +166,11 @@ __global__ void __launch_bounds__(kThreads)
             uint8_t *dst = p.codes + ((r0 + row) * p.cols + c0 + col) / 2;
             if constexpr (BF16) {
                 const uint32_t lo = mx_codes_bf16x8(a.x, a.y, a.z, a.w, inv);
-                if constexpr (kVec == 2) {
-                    const uint32_t hi = mx_codes_bf16x8(b.x, b.y, b.z, b.w, inv);
-                    if (live)
-                        *reinterpret_cast<uint2 *>(dst) =
-                            sb == kMxNan ? make_uint2(0u, 0u)
-                                         : make_uint2(flip ? hi : lo, flip ? lo : hi);
-                } else if (live) {
-                    *reinterpret_cast<uint32_t *>(dst) = sb == kMxNan ? 0u : lo;
-                }
+                const uint32_t hi = mx_codes_bf16x8(b.x, b.y, b.z, b.w, inv);
+                if (live)
+                    *reinterpret_cast<uint2 *>(dst) =
+                        sb == kMxNan ? make_uint2(0u, 0u)
+                                     : make_uint2(flip ? hi : lo, flip ? lo : hi);
             } else {
                 const uint32_t ab = mx_codes_f32x8(a, b, inv); // four codes in either half
                 const uint32_t w = flip ? __byte_perm(ab, 0u, 0x1032) : ab;
