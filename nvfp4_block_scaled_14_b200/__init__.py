@@ -439,11 +439,10 @@ def _bad_array(what, name, t, device, dtype, shape):
 
 
 def _check_array(what, name, t, device, dtype, shape):
-    """t (None: nothing to check) lies contiguous on the CUDA device, with that type and shape
-    (None: any)."""
-    if t is not None and not (isinstance(t, torch.Tensor) and t.is_cuda and t.device == device and
-                              (dtype is None or t.dtype == dtype) and
-                              (shape is None or t.shape == shape) and t.is_contiguous()):
+    """t lies contiguous on the CUDA device, with that type and shape (None: any)."""
+    if not (isinstance(t, torch.Tensor) and t.is_cuda and t.device == device and
+            (dtype is None or t.dtype == dtype) and (shape is None or t.shape == shape) and
+            t.is_contiguous()):
         _bad_array(what, name, t, device, dtype, shape)
 
 
@@ -469,6 +468,12 @@ def _check_mx(what, q, device, swizzled=False):
         if q.scales_lin is None:
             raise ValueError(f"{what} needs the linear scales")
         _check_array(what, "scales_lin", q.scales_lin, device, torch.uint8, (rows, cols // 32))
+
+
+def _codes_device(what, q):
+    if not isinstance(q.codes, torch.Tensor):
+        raise TypeError(f"{what} expects codes as a tensor")
+    return q.codes.device
 
 
 def _empty(rows, cols, dtype, device):
@@ -532,7 +537,7 @@ def dequantize_mxfp4(q: MXFP4Tensor, out_dtype=torch.float32,
     """fp32 / bf16 values of q [rows, cols] (needs its linear scales)."""
     if not isinstance(q, MXFP4Tensor):
         raise TypeError("dequantize_mxfp4 expects an MXFP4Tensor")
-    dev = q.codes.device
+    dev = _codes_device("dequantize_mxfp4", q)
     _check_mx("dequantize_mxfp4", q, dev)
     out = _mx_out("dequantize_mxfp4", out, q.rows, q.cols, out_dtype, dev)
     _launch("nvfp4_dequantize_mxfp4", dev, q.codes.data_ptr(), q.scales_lin.data_ptr(), q.rows,
@@ -548,7 +553,7 @@ def linear_mxfp4(a: MXFP4Tensor, w: MXFP4Tensor, out_dtype=torch.bfloat16,
     resident_weights: as in linear()."""
     if not isinstance(a, MXFP4Tensor):
         raise TypeError("linear_mxfp4 expects MXFP4Tensor operands")
-    dev = a.codes.device
+    dev = _codes_device("linear_mxfp4", a)
     _check_mx("linear_mxfp4", a, dev, swizzled=True)
     _check_mx("linear_mxfp4", w, dev, swizzled=True)
     if a.cols != w.cols:
@@ -631,7 +636,8 @@ def moe_route(x: torch.Tensor, w: torch.Tensor, top_k: int, bias: torch.Tensor =
     T, H = x.shape
     E = w.shape[0]
     _check_array("moe_route", "w", w, dev, None, (E, H))
-    _check_array("moe_route", "bias", bias, dev, torch.float32, (E,))
+    if bias is not None:
+        _check_array("moe_route", "bias", bias, dev, torch.float32, (E,))
     if not 1 <= top_k <= min(E, 32):
         raise ValueError("moe_route: top_k must be 1..min(experts, 32)")
     ids = _empty(T, top_k, torch.int32, dev)
@@ -659,6 +665,8 @@ def moe_experts(x: torch.Tensor, ids: torch.Tensor, weights: torch.Tensor,
         raise TypeError("moe_experts expects ExpertWeights")
     if (gate_up.global_scale is None) != (down.global_scale is None):
         raise ValueError("moe_experts: gate_up and down must have the same format")
+    if not isinstance(ids, torch.Tensor) or not isinstance(gate_up.codes, torch.Tensor):
+        raise TypeError("moe_experts expects ids and codes as tensors")
     dev = x.device
     x = x.contiguous()
     T, H = x.shape
@@ -677,11 +685,12 @@ def moe_experts(x: torch.Tensor, ids: torch.Tensor, weights: torch.Tensor,
             ("ids", ids, torch.int32, (T, k)), ("weights", weights, torch.float32, (T, k)),
             ("gate_up codes", gate_up.codes, u8, (E, 2 * F, H // 2)),
             ("gate_up scales", gate_up.scales, u8, (E, 2 * F, H // b)),
-            ("gate_up global_scale", gate_up.global_scale, torch.float32, (E,)),
             ("down codes", down.codes, u8, (E, H, F // 2)),
-            ("down scales", down.scales, u8, (E, H, F // b)),
-            ("down global_scale", down.global_scale, torch.float32, (E,))):
+            ("down scales", down.scales, u8, (E, H, F // b))):
         _check_array("moe_experts", name, t, dev, dtype, shape)
+    if not mx:
+        for name, w in (("gate_up global_scale", gate_up), ("down global_scale", down)):
+            _check_array("moe_experts", name, w.global_scale, dev, torch.float32, (E,))
     if out is None:
         out = _empty(T, H, torch.bfloat16, dev)
     else:

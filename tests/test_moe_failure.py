@@ -111,3 +111,27 @@ def test_only_the_first_barrier_is_waited_for(layer):
     assert ms < 2 * one + 3.0, (ms, one)  # 1 ms for copies in flight, and the call itself
     status, y, _ = call()
     assert status == 0 and torch.equal(y, ref)
+
+
+@pytest.mark.gpu
+def test_binding_types(cuda):
+    up, down = make_experts(2, 128, 64, "mxfp4", 1)[0], make_experts(2, 64, 64, "mxfp4", 2)[0]
+    x = torch.zeros(2, 64, device="cuda", dtype=torch.bfloat16)
+    ids, p = some_ids(2, 2, 2, 1)
+    for bad in (lambda: nv.moe_experts(x, ids.tolist(), p, up, down),
+                lambda: nv.moe_experts(x, None, p, up, down),
+                lambda: nv.moe_experts(x, ids, p, nv.ExpertWeights(None, up.scales), down)):
+        with pytest.raises(TypeError):
+            bad()
+    for bad in (lambda: nv.moe_experts(x, ids, None, up, down),
+                lambda: nv.moe_experts(x, ids, p, nv.ExpertWeights(up.codes, None), down),
+                lambda: nv.moe_experts(x, ids, p, up, nv.ExpertWeights(None, down.scales))):
+        with pytest.raises(ValueError):
+            bad()
+    q = nv.quantize_mxfp4(x)
+    for bad in (lambda: nv.linear_mxfp4(nv.MXFP4Tensor(None, q.scales_swz, None, 2, 64), q),
+                lambda: nv.dequantize_mxfp4(nv.MXFP4Tensor(None, None, None, 2, 64))):
+        with pytest.raises(TypeError):
+            bad()
+    with pytest.raises(ValueError):
+        nv.linear_mxfp4(q, nv.MXFP4Tensor(None, q.scales_swz, None, 2, 64))
