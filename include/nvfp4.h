@@ -428,6 +428,8 @@ nvfp4_status nvfp4_linear_dynamic_mxfp4(const void *x, nvfp4_dtype x_dt, const u
  *   ids[t, s]     the expert (int32);
  *   weights[t, s] its softmax weight (fp32): exp(z) over the sum of exp(z) of the chosen experts
  *                 (renormalize != 0) or of all.
+ * (Two experts whose z differ by less than the rounding of those fp32 sums, about 2^-21 of the sum of
+ * the products' sizes at most, may come in either order.)
  * A z of -infinity (a bias of -infinity shuts an expert off) or NaN is never chosen: where fewer
  * than top_k experts are left, the remaining slots hold id -1 and weight 0.
  * T: any. H: multiple of 32. E: 1..512. top_k: 1..min(E, 32). No workspace.

@@ -192,11 +192,11 @@ __global__ void __cluster_dims__(kRouteCluster, 1, 1) __launch_bounds__(kRouteTh
 
 constexpr int kTerms = 8; // FP4 terms of an activation: the rows of one swizzle atom
 // Tokens of a column tile: 128 MMA columns. An expert with more tokens streams its weights once per
-// tile (tiles of 8: 64 tokens, 64 experts of 2048 x 1024, top 8, 77 us instead of 67; larger tiles'
-// two accumulators and the scales pass TMEM).
+// tile (tiles of 8: 64 tokens, 64 experts of 2048 x 1024, top 8, 77 us where these took 67; two
+// accumulators of larger tiles and the scales pass TMEM, one would fit).
 constexpr int kCols = 16;
-// Groups of four scale-feeder warps, in turn: one takes 750 cycles a k-tile (64 tokens: 71 us instead
-// of 67), a third gives nothing (68.9 against 68.5).
+// Groups of four scale-feeder warps, in turn: one takes 750 cycles a k-tile (64 tokens: 71 us where
+// two took 67), a third gives nothing (68.9 against 68.5).
 constexpr int kFeeders = 2;
 constexpr int kThreads = 32 * (7 + 4 * kFeeders);
 constexpr int kUpRows = 64, kDownRows = 128; // rows of F, of H, per tile
@@ -761,14 +761,16 @@ __device__ __forceinline__ void put_y(__nv_bfloat16 *y, const float4 &v)
 //                sums in shared memory, which go to y or, split by split, to the workspace.
 // A stage's bytes and scales complete one barrier, and the MMAs that have read them another.
 // Measured, with the router, ids and inputs new each call: 64 tokens, 64 MXFP4 experts of 2048 x 1024,
-// top 8: 67 us (214 MB of met weights: 3.2 TB/s); 16 tokens, 28 of 32 NVFP4 experts of 4096 x 1280, top
-// 4: 72 us; one token, 6 experts of 2048 x 1408: 28 us. Of the 64 tokens' 60 us in this kernel, gate/up
-// take 26 (22 at the copy rate), down 17 (11), the rest are lists (3), terms (2.5), the barriers with
-// the wait for the slowest CTA (9) and the sums. Products are bound by HBM and by the roles' latency
+// top 8: 65 us (214 MB of met weights: 3.3 TB/s); 16 tokens, 28 of 32 NVFP4 experts of 4096 x 1280, top
+// 4: 71 us; one token, 6 experts of 2048 x 1408: 26.5 us. Of the 64 tokens' 52 us from this kernel's
+// start to its end, gate/up take 22 to 25 (22 at the copy rate), down 13 to 14 (11), the rest are lists
+// (3), terms (2.5), three barriers with the wait for the slowest CTA (10) and the sums. Products are
+// bound by HBM and by the roles' latency
 // together: a k-tile's 16 KB take 700 cycles of an SM's share, and the MMA warp's step (a completed
-// wait is 95 cycles, four MMAs and a commit 300) leaves little of that; with all weights in L2 the
-// whole call still takes 63 us, and separate rings for weights and terms, with a second wait and
-// commit a step, took 77. So a role is a warp of its own with few instructions a step, and in a group
+// wait is 95 cycles, four MMAs and a commit 300) leaves little of that; with the weights of eight
+// experts for all, which L2 holds, the whole call still takes 60 us, and separate rings for weights and
+// terms, with a second wait and commit a step, took 77 where one took 67. So a role is a warp of its own
+// with few instructions a step, and in a group
 // of warps one polls while the others sleep at a named barrier. Waits are bounded. The first that gives
 // up tells the CTA (s_dead) and the status word: no further tiles are copied and no stage completes any
 // more, each other role stops waiting once one wait of its own has run out or at the next grid barrier,
@@ -1270,9 +1272,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
 }
 
-// Jobs per 128-row block of y: as many as give every SM at most one. (Two a CTA where that leaves SMs
-// idle, 288 jobs instead of 128 for 32 blocks, costs more in sums written and read than it fills: 16
-// tokens, H 4096: 71.6 us against 72.6.)
+// Jobs per 128-row block of y: as many as give every SM at most one, whatever the number of k-tiles.
+// (Two a CTA where that leaves SMs idle, 288 jobs instead of 128 for 32 blocks, costs more in sums
+// written and read than it fills: 16 tokens, H 4096: 71.6 us against 72.6. Not measured at H above
+// 9472, where a block has one job and up to half of the SMs none.)
 int moe_splits(int64_t H)
 {
     const int64_t s = num_sms() / ((H + kDownRows - 1) / kDownRows);

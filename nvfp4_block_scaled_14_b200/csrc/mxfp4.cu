@@ -14,8 +14,11 @@
 // SM more L1: a lane's two 16-byte loads touch each sector twice, and where the second finds it gone
 // both directions take 40 us instead of 33).
 //
-// 4096 x 12288 bf16: along rows 21.0 us (6.1 TB/s), columns 23.0 us (5.5 TB/s), both 33.3 us (4.6
-// TB/s: bound by the arithmetic of both directions beside the loads, 60% of the issue slots).
+// 4096 x 12288 bf16: along rows 21.0 us (6.1 TB/s), columns 22.9 us (5.6 TB/s), both 33.2 us (4.6
+// TB/s). fp32 4096 x 8192: rows 27.3 us (5.6 TB/s), columns 33.7 us (4.5 TB/s), both 42.9 us (4.0 TB/s).
+// "Both" and fp32 columns are at neither limit (67 % of the issue slots for bf16, 36 to 49 % for fp32):
+// a CTA's loads, directions and stores follow one another, and registers (bf16) or shared memory (fp32)
+// leave an SM 4 CTAs (bf16 both), 3 (fp32 columns) or 2 (fp32 both) to overlap them.
 #include <mutex>
 
 #include "mxfp4_encode.cuh"
