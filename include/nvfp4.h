@@ -423,13 +423,12 @@ nvfp4_status nvfp4_linear_dynamic_mxfp4(const void *x, nvfp4_dtype x_dt, const u
 
 /*
  * Router of a mixture-of-experts layer: z = x . W^T + bias (x: T x H bf16, W: E x H bf16, bias:
- * E fp32 or NULL; products summed in fp32 in blocks of 32 and in fp64 above), and for
+ * E fp32 or NULL; products summed in fp32 in blocks of 32 and in fp64 above, or in fp64 throughout
+ * where that could decide which expert comes first), and for
  * each token the top_k largest z in decreasing order, equal ones by the lower expert:
  *   ids[t, s]     the expert (int32);
  *   weights[t, s] its softmax weight (fp32): exp(z) over the sum of exp(z) of the chosen experts
  *                 (renormalize != 0) or of all.
- * (Two experts whose z differ by less than the rounding of those fp32 sums, about 2^-21 of the sum of
- * the products' sizes at most, may come in either order.)
  * A z of -infinity (a bias of -infinity shuts an expert off) or NaN is never chosen: where fewer
  * than top_k experts are left, the remaining slots hold id -1 and weight 0.
  * T: any. H: multiple of 32. E: 1..512. top_k: 1..min(E, 32). No workspace.

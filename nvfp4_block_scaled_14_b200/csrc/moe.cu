@@ -30,6 +30,9 @@ namespace {
 
 constexpr int kRouteThreads = 256;
 constexpr int kRouteCluster = 8;
+// Blocks of K whose loads a warp has under way: 114 registers, two CTAs an SM. Eight: 154, one CTA (4096
+// tokens, 128 experts of 4096: 265 us instead of 162; 64 tokens 7.0 instead of 7.6). Three: 174 and 7.9 us.
+constexpr int kRouteAhead = 4;
 
 struct RouteParams {
     const uint4 *x, *w; // bf16 [T x H], [E x H]
@@ -43,6 +46,11 @@ struct RouteParams {
 __device__ __forceinline__ void st_cluster_f64(uint32_t addr, double v)
 {
     asm volatile("st.shared::cluster.f64 [%0], %1;" ::"r"(addr), "d"(v) : "memory");
+}
+
+__device__ __forceinline__ void max_cluster_u32(uint32_t addr, uint32_t v)
+{
+    asm volatile("red.relaxed.cluster.shared::cluster.max.u32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
 }
 
 // c = A B (16 x 8, K 16, bf16), and c += A B.
@@ -64,22 +72,105 @@ __device__ __forceinline__ void mma_bf16(float (&c)[4], uint32_t a0, uint32_t a1
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
+// Close calls of a token: every expert that fewer than k others precede by more than tol, and that is
+// within tol of another, gets its exact logit (products of bf16, and their sum, in fp64), and s_sel the
+// k experts in order. s_list: [E], part: [128][8]. By the whole CTA; apart from the kernel, whose
+// registers it would take.
+__device__ __noinline__ void route_close(const RouteParams &p, int64_t tk, double tol, double *s_z,
+                                         int *s_sel, int16_t *s_list, int *s_close, double *part)
+{
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int64_t nvec = p.H >> 3;
+    if (tid < 32)
+        s_sel[tid] = -1;
+    if (tid == 32)
+        *s_close = 0;
+    __syncthreads();
+    if (tol > 0.0) // (else a row of zeros: the logits are exact)
+        for (int e = tid; e < p.E; e += kRouteThreads) {
+            const double z = s_z[e], hi = z + tol, lo = z - tol;
+            int sure = 0, all = 0;
+            for (int q = 0; q < p.E; ++q) {
+                sure += s_z[q] > hi ? 1 : 0;
+                all += s_z[q] >= lo ? 1 : 0;
+            }
+            if (z > -INFINITY && sure < p.k && all - sure > 1)
+                s_list[atomicAdd(s_close, 1)] = (int16_t)e; // in any order
+        }
+    __syncthreads();
+    const int listed = *s_close;
+    for (int i0 = 0; i0 < listed; i0 += 128) {
+        const int m = min(listed - i0, 128);
+        for (int i = 0; i < m; ++i) {
+            const uint4 *x = p.x + tk * nvec, *w = p.w + s_list[i0 + i] * nvec;
+            double z = 0.0;
+#pragma unroll 2
+            for (int64_t c = tid; c < nvec; c += kRouteThreads) {
+                const uint4 a = __ldg(x + c), b = __ldg(w + c);
+                const uint32_t u[4] = {a.x, a.y, a.z, a.w}, v[4] = {b.x, b.y, b.z, b.w};
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    z = fma((double)__uint_as_float(u[j] << 16),
+                            (double)__uint_as_float(v[j] << 16), z);
+                    z = fma((double)__uint_as_float(u[j] & 0xFFFF0000u),
+                            (double)__uint_as_float(v[j] & 0xFFFF0000u), z);
+                }
+            }
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1)
+                z += __shfl_xor_sync(0xFFFFFFFFu, z, o);
+            if (lane == 0)
+                part[i * 8 + warp] = z;
+        }
+        __syncthreads();
+        if (tid < m) {
+            const int e = s_list[i0 + tid];
+            double z = 0.0;
+#pragma unroll
+            for (int w = 0; w < 8; ++w)
+                z += part[tid * 8 + w];
+            if (p.bias)
+                z += (double)__ldg(p.bias + e);
+            s_z[e] = z == z ? z : -INFINITY;
+        }
+        __syncthreads();
+    }
+    for (int e = tid; e < p.E; e += kRouteThreads) {
+        const double z = s_z[e];
+        int n = 0;
+        for (int q = 0; q < p.E; ++q)
+            n += (s_z[q] > z || (s_z[q] == z && q < e)) ? 1 : 0;
+        if (n < p.k && z > -INFINITY)
+            s_sel[n] = e;
+    }
+    __syncthreads();
+}
+
 // A cluster of 8 CTAs takes 8 tokens. Logits: 16 experts are the rows of bf16 MMAs, the tokens the
 // columns; a CTA takes chunks of 16 experts (with few chunks, a slice of K too), its warps every
 // eighth 32-wide block of K. Each block's 32 products are summed in fp32 by two MMAs and the blocks
-// in fp64, so that the choice between two close experts does not hang on the order of a long sum.
-// The logits go to the CTA that ranks the token: expert e is chosen if fewer than k experts precede
-// it, counted by every thread at once. Bound by the latency of one round of loads (W is 1 MB at 128
-// experts of 4096) and of the cluster barrier.
-__global__ void __cluster_dims__(kRouteCluster, 1, 1) __launch_bounds__(kRouteThreads)
-    moe_route_kernel(const RouteParams p)
+// in fp64; two more MMAs sum the products' sizes, S. The logits go to the CTA that ranks the token:
+// expert e is chosen if fewer than k experts precede it, counted by every thread at once. A block's two
+// MMAs are off by a unit in the last place of the sum of its sizes each, 2^-22 S a logit in all, so two
+// logits that are 2^-21 S apart (S: the token's largest) have the order of the exact ones. An expert
+// that may be chosen and is closer to another gets its sum in fp64 throughout, and the count runs again
+// (one token in 500 or so of 128 random experts of 4096).
+// Bound by the latency of one round of loads (W is 1 MB at 128 experts of 4096) and of the cluster barrier.
+__global__ void __cluster_dims__(kRouteCluster, 1, 1) __launch_bounds__(kRouteThreads, 2)
+    moe_route_kernel(const __grid_constant__ RouteParams p)
 {
     __shared__ double s_z[512];           // [slice][expert], then [expert]: this CTA's token
     __shared__ double s_part[8][16 * 8];  // [warp][expert][token]
+    __shared__ float s_size[8][16 * 8];   // as s_part: sizes
+    __shared__ uint32_t s_most[8];        // [slice]: bits of the largest size of this CTA's token
     __shared__ int s_sel[32];
+    __shared__ int s_close;               // experts of s_list
+    __shared__ int16_t s_list[512];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
     const int rank = (int)cluster_ctarank();
     const int64_t t0 = (int64_t)(blockIdx.x / kRouteCluster) * 8;
+    if (tid < 8)
+        s_most[tid] = 0u;
     cluster_arrive(); // matched below: every CTA of the cluster runs before remote stores
     const int chunks = (p.E + 15) / 16;
     const int slices = chunks == 1 ? 8 : chunks == 2 ? 4 : chunks <= 4 ? 2 : 1;
@@ -89,7 +180,7 @@ __global__ void __cluster_dims__(kRouteCluster, 1, 1) __launch_bounds__(kRouteTh
     const int nblk = (int)(p.H >> 5);
     const int b0 = (int)((int64_t)nblk * slice / slices);
     const int b1 = (int)((int64_t)nblk * (slice + 1) / slices);
-    const uint32_t zaddr = smem_u32(s_z);
+    const uint32_t zaddr = smem_u32(s_z), maddr = smem_u32(s_most);
     pdl_wait();
     const int64_t tok = t0 + g < p.T ? t0 + g : p.T - 1;
     for (int c = rank % per; c < chunks; c += per) {
@@ -97,31 +188,60 @@ __global__ void __cluster_dims__(kRouteCluster, 1, 1) __launch_bounds__(kRouteTh
         const uint4 *wb = p.w + (int64_t)min(c * 16 + g + 8, p.E - 1) * nvec + t;
         const uint4 *xr = p.x + tok * nvec + t;
         double acc[4] = {0.0, 0.0, 0.0, 0.0};
-#pragma unroll 8
-        for (int b = b0 + warp; b < b1; b += 8) {
-            const uint4 a = __ldg(wa + 4 * b), d = __ldg(wb + 4 * b), x = __ldg(xr + 4 * b);
-            float f[4]; // lane t's k indices: its 8 values of the block, whatever their order
-            mma_bf16_first(f, a.x, d.x, a.y, d.y, x.x, x.y);
-            mma_bf16(f, a.z, d.z, a.w, d.w, x.z, x.w);
+        float size[4] = {};
+#pragma unroll 1
+        for (int b = b0 + warp; b < b1; b += 8 * kRouteAhead) {
+            uint4 a[kRouteAhead], d[kRouteAhead], x[kRouteAhead];
 #pragma unroll
-            for (int j = 0; j < 4; ++j)
-                acc[j] += (double)f[j];
+            for (int i = 0; i < kRouteAhead; ++i)
+                if (b + 8 * i < b1) {
+                    a[i] = __ldg(wa + 4 * (b + 8 * i));
+                    d[i] = __ldg(wb + 4 * (b + 8 * i));
+                    x[i] = __ldg(xr + 4 * (b + 8 * i));
+                }
+#pragma unroll
+            for (int i = 0; i < kRouteAhead; ++i) {
+                if (b + 8 * i >= b1)
+                    break;
+                float f[4]; // lane t's k indices: its 8 values of the block, whatever their order
+                mma_bf16_first(f, a[i].x, d[i].x, a[i].y, d[i].y, x[i].x, x[i].y);
+                mma_bf16(f, a[i].z, d[i].z, a[i].w, d[i].w, x[i].z, x[i].w);
+                constexpr uint32_t kAbs = kAbs16x2;
+                mma_bf16(size, a[i].x & kAbs, d[i].x & kAbs, a[i].y & kAbs, d[i].y & kAbs,
+                         x[i].x & kAbs, x[i].y & kAbs);
+                mma_bf16(size, a[i].z & kAbs, d[i].z & kAbs, a[i].w & kAbs, d[i].w & kAbs,
+                         x[i].z & kAbs, x[i].w & kAbs);
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    acc[j] += (double)f[j];
+            }
         }
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
-            s_part[warp][(g + (j >> 1) * 8) * 8 + 2 * t + (j & 1)] = acc[j];
+        for (int j = 0; j < 4; ++j) {
+            const int at = (g + (j >> 1) * 8) * 8 + 2 * t + (j & 1);
+            s_part[warp][at] = acc[j];
+            s_size[warp][at] = size[j];
+        }
         __syncthreads();
         if (c < per)
             cluster_wait(); // (the first chunk) the other CTAs have started
         if (tid < 128) {
             const int e = c * 16 + (tid >> 3), j = tid & 7;
             double z = 0.0;
+            float size = 0.0f;
 #pragma unroll
-            for (int w = 0; w < 8; ++w)
+            for (int w = 0; w < 8; ++w) {
                 z += s_part[w][tid];
+                size += s_size[w][tid];
+            }
             if (e < p.E)
                 st_cluster_f64(mapa_shared(zaddr + 8u * (uint32_t)(slice * p.E + e), (uint32_t)j),
                                z);
+            size = fmaxf(size, __shfl_xor_sync(0xFFFFFFFFu, size, 8)); // of four experts; no NaN
+            size = fmaxf(size, __shfl_xor_sync(0xFFFFFFFFu, size, 16));
+            if (lane < 8)
+                max_cluster_u32(mapa_shared(maddr + 4u * (uint32_t)slice, (uint32_t)j),
+                                __float_as_uint(size));
         }
         __syncthreads();
     }
@@ -134,32 +254,46 @@ __global__ void __cluster_dims__(kRouteCluster, 1, 1) __launch_bounds__(kRouteTh
         return;
     if (tid < 32)
         s_sel[tid] = -1;
-    for (int e = tid; e < p.E; e += kRouteThreads) {
-        double z = s_z[e];
-        for (int q = 1; q < slices; ++q)
-            z += s_z[q * p.E + e];
-        if (p.bias)
-            z += (double)__ldg(p.bias + e);
-        s_z[e] = z == z ? z : -INFINITY; // a NaN logit is never chosen
+    int open_ = 0; // experts that may be chosen at all
+    for (int e0 = 0; e0 < p.E; e0 += kRouteThreads) {
+        const int e = e0 + tid;
+        double z = -INFINITY;
+        if (e < p.E) {
+            z = s_z[e];
+            for (int q = 1; q < slices; ++q)
+                z += s_z[q * p.E + e];
+            if (p.bias)
+                z += (double)__ldg(p.bias + e);
+            z = z == z ? z : -INFINITY; // a NaN logit is never chosen
+            s_z[e] = z;
+        }
+        open_ += __syncthreads_count(z > -INFINITY);
     }
-    __syncthreads();
-    // parts threads share an expert's count (E <= 64: 4, <= 128: 2)
+    float most = 0.0f; // (of the slices' largest: not below the largest sum)
+    for (int q = 0; q < slices; ++q)
+        most += __uint_as_float(s_most[q]);
+    const double tol = most < INFINITY ? (double)most * 0x1p-21 : 0.0; // (else fp32 holds no sums)
+    // An expert's place, if those within tol below it precede it: its own if there are none, a later one
+    // if there are. So the first place of a close call stays empty. parts threads share an expert's count
+    // (E <= 64: 4, <= 128: 2).
     const int parts = p.E <= 64 ? 4 : p.E <= 128 ? 2 : 1;
     const int part = tid % parts;
     for (int e0 = 0; e0 < p.E; e0 += kRouteThreads / parts) {
         const int e = e0 + tid / parts;
-        const double z = e < p.E ? s_z[e] : -INFINITY;
-        int n = 0;
-        for (int q = part; q < p.E; q += parts) {
-            const double o = s_z[q];
-            n += (o > z || (o == z && q < e)) ? 1 : 0;
-        }
+        const double lo = e < p.E ? s_z[e] - tol : -INFINITY;
+        int n = -1; // (itself)
+        for (int q = part; q < p.E; q += parts)
+            n += s_z[q] >= lo ? 1 : 0;
         for (int o = 1; o < parts; o <<= 1)
-            n += __shfl_xor_sync(0xFFFFFFFFu, n, o);
-        if (part == 0 && e < p.E && n < p.k && z > -INFINITY)
+            n += __shfl_xor_sync(0xFFFFFFFFu, n, o) + 1;
+        if (part == 0 && lo > -INFINITY && n < p.k)
             s_sel[n] = e;
     }
     __syncthreads();
+    if (__any_sync(0xFFFFFFFFu, lane < min(p.k, open_) && s_sel[lane] < 0)) {
+        __syncthreads(); // every warp has seen it
+        route_close(p, tk, tol, s_z, s_sel, s_list, &s_close, &s_part[0][0]);
+    }
     if (warp == 0) {
         const int e = lane < p.k ? s_sel[lane] : -1;
         const double top = s_sel[0] >= 0 ? s_z[s_sel[0]] : 0.0;
