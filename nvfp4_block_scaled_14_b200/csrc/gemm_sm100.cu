@@ -6,7 +6,7 @@
 // multiply in FP4 with weights and activations both in 4 bits). The same kernels take MXFP4
 // operands (template parameter F, fp4_format.cuh): one E8M0 scale per 32 values, two scale atoms a
 // k-tile instead of four, kind::mxf4 with scale_vec::2X, no global scale. M 4096, N 12288, K 4096
-// bf16 out: 87 us in a burst (4750 TFLOP/s), 100 us called without a pause under the power cap.
+// bf16 out: 86 us in a burst (4790 TFLOP/s), 100 us called without a pause under the power cap.
 //
 // Kernel structure (one CTA per SM, persistent over work units, 10 warps):
 //   warp 0      TMA producer: per 256-wide k-tile loads the A tile (128 rows x 128 B of packed

@@ -895,14 +895,14 @@ __device__ __forceinline__ void put_y(__nv_bfloat16 *y, const float4 &v)
 //                sums in shared memory, which go to y or, split by split, to the workspace.
 // A stage's bytes and scales complete one barrier, and the MMAs that have read them another.
 // Measured, with the router, ids and inputs new each call: 64 tokens, 64 MXFP4 experts of 2048 x 1024,
-// top 8: 65 us (214 MB of met weights: 3.3 TB/s); 16 tokens, 28 of 32 NVFP4 experts of 4096 x 1280, top
-// 4: 71 us; one token, 6 experts of 2048 x 1408: 26.5 us. Of the 64 tokens' 52 us from this kernel's
+// top 8: 63 us (214 MB of met weights: 3.4 TB/s); 16 tokens, 28 of 32 NVFP4 experts of 4096 x 1280, top
+// 4: 69 us; one token, 6 experts of 2048 x 1408: 25 us. Of the 64 tokens' 52 us from this kernel's
 // start to its end, gate/up take 22 to 25 (22 at the copy rate), down 13 to 14 (11), the rest are lists
 // (3), terms (2.5), three barriers with the wait for the slowest CTA (10) and the sums. Products are
 // bound by HBM and by the roles' latency
 // together: a k-tile's 16 KB take 700 cycles of an SM's share, and the MMA warp's step (a completed
 // wait is 95 cycles, four MMAs and a commit 300) leaves little of that; with the weights of eight
-// experts for all, which L2 holds, the whole call still takes 60 us, and separate rings for weights and
+// experts for all, which L2 holds, the whole call took 60 us where it took 65, and separate rings for weights and
 // terms, with a second wait and commit a step, took 77 where one took 67. So a role is a warp of its own
 // with few instructions a step, and in a group
 // of warps one polls while the others sleep at a named barrier. Waits are bounded. The first that gives
