@@ -1309,9 +1309,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     }
 }
 
-// Sum split-K partials in split order, scale by alpha, cast, store. Without swap a thread takes four
-// columns of a row (the partials' rows are padded to whole tiles): bound by reading them from L2.
-template <bool SWAP>
+// Sum split-K partials in split order, scale by alpha, cast, store. Without swap a thread takes VEC (1
+// or 4) columns of a row (the partials' rows are padded to whole tiles), flat over rows and columns, so
+// that narrow outputs fill the blocks too (8192 x 16, K 1024: 22.8 us for the call with a block a row,
+// 12.2 so). Four columns where there are more outputs than threads on the device, bound by reading the
+// partials from L2 (777 x 1001, K 2080: 13.3 us, 16.0 with one); one where each can have its own, bound by
+// a thread's loads one after the other (200 x 264, K 8192: 12.5 us, 16.2 with four). A split product has
+// at most half as many 128 x 256 tiles as SMs: 32 bits.
+template <bool SWAP, int VEC>
 __global__ void splitk_reduce_kernel(const float *__restrict__ partial, int splits,
                                      int64_t rows_a, int64_t rows_b, int64_t a_pad,
                                      int64_t b_pad, const float *__restrict__ a_gs,
@@ -1338,26 +1343,23 @@ __global__ void splitk_reduce_kernel(const float *__restrict__ partial, int spli
             put(b * ldy + a, acc);
         }
     } else {
-        // flat over (row, four columns), so that narrow outputs fill the blocks too (8192 x 16, K 1024:
-        // 22.7 us for the call with a block a row, 12.3 so). A split product has at most half as
-        // many 128 x 256 tiles as SMs: 32 bits.
-        const uint32_t quads = (uint32_t)((rows_b + 3) / 4), total = (uint32_t)rows_a * quads;
+        using Vec = typename std::conditional<VEC == 4, float4, float>::type;
+        const uint32_t groups = (uint32_t)((rows_b + VEC - 1) / VEC), total = (uint32_t)rows_a * groups;
         for (uint32_t i = blockIdx.x * blockDim.x + threadIdx.x; i < total;
              i += gridDim.x * blockDim.x) {
-            const int64_t a = i / quads, q = i % quads;
-            const float4 *src = reinterpret_cast<const float4 *>(partial + a * b_pad) + q;
-            float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-#pragma unroll 4
+            const int64_t a = i / groups, q = i % groups;
+            const Vec *src = reinterpret_cast<const Vec *>(partial + a * b_pad) + q;
+            float acc[VEC] = {};
             for (int s = 0; s < splits; ++s) {
-                const float4 v = src[(int64_t)s * a_pad * (b_pad >> 2)];
-                acc.x += v.x;
-                acc.y += v.y;
-                acc.z += v.z;
-                acc.w += v.w;
+                const Vec v = src[(int64_t)s * a_pad * (b_pad / VEC)];
+#pragma unroll
+                for (int j = 0; j < VEC; ++j)
+                    acc[j] += reinterpret_cast<const float *>(&v)[j];
             }
-            const float r[4] = {acc.x, acc.y, acc.z, acc.w};
-            for (int j = 0; j < 4 && 4 * q + j < rows_b; ++j)
-                put(a * ldy + 4 * q + j, r[j]);
+#pragma unroll
+            for (int j = 0; j < VEC; ++j)
+                if (VEC * q + j < rows_b)
+                    put(a * ldy + VEC * q + j, acc[j]);
         }
     }
 }
@@ -2485,13 +2487,15 @@ cudaError_t launch_linear_fmt(const LinearPlan &pl, const uint8_t *a_codes, cons
         return e;
     const float *part = reinterpret_cast<const float *>(ws);
     const int64_t a_pad = pl.tiles_a * 128, b_pad = pl.tiles_b * pl.bn;
-    const int64_t cap = (int64_t)num_sms() * 8;
-    const int64_t items = pl.swap_ab ? pl.rows_a * pl.rows_b : pl.rows_a * ((pl.rows_b + 3) / 4);
-    const int64_t want = (items + 255) / 256;
+    const int64_t cap = (int64_t)num_sms() * 8, outputs = pl.rows_a * pl.rows_b; // 8 x 256 threads an SM
+    const bool one = pl.swap_ab || outputs <= cap * 256;
+    const int64_t want = ((one ? outputs : pl.rows_a * ((pl.rows_b + 3) / 4)) + 255) / 256;
     const unsigned g = (unsigned)(want < cap ? want : cap);
-    return launch_pdl(pl.swap_ab ? splitk_reduce_kernel<true> : splitk_reduce_kernel<false>, dim3(g),
-                      256, 0, s, part, pl.splits, pl.rows_a, pl.rows_b, a_pad, b_pad, a_gs, w_gs, y, N,
-                      out_bf16);
+    return launch_pdl(pl.swap_ab ? splitk_reduce_kernel<true, 1>
+                      : one      ? splitk_reduce_kernel<false, 1>
+                                 : splitk_reduce_kernel<false, 4>,
+                      dim3(g), 256, 0, s, part, pl.splits, pl.rows_a, pl.rows_b, a_pad, b_pad, a_gs,
+                      w_gs, y, N, out_bf16);
 }
 
 } // namespace

@@ -18,7 +18,8 @@ def _cuda():
 
 
 SHAPES = [(4096, 8, 1024), (8192, 16, 1024), (3001, 30, 512), (130, 1, 2048), (1000, 3, 544),
-          (2050, 129, 1056), (400, 1998, 512)]
+          (2050, 129, 1056), (400, 1998, 512), (200, 264, 8192), (130, 30, 29984),
+          (777, 1001, 2080)]
 
 
 @pytest.mark.parametrize("M,N,K", SHAPES)
